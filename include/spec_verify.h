@@ -61,6 +61,7 @@ extern "C" {
 /* storage type of the logits */
 #define SV_F32 0   /* IEEE float32 */
 #define SV_BF16 1  /* bfloat16 (upper half of a float32) */
+#define SV_F16 2   /* IEEE float16: keys, values and queries of the paged operators only */
 
 /* status codes returned by the host entry points */
 #define SV_OK 0
@@ -83,6 +84,11 @@ extern "C" {
 #define SV_DEV_OUT_OF_BOUNDS 256u  /* checked build only (libspec_verify_checked.so, compiled with
                                       -DSV_CHECKED): an index failed its bounds test and the
                                       access was skipped */
+
+#define SV_DEV_BAD_PAGE 512u       /* paged operators: a page or slot outside the cache */
+#define SV_DEV_NO_PAGES 1024u      /* spec_paged_plan: the free stack could not serve a row */
+#define SV_DEV_TOKENS_CLIPPED 2048u /* spec_paged_plan: a row's tokens passed max_tokens */
+#define SV_DEV_TIMEOUT 4096u       /* spec_paged_attention: a wait inside the kernel ran out */
 
 #define SV_MAX_K 16
 #define SV_MAX_TREE_NODES 128
@@ -337,6 +343,147 @@ int spec_verify_and_plug(const void* target_logits, const void* draft_logits, in
                          float* logp_out, float* logq_out,
                          int32_t* tokens, int32_t* seq_len, int max_len, int32_t* last_token,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The target model's pass over a paged key/value cache.  Lengths live on the
+ * device (spec_verify_plug advances them there), so the three calls below
+ * read them there and the host never waits for them:
+ *
+ *   spec_paged_plan       block tables, slot map, positions and packed
+ *                         offsets of a step, from the request lengths;
+ *   spec_paged_append     the new tokens' keys and values go to their slots;
+ *   spec_paged_attention  the new tokens attend to the cache.
+ *
+ * A step of B requests packs their new tokens one request after the other:
+ * request b owns tokens cu_new[b] .. cu_new[b+1]-1 of every packed array.
+ * The cache is k_cache, v_cache [n_pages, Hk, page_size, D], dense; slot
+ * s = page * page_size + offset names one token's place.  page_size is a
+ * power of two in [8, 256]; n_pages * page_size < 2^31 (offsets into the
+ * cache are 64 bits wide).
+ *
+ * `flags` is one uint32 on the device, or NULL: SV_DEV_* bits are OR-ed into
+ * it and never cleared.  Arrays that a call writes must not overlap those
+ * that it reads, except where it says so.
+ */
+
+/* Rows of one spec_paged_plan call. */
+#define SV_MAX_PLAN_ROWS 8192
+
+/*
+ * Pages, slots and offsets of a step.  Row b has seq_len[b] tokens in the
+ * cache, brings num_new[b] more and holds page_count[b] pages, the first
+ * entries of block_table[b, :].  With want = ceil((seq_len + num_new) /
+ * page_size):
+ *   - pages past want go back to the free stack (a row with seq_len =
+ *     num_new = 0 gives back all it holds);
+ *   - missing pages are taken, rows in their order: first those given back
+ *     by this call, in the order of rows and entries, then the stack from
+ *     its top.  What is left of the former goes on the stack in reverse
+ *     order, so that taking pages and giving them back restores it.
+ *
+ *   seq_len, num_new, page_count  [B] int32, device.
+ *   block_table  [B, max_pages] int32, in/out: entries page_count ..
+ *                want-1 are written; entries past a row's count are stale.
+ *   free_pages   [n_pages] int32, in/out: the stack, free_count[0] entries;
+ *                the entry free_count[0]-1 is taken first.
+ *   free_count   [1] int32.
+ *   cu_new       [B+1] int32 out: exclusive sums of the rows' new tokens.
+ *   kv_len       [B] int32 out: seq_len + num_new; 0 for rows not served.
+ *   slot_map     [max_tokens] int32 out: slot of every new token; -1 past
+ *                cu_new[B] and for rows not served.
+ *   positions    [max_tokens] int32 out: seq_len + index of every new token
+ *                in its row; -1 past cu_new[B].
+ *   page_count_out [B], free_count_out [1]  int32 out; they may be
+ *                page_count and free_count themselves.
+ *
+ * Rows that are not served keep their pages: a row whose need the stack
+ * cannot meet after the rows before it (SV_DEV_NO_PAGES; its tokens stay in
+ * the packed order with slot -1), a row whose tokens would pass max_tokens
+ * (SV_DEV_TOKENS_CLIPPED, no tokens), and a row with a negative length, a
+ * page count outside [0, max_pages] or more than max_pages * page_size
+ * tokens (SV_DEV_BAD_LENGTH, no tokens).  A page outside [0, n_pages) gives
+ * slot -1 and SV_DEV_BAD_PAGE.
+ *
+ * One launch.  Returns SV_OK, SV_ERR_SHAPE (B outside [0, SV_MAX_PLAN_ROWS],
+ * max_pages < 1, max_tokens < 0, n_pages < 1, a page size that is none, or
+ * B * max_pages, max_pages * page_size or n_pages * page_size >= 2^31),
+ * SV_ERR_NULL, SV_ERR_ALIGN or SV_ERR_CUDA.  With B == 0 the arrays of B
+ * entries may be NULL.
+ */
+int spec_paged_plan(const int32_t* seq_len, const int32_t* num_new, const int32_t* page_count,
+                    int32_t* block_table, int32_t* free_pages, const int32_t* free_count, int B,
+                    int page_size, int max_pages, int n_pages, int max_tokens, int32_t* cu_new,
+                    int32_t* kv_len, int32_t* slot_map, int32_t* positions,
+                    int32_t* page_count_out, int32_t* free_count_out, uint32_t* flags,
+                    void* stream);
+
+/*
+ * k_cache[slot_map[t]] = k_new[t] and the same for v, for t in [0, T); a
+ * negative slot skips its token.  A slot past the cache is skipped and sets
+ * SV_DEV_BAD_PAGE.  Slots that are not -1 must differ from one another.
+ *
+ *   k_new, v_new  [T, Hk, D] of `dtype` (SV_BF16 or SV_F16); heads dense, tokens
+ *                 k_stride / v_stride elements apart (multiples of 8, at
+ *                 least Hk * D): slices of a fused projection's output do.
+ *   D             64 or 128.
+ *
+ * All data pointers 16-byte aligned.  Returns SV_OK, SV_ERR_DTYPE,
+ * SV_ERR_SHAPE, SV_ERR_NULL, SV_ERR_ALIGN or SV_ERR_CUDA.  T == 0 is a no-op.
+ */
+int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                      const int32_t* slot_map, int dtype, int T, int Hk, int D, int page_size,
+                      int n_pages, void* k_cache, void* v_cache, uint32_t* flags, void* stream);
+
+/*
+ * Attention of every request's new tokens over its cached keys and values,
+ * those of the new tokens (already appended) included.  Request b has n =
+ * cu_new[b+1] - cu_new[b] new tokens and L = kv_len[b] cached ones; its token
+ * i (0 <= i < n) sees the keys j <= L - n + i.  With query head h on key head
+ * h / (Hq / Hk):
+ *
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j]) v[j]
+ *   lse[t, h] = log sum_j exp(scale * q[t, h] . k[j])
+ *
+ * A token that sees no key (L - n + i < 0, or L == 0) gets out = 0 and lse =
+ * -inf, and so do the tokens from cu_new[B] to T.  Sums and softmax
+ * statistics are float32; the probabilities are rounded to `dtype` once,
+ * before their product with v.  Scores must be finite (no NaN or infinity
+ * in q or in the keys and values that a request has); what a page holds past
+ * kv_len is never looked at.  Results do not depend on timing.
+ *
+ *   q            [T, Hq, D] of `dtype` (SV_BF16 or SV_F16); heads dense, tokens
+ *                q_stride elements apart (a multiple of 8, at least Hq * D).
+ *   block_table  [B, max_pages] int32; only a row's first
+ *                ceil(kv_len / page_size) entries are read.  An entry
+ *                outside [0, n_pages) reads as zeros, SV_DEV_BAD_PAGE.
+ *   cu_new       [B+1] int32, kv_len [B] int32.  A row whose offsets
+ *                decrease or leave [0, T] is skipped, a length outside [0,
+ *                max_pages * page_size] is clamped; SV_DEV_BAD_LENGTH.
+ *   D            64 or 128; Hq a multiple of Hk, Hq / Hk <= 128.
+ *   scale        > 0, finite.
+ *   out          [T, Hq, D] of `dtype`, dense.
+ *   lse          [T, Hq] float32, dense, or NULL.
+ *   workspace    device scratch, 16-byte aligned, of at least
+ *                spec_paged_attention_workspace_bytes(D) bytes, for this
+ *                call's use alone.  Its first SV_ATTENTION_COUNTER_BYTES
+ *                must be zero before its first call (one cudaMemsetAsync);
+ *                every call leaves them zero again, except one that set
+ *                SV_DEV_TIMEOUT.
+ *
+ * One launch.  Returns SV_OK, SV_ERR_DTYPE, SV_ERR_SHAPE, SV_ERR_NULL,
+ * SV_ERR_ALIGN, SV_ERR_WORKSPACE or SV_ERR_CUDA.  T == 0 is a no-op; with
+ * B == 0 the arrays of B entries may be NULL.
+ */
+#define SV_ATTENTION_COUNTER_BYTES 4096
+
+size_t spec_paged_attention_workspace_bytes(int D);
+
+int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                         int dtype, const int32_t* block_table, const int32_t* cu_new,
+                         const int32_t* kv_len, int B, int T, int Hq, int Hk, int D, int page_size,
+                         int max_pages, int n_pages, float scale, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, uint32_t* flags, void* stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char* spec_verify_status_string(int status);

@@ -15,6 +15,7 @@ LIB_CHECKED_PATH = os.path.join(PKG, "libspec_verify_checked.so")
 
 SV_F32 = 0
 SV_BF16 = 1
+SV_F16 = 2   # the paged operators only
 
 SV_OK = 0
 SV_ERR_NULL = 1
@@ -34,13 +35,21 @@ SV_DEV_BAD_LENGTH = 32
 SV_DEV_BAD_TREE = 64
 SV_DEV_OUT_OF_BOUNDS = 256
 
+SV_DEV_BAD_PAGE = 512
+SV_DEV_NO_PAGES = 1024
+SV_DEV_TOKENS_CLIPPED = 2048
+SV_DEV_TIMEOUT = 4096
+
 SV_MAX_K = 16
 SV_MAX_TREE_NODES = 128
 SV_STATIC_SCRATCH_BYTES = 8 << 20
+SV_MAX_PLAN_ROWS = 8192
+SV_ATTENTION_COUNTER_BYTES = 4096
 
 # every function of include/spec_verify.h: (restype, argtypes)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 _SIG = {
     "spec_verify_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "spec_verify_max_vocab": (_I, [_I]),
@@ -58,6 +67,12 @@ _SIG = {
     "spec_verify_status_string": (ctypes.c_char_p, [_I]),
     "spec_verify_row_stats": (_I, [_P, _P, _I, _P, _P, _I, _I, _I, _P, ctypes.c_size_t, _P]),
     "spec_verify_static_device_errors": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
+    "spec_paged_plan": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P,
+                             _P]),
+    "spec_paged_append": (_I, [_P, _L, _P, _L, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "spec_paged_attention_workspace_bytes": (ctypes.c_size_t, [_I]),
+    "spec_paged_attention": (_I, [_P, _L, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                  ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P, _P]),
 }
 
 _lib = None
@@ -183,6 +198,41 @@ def spec_verify_static_raw(target_ptr, draft_ptr, dtype, tokens_ptr, uniforms_pt
     return int(load().spec_verify_static(target_ptr, draft_ptr, dtype, tokens_ptr, uniforms_ptr,
                                          temperature_ptr, B, K, V, accepted_ptr, out_tokens_ptr,
                                          logp_ptr, logq_ptr, stream_handle))
+
+
+def spec_paged_plan_raw(seq_len_ptr, num_new_ptr, page_count_ptr, block_table_ptr, free_pages_ptr,
+                        free_count_ptr, B, page_size, max_pages, n_pages, max_tokens, cu_new_ptr,
+                        kv_len_ptr, slot_map_ptr, positions_ptr, page_count_out_ptr,
+                        free_count_out_ptr, flags_ptr, stream_handle) -> int:
+    """Pages, slots and packed offsets of a step from the request lengths."""
+    return load().spec_paged_plan(
+        seq_len_ptr, num_new_ptr, page_count_ptr, block_table_ptr, free_pages_ptr, free_count_ptr,
+        B, page_size, max_pages, n_pages, max_tokens, cu_new_ptr, kv_len_ptr, slot_map_ptr,
+        positions_ptr, page_count_out_ptr, free_count_out_ptr, flags_ptr, stream_handle)
+
+
+def spec_paged_append_raw(k_new_ptr, k_stride, v_new_ptr, v_stride, slot_map_ptr, dtype, T, Hk, D,
+                          page_size, n_pages, k_cache_ptr, v_cache_ptr, flags_ptr,
+                          stream_handle) -> int:
+    """New keys and values to their slots of the paged cache."""
+    return load().spec_paged_append(
+        k_new_ptr, k_stride, v_new_ptr, v_stride, slot_map_ptr, dtype, T, Hk, D, page_size, n_pages,
+        k_cache_ptr, v_cache_ptr, flags_ptr, stream_handle)
+
+
+def spec_paged_attention_workspace_bytes(D: int) -> int:
+    return int(load().spec_paged_attention_workspace_bytes(D))
+
+
+def spec_paged_attention_raw(q_ptr, q_stride, k_cache_ptr, v_cache_ptr, dtype, block_table_ptr,
+                             cu_new_ptr, kv_len_ptr, B, T, Hq, Hk, D, page_size, max_pages, n_pages,
+                             scale, out_ptr, lse_ptr, workspace_ptr, workspace_bytes, flags_ptr,
+                             stream_handle) -> int:
+    """Attention of the new tokens over the paged cache."""
+    return load().spec_paged_attention(
+        q_ptr, q_stride, k_cache_ptr, v_cache_ptr, dtype, block_table_ptr, cu_new_ptr, kv_len_ptr,
+        B, T, Hq, Hk, D, page_size, max_pages, n_pages, scale, out_ptr, lse_ptr, workspace_ptr,
+        workspace_bytes, flags_ptr, stream_handle)
 
 
 def spec_verify_device_errors(workspace_ptr, stream_handle) -> int:

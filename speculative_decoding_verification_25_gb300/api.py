@@ -7,6 +7,11 @@ streams; the verify step itself runs in the library's kernels.
 ``target`` [B, K+1, V] and ``draft`` [B, K, V] are CUDA tensors of
 torch.bfloat16 or torch.float32; ``draft_tokens`` [B, K] int32;
 ``uniforms`` [B, K+1] float32; ``temperature`` [B] float32 (0 = greedy).
+
+``paged_plan``, ``paged_append`` and ``paged_attention`` are the target
+model's pass over a paged key/value cache, with the request lengths on the
+device: a step plans its pages and slots, and every layer appends the new
+tokens' keys and values and attends.
 """
 from __future__ import annotations
 
@@ -18,7 +23,9 @@ from . import _native as N
 from . import _native as _N
 
 _DTYPES = {torch.bfloat16: N.SV_BF16, torch.float32: N.SV_F32}
+_CACHE_DTYPES = {torch.bfloat16: N.SV_BF16, torch.float16: N.SV_F16}
 _workspaces: dict = {}
+_attention_workspaces: dict = {}
 
 
 class VerifyResult(NamedTuple):
@@ -244,3 +251,190 @@ def verify_tree(target: torch.Tensor, node_tokens: torch.Tensor, parents: torch.
     if status != _N.SV_OK:
         raise _N.SpecVerifyError(status, "spec_verify_tree")
     return res
+
+
+class PagedPlan(NamedTuple):
+    cu_new: torch.Tensor       # [B+1] int32: exclusive sums of the new tokens
+    kv_len: torch.Tensor       # [B] int32: cached tokens once the new ones are, 0 = not served
+    slot_map: torch.Tensor     # [max_tokens] int32: place of every new token, -1 = none
+    positions: torch.Tensor    # [max_tokens] int32: position of every new token, -1 = none
+    page_count: torch.Tensor   # [B] int32: pages held now
+    free_count: torch.Tensor   # [1] int32: pages on the stack now
+
+
+def _flags_ptr(flags, dev):
+    if flags is None:
+        return None
+    _check(flags, "flags", dtype=torch.int32, shape=(1,), device=dev)
+    return flags.data_ptr()
+
+
+def paged_plan(seq_len: torch.Tensor, num_new: torch.Tensor, page_count: torch.Tensor,
+               block_table: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor, *,
+               page_size: int, max_tokens: int, out: Optional[PagedPlan] = None,
+               flags: Optional[torch.Tensor] = None,
+               stream: Optional[torch.cuda.Stream] = None) -> PagedPlan:
+    """Pages, slots, positions and packed offsets of a step (spec_paged_plan).
+
+    Row b has ``seq_len[b]`` cached tokens and brings ``num_new[b]``; it holds
+    ``page_count[b]`` pages, the first entries of ``block_table`` [B,
+    max_pages].  Pages it no longer needs go to the stack ``free_pages``
+    (``free_count`` [1] entries), missing ones come from it; both arrays are
+    updated in place.  The counts come back in the result, whose tensors may
+    be ``page_count`` and ``free_count`` themselves (pass them in ``out``).
+    All tensors are int32; ``flags`` (one int32) collects SV_DEV_* bits."""
+    B = seq_len.shape[0] if seq_len.dim() else 0
+    dev = seq_len.device
+    _check(seq_len, "seq_len", dtype=torch.int32, shape=(B,))
+    _check(num_new, "num_new", dtype=torch.int32, shape=(B,), device=dev)
+    _check(page_count, "page_count", dtype=torch.int32, shape=(B,), device=dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    max_pages = block_table.shape[1]
+    _check(block_table, "block_table", dtype=torch.int32, shape=(B, max_pages), device=dev)
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [n_pages]")
+    _check(free_pages, "free_pages", dtype=torch.int32, device=dev)
+    _check(free_count, "free_count", dtype=torch.int32, shape=(1,), device=dev)
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    if out is None:
+        if max_tokens < 0:
+            raise ValueError("max_tokens must not be negative")
+        with torch.cuda.stream(st):   # outputs belong to the stream that writes them
+            out = PagedPlan(*(torch.empty(n, dtype=torch.int32, device=dev)
+                              for n in (B + 1, B, max_tokens, max_tokens, B, 1)))
+    else:
+        for name, n in zip(PagedPlan._fields, (B + 1, B, max_tokens, max_tokens, B, 1)):
+            _check(getattr(out, name), "out." + name, dtype=torch.int32, shape=(n,), device=dev)
+    status = N.spec_paged_plan_raw(
+        seq_len.data_ptr(), num_new.data_ptr(), page_count.data_ptr(), block_table.data_ptr(),
+        free_pages.data_ptr(), free_count.data_ptr(), B, page_size, max_pages, free_pages.shape[0],
+        max_tokens, out.cu_new.data_ptr(), out.kv_len.data_ptr(), out.slot_map.data_ptr(),
+        out.positions.data_ptr(), out.page_count.data_ptr(), out.free_count.data_ptr(),
+        _flags_ptr(flags, dev), st.cuda_stream)
+    if status != N.SV_OK:
+        raise N.SpecVerifyError(status, "spec_paged_plan")
+    return out
+
+
+def _check_cache(k_cache, v_cache):
+    """(dtype code, n_pages, Hk, page_size, D) of a paged cache."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [n_pages, Hk, page_size, D]")
+    if k_cache.dtype not in _CACHE_DTYPES:
+        raise TypeError(f"k_cache dtype {k_cache.dtype} is not bfloat16 or float16")
+    _check(k_cache, "k_cache")
+    _check(v_cache, "v_cache", dtype=k_cache.dtype, shape=k_cache.shape, device=k_cache.device)
+    return (_CACHE_DTYPES[k_cache.dtype], *k_cache.shape)
+
+
+def _check_packed(t, name, dtype, shape, dev):
+    """A packed [T, heads, D] tensor whose heads are dense; its token stride."""
+    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.numel() == 0:
+        return shape[1] * shape[2]
+    stride_t, stride_h, stride_d = t.stride()
+    if shape[0] == 1:
+        stride_t = max(stride_t, shape[1] * shape[2])
+    if stride_d != 1 or (stride_h != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name} must have dense heads (strides [any, {shape[2]}, 1])")
+    return stride_t
+
+
+def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor,
+                 k_cache: torch.Tensor, v_cache: torch.Tensor, *,
+                 flags: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Write the new tokens' keys and values [T, Hk, D] (dense heads, any
+    token stride) to the slots ``slot_map`` [T] of the paged cache [n_pages,
+    Hk, page_size, D]; a negative slot skips its token (spec_paged_append)."""
+    dt, n_pages, Hk, page_size, D = _check_cache(k_cache, v_cache)
+    dev = k_cache.device
+    if slot_map.dim() != 1:
+        raise ValueError("slot_map must be [T]")
+    T = slot_map.shape[0]
+    _check(slot_map, "slot_map", dtype=torch.int32, device=dev)
+    k_stride = _check_packed(k_new, "k_new", k_cache.dtype, (T, Hk, D), dev)
+    v_stride = _check_packed(v_new, "v_new", k_cache.dtype, (T, Hk, D), dev)
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    status = N.spec_paged_append_raw(
+        k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, slot_map.data_ptr(), dt, T, Hk, D,
+        page_size, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), _flags_ptr(flags, dev),
+        st.cuda_stream)
+    if status != N.SV_OK:
+        raise N.SpecVerifyError(status, "spec_paged_append")
+
+
+class AttentionResult(NamedTuple):
+    out: torch.Tensor                      # [T, Hq, D]
+    lse: Optional[torch.Tensor] = None     # [T, Hq] float32: log of the softmax's sum
+
+
+def attention_workspace(D: int, device: torch.device,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The cached workspace of ``paged_attention`` on a (device, stream), its
+    counters zeroed once; calls on different streams must not share one."""
+    need = N.spec_paged_attention_workspace_bytes(D)
+    if need == 0:
+        raise ValueError(f"invalid head dimension {D}")
+    index = device.index if device.index is not None else torch.cuda.current_device()
+    st = stream if stream is not None else torch.cuda.current_stream(index)
+    key = (index, st.cuda_stream)
+    ws = _attention_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        with torch.cuda.stream(st):   # allocated and zeroed on the stream that uses it
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            ws[:N.SV_ATTENTION_COUNTER_BYTES].zero_()
+        _attention_workspaces[key] = ws
+    return ws
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, cu_new: torch.Tensor, kv_len: torch.Tensor, *,
+                    scale: Optional[float] = None, want_lse: bool = False,
+                    out: Optional[AttentionResult] = None, flags: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> AttentionResult:
+    """Causal attention of the packed new tokens ``q`` [T, Hq, D] (dense heads,
+    any token stride) over the paged cache [n_pages, Hk, page_size, D]
+    (spec_paged_attention).  Request b has tokens cu_new[b]..cu_new[b+1]-1,
+    the last of its ``kv_len[b]`` cached ones; a token that sees no key gets
+    zeros.  ``scale`` defaults to D ** -0.5."""
+    dt, n_pages, Hk, page_size, D = _check_cache(k_cache, v_cache)
+    dev = k_cache.device
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
+    T, Hq, _ = q.shape
+    q_stride = _check_packed(q, "q", k_cache.dtype, (T, Hq, D), dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    _check(block_table, "block_table", dtype=torch.int32, device=dev)
+    _check(cu_new, "cu_new", dtype=torch.int32, shape=(B + 1,), device=dev)
+    _check(kv_len, "kv_len", dtype=torch.int32, shape=(B,), device=dev)
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    if out is None:
+        with torch.cuda.stream(st):   # outputs belong to the stream that writes them
+            out = AttentionResult(
+                torch.empty(T, Hq, D, dtype=q.dtype, device=dev),
+                torch.empty(T, Hq, dtype=torch.float32, device=dev) if want_lse else None)
+    else:
+        _check(out.out, "out.out", dtype=q.dtype, shape=(T, Hq, D), device=dev)
+        if out.lse is not None:
+            _check(out.lse, "out.lse", dtype=torch.float32, shape=(T, Hq), device=dev)
+    if workspace is None:
+        workspace = attention_workspace(D, dev, st)
+    status = N.spec_paged_attention_raw(
+        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, block_table.data_ptr(),
+        cu_new.data_ptr(), kv_len.data_ptr(), B, T, Hq, Hk, D, page_size, max_pages, n_pages,
+        D ** -0.5 if scale is None else scale, out.out.data_ptr(),
+        out.lse.data_ptr() if out.lse is not None else None, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _flags_ptr(flags, dev), st.cuda_stream)
+    if status != N.SV_OK:
+        raise N.SpecVerifyError(status, "spec_paged_attention")
+    return out

@@ -21,10 +21,14 @@
 
 #include "spec_verify.h"
 #include "sv_draw.cuh"
+#include "sv_host.h"
 #include "sv_plug.cuh"
 #include "sv_tree.cuh"
 
 namespace {
+
+using sv::aligned_to;
+using sv::launch_early;
 
 constexpr size_t kHeaderBytes = 256;   // device flag word at offset 0
 constexpr int kMaxDevices = 64;
@@ -113,8 +117,6 @@ DeviceCache* device_cache(int dev) {
   return &dc;
 }
 
-bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Workspace of the verify calls, in 256-byte aligned regions after the
@@ -182,29 +184,6 @@ int validate(const void* target_logits, const void* draft_logits, int dtype,
 bool vector_path(const void* target_logits, const void* draft_logits, int V, int dtype) {
   return aligned_to(target_logits, 16) && aligned_to(draft_logits, 16) &&
          ((size_t)V * (size_t)elt_of(dtype)) % 16 == 0;
-}
-
-// A plain launch that may start while the preceding kernel on the stream
-// drains (programmatic dependent launch).  Only for kernels that call
-// wait_for_preceding_grid() before their first memory access; without the
-// attribute (refused) it falls back to plain stream order.
-cudaError_t launch_early(const void* fn, dim3 grid, dim3 block, void** args, cudaStream_t st) {
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    e = cudaLaunchKernel(fn, grid, block, args, 0, st);
-  }
-  return e;
 }
 
 // Where the fused plug step writes (tokens == nullptr: no plug).

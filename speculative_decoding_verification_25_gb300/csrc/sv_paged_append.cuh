@@ -1,0 +1,75 @@
+// New keys and values to their slots of the paged cache: a copy, bound by
+// HBM (4 * D * 2 bytes per token and head).  A thread moves 16-byte pieces,
+// kAppendPieces of K and of V in flight, with plain integer steps from one
+// piece to the next: `step` pieces further on is `step_tokens` tokens and
+// `step_pieces` pieces further.
+#pragma once
+
+#include "sv_paged.cuh"
+
+namespace sv {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendPieces = 4;
+
+struct AppendArgs {
+  const char* k_new;   // token pitch in bytes
+  const char* v_new;
+  long long k_pitch, v_pitch;
+  const int32_t* slot_map;
+  int T, Hk, page_shift;
+  int head_shift;       // log2 of 16-byte pieces per head
+  int pieces;           // Hk << head_shift: pieces per token
+  int step_tokens, step_pieces;
+  long long n_slots;
+  char* k_cache;
+  char* v_cache;
+  unsigned* flags;
+};
+
+__global__ void __launch_bounds__(kAppendThreads) sv_paged_append_kernel(AppendArgs a) {
+  wait_for_preceding_grid();
+  allow_dependent_launch();
+  const long long i = (long long)blockIdx.x * kAppendThreads + threadIdx.x;
+  long long t = i / a.pieces;
+  int c = (int)(i - t * a.pieces);
+  bool bad = false;
+  while (t < a.T) {
+    uint32_t k[kAppendPieces][4], v[kAppendPieces][4];
+    long long to[kAppendPieces];
+#pragma unroll
+    for (int u = 0; u < kAppendPieces; ++u) {
+      to[u] = -1;
+      if (t < a.T) {
+        const int slot = a.slot_map[t];
+        if (slot >= 0) {
+          if (slot < a.n_slots) {
+            const int h = c >> a.head_shift, d = c & ((1 << a.head_shift) - 1);
+            const long long page = slot >> a.page_shift;
+            const int off = slot & ((1 << a.page_shift) - 1);
+            to[u] = ((((page * a.Hk + h) << a.page_shift) + off) << a.head_shift) + d;
+            ldg_stream16(a.k_new + t * a.k_pitch + (long long)c * 16, k[u]);
+            ldg_stream16(a.v_new + t * a.v_pitch + (long long)c * 16, v[u]);
+          } else {
+            bad = true;
+          }
+        }
+      }
+      t += a.step_tokens;
+      c += a.step_pieces;
+      if (c >= a.pieces) {
+        c -= a.pieces;
+        ++t;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendPieces; ++u) {
+      if (to[u] < 0) continue;
+      *(uint4*)(a.k_cache + to[u] * 16) = make_uint4(k[u][0], k[u][1], k[u][2], k[u][3]);
+      *(uint4*)(a.v_cache + to[u] * 16) = make_uint4(v[u][0], v[u][1], v[u][2], v[u][3]);
+    }
+  }
+  if (bad) set_flag(a.flags, kDevBadPage);
+}
+
+}  // namespace sv
