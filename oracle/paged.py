@@ -84,7 +84,7 @@ class Attention(NamedTuple):
     lse_tol: np.ndarray
 
 
-UNIT = {"bf16": (2.0 ** -9, 2.0 ** -134), "f16": (2.0 ** -11, 2.0 ** -25)}   # rounding: relative, absolute
+UNIT = {"bf16": (2.0 ** -8, 2.0 ** -134), "f16": (2.0 ** -11, 2.0 ** -25)}   # rounding to 8 and 11 significant bits: relative, absolute
 
 
 def attention_tolerance(dtype, D, x_abs, p, v, o, lse):

@@ -80,3 +80,23 @@ def test_page_size_does_not_matter():
     pages = paged.attention(q, *(x.reshape(4, 2, 1, 4).transpose(0, 2, 1, 3) for x in kv), np.array([[0, 1, 2, 3]]),
                             [0, 3], [7], 1.0, "bf16")
     np.testing.assert_allclose(whole.out, pages.out, rtol=1e-13)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_bounds_admit_one_rounding_of_probabilities_and_results(dtype):
+    """Exact arithmetic that rounds the probabilities once and the result once
+    stays inside the bounds, on few keys, where nothing averages out."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float16
+    rounded = lambda x: torch.from_numpy(x).to(dt).double().numpy()
+    rng = np.random.default_rng(7)
+    worst = 0.0
+    for L in (1, 2, 3, 5, 8):
+        for _ in range(60):
+            q, k, v = (rounded(rng.normal(size=s)) for s in ((1, 4, 64), (1, 1, L, 64), (1, 1, L, 64)))
+            r = paged.attention(q, k, v, np.array([[0]]), [0, 1], [L], 0.125, dtype)
+            x = q[0] @ k[0, 0].T * 0.125
+            w = np.exp(x - x.max(-1, keepdims=True))
+            o = rounded(rounded(w) @ v[0, 0] / w.sum(-1, keepdims=True))
+            worst = max(worst, float((np.abs(o - r.out[0]) / r.out_tol[0]).max()))
+    assert 0.4 < worst <= 1, worst
