@@ -1,6 +1,7 @@
 // Host side of the paged cache operators declared in include/spec_verify.h:
 // argument checks, launch geometry and the C entry points.  Each is one
 // launch on the caller's stream.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -20,14 +21,38 @@ using sv::launch_early;
 constexpr int kMaxDevices = 64;
 constexpr int kMaxCluster = 8;   // portable cluster size
 
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
 struct PagedDevice {
   std::once_flag once;
   int sm_count = 0;
+  EncodeTiled encode = nullptr;   // the driver's tensor map encoder
   cudaError_t error = cudaSuccess;
 };
 PagedDevice g_paged[kMaxDevices];
 
-// SM count and the kernels' shared memory limits; once per device.
+// The attention kernel's variants.
+struct AttentionVariant {
+  const void* fn;
+  int threads, smem_bytes, ctas_per_sm, keys;
+};
+template <typename E, int kD, bool kWide>
+AttentionVariant variant() {
+  using S = sv::AttnShape<kD, kWide>;
+  return {(const void*)sv::sv_paged_attention_kernel<E, kD, kWide>, S::kThreads, S::kSmemBytes,
+          S::kCtasPerSm, S::kKeys};
+}
+AttentionVariant attention_variant(int dtype, int D, bool wide) {
+  if (dtype == SV_BF16) {
+    if (D == 128) return wide ? variant<__nv_bfloat16, 128, true>() : variant<__nv_bfloat16, 128, false>();
+    return wide ? variant<__nv_bfloat16, 64, true>() : variant<__nv_bfloat16, 64, false>();
+  }
+  if (D == 128) return wide ? variant<__half, 128, true>() : variant<__half, 128, false>();
+  return wide ? variant<__half, 64, true>() : variant<__half, 64, false>();
+}
+
+// SM count, the kernels' shared memory limits and the tensor map encoder;
+// once per device.
 PagedDevice* paged_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
@@ -38,6 +63,18 @@ PagedDevice* paged_device() {
       d.error = cudaFuncSetAttribute((const void*)sv::sv_paged_plan_kernel,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      SV_MAX_PLAN_ROWS * sv::kPlanRowBytes);
+    for (int i = 0; i < 8 && d.error == cudaSuccess; ++i) {
+      const AttentionVariant v = attention_variant(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, i & 4);
+      d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
+    }
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+    if (d.error == cudaSuccess)
+      d.error = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                 cudaEnableDefault, &found);
+    if (d.error == cudaSuccess && found != cudaDriverEntryPointSuccess)
+      d.error = cudaErrorSymbolNotFound;
+    d.encode = (EncodeTiled)fn;
   });
   return d.error == cudaSuccess ? &d : nullptr;
 }
@@ -53,10 +90,15 @@ constexpr long long k2_31 = 1ll << 31;
 
 int done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
-template <typename E>
-const void* attention_fn(int D) {
-  return D == 128 ? (const void*)sv::sv_paged_attention_kernel<E, 128>
-                  : (const void*)sv::sv_paged_attention_kernel<E, 64>;
+// A map of 16-bit elements for boxes of 64 columns (128 bytes, swizzled) by
+// box1 (by box2): dims and boxes innermost first, pitches in bytes.
+bool encode_map(const PagedDevice& d, CUtensorMap* map, int dtype, const void* base, int rank,
+                const cuuint64_t* dims, const cuuint64_t* pitches, const cuuint32_t* box) {
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return d.encode(map, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  (cuuint32_t)rank, const_cast<void*>(base), dims, pitches, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -161,7 +203,8 @@ int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, in
 
 size_t spec_paged_attention_workspace_bytes(int D) {
   if (D != 64 && D != 128) return 0;
-  return SV_ATTENTION_COUNTER_BYTES;
+  return SV_ATTENTION_COUNTER_BYTES +
+         (size_t)sv::kAttnMaxCtas * 2 * sv::kAttnRowsPerSlot * (D + 2) * sizeof(float);
 }
 
 int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -173,7 +216,7 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   const int shift = page_shift_of(page_size);
   if (shift < 0 || B < 0 || T < 0 || Hk < 1 || Hq < Hk || Hq % Hk || Hq / Hk > 128 || Hq > 4096 ||
       (D != 64 && D != 128) || max_pages < 1 || n_pages < 1 ||
-      (long long)max_pages * page_size >= k2_31 || (long long)n_pages * page_size >= k2_31 ||
+      (long long)max_pages * page_size >= k2_31 || (long long)n_pages * page_size * Hk >= k2_31 ||
       q_stride < (int64_t)Hq * D || !(scale > 0.f && scale <= 3.4e38f))
     return SV_ERR_SHAPE;
   if (T == 0) return SV_OK;
@@ -186,11 +229,20 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
       !aligned_to(lse, 4) || !aligned_to(flags, 4))
     return SV_ERR_ALIGN;
   if (workspace_bytes < spec_paged_attention_workspace_bytes(D)) return SV_ERR_WORKSPACE;
+  PagedDevice* dev = paged_device();
+  if (!dev) return SV_ERR_CUDA;
+  const int G = Hq / Hk;
+  // The narrow form holds 128 query rows (the G heads of a request's tokens
+  // on one key head) and streams the cache with two CTAs per SM; the wide
+  // form holds 256 and keeps the tensor core busier.  The host knows the
+  // mean of the rows alone; both forms take requests of any length.
+  const bool wide = (long long)T * G > 128ll * (B > 0 ? B : 1);
+  const AttentionVariant v = attention_variant(dtype, D, wide);
+  int ctas = dev->sm_count * v.ctas_per_sm;
+  const int most = sv::kAttnMaxCtas * v.ctas_per_sm / 2;
+  if (ctas > most) ctas = most;
+
   sv::AttnArgs a;
-  a.q = (const char*)q;
-  a.q_pitch = (long long)q_stride * 2;
-  a.k_cache = (const char*)k_cache;
-  a.v_cache = (const char*)v_cache;
   a.block_table = block_table;
   a.cu_new = cu_new;
   a.kv_len = kv_len;
@@ -198,19 +250,31 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   a.T = T;
   a.Hq = Hq;
   a.Hk = Hk;
+  a.G = G;
   a.page_shift = shift;
   a.max_pages = max_pages;
   a.n_pages = n_pages;
-  a.scale = scale;
+  a.tile_tokens = 128 / G;
+  a.scale_log2 = scale * sv::kLog2e;
   a.out = (char*)out;
   a.lse = lse;
+  a.tickets = (int*)workspace;
+  a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
   a.flags = flags;
-  const long long warps = (long long)T * Hq;
-  void* args[] = {&a};
-  return done(launch_early(
-      dtype == SV_BF16 ? attention_fn<__nv_bfloat16>(D) : attention_fn<__half>(D),
-      dim3((unsigned)((warps * 32 + sv::kAttnThreads - 1) / sv::kAttnThreads)),
-      dim3(sv::kAttnThreads), args, (cudaStream_t)stream));
+  CUtensorMap q_map, k_map, v_map;
+  const cuuint64_t q_dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+  const cuuint64_t q_pitches[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)a.tile_tokens};
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)n_pages * Hk * page_size};
+  const cuuint64_t pitches[1] = {(cuuint64_t)D * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)(page_size < v.keys ? page_size : v.keys)};
+  if (!encode_map(*dev, &q_map, dtype, q, 3, q_dims, q_pitches, q_box) ||
+      !encode_map(*dev, &k_map, dtype, k_cache, 2, dims, pitches, box) ||
+      !encode_map(*dev, &v_map, dtype, v_cache, 2, dims, pitches, box))
+    return SV_ERR_CUDA;
+  void* args[] = {&a, &q_map, &k_map, &v_map};
+  return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args,
+                           (cudaStream_t)stream, (size_t)v.smem_bytes));
 }
 
 }  // extern "C"

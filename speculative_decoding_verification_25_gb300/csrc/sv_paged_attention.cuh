@@ -1,145 +1,747 @@
 // Attention of each request's new tokens over its paged keys and values.
 //
-// With s_j = scale * log2(e) * q.k_j the softmax is a running pair (m, l) and
-// a running sum o: for keys taken in any order, m' = max(m, s_j),
-// l' = l 2^(m-m') + 2^(s_j-m'), o' = o 2^(m-m') + 2^(s_j-m') v_j, and the
-// result is o / l.
+// With s_j = scale * log2(e) * q.k_j and any reference r, the result is
+// sum_j 2^(s_j - r) v_j / sum_j 2^(s_j - r).  Keys are taken a tile at a time;
+// r follows the running maximum only when that has risen by more than
+// kSlack, so a tile seldom has to scale what was summed before it, and the
+// probabilities stay below 2^kSlack.
 //
-// One warp per (token, query head): a lane scores one key of 32, then the
-// lanes share out the head's dimensions for the product with the values.
+// Both products run on the tensor core (tcgen05).  A query tile is 128 rows:
+// the G query heads of one key head for 128 / G consecutive tokens, since
+// they share every key and value.  S = Q K^T goes to tensor memory; four
+// warps take it a row per thread, leave P = 2^(S - r), rounded to the
+// operands' type, in the place of S, and O += P V reads P from there.  Rows
+// never meet: no shuffle, and unused rows may hold anything.
+//
+// A CTA is one loader warp (TMA into a ring of key and value tiles), one
+// warp that issues the products, and four softmax warps per query tile.
+// Two forms:
+//   wide    two query tiles of one unit against tiles of 128 keys: while one
+//           tile's softmax runs, the tensor core works on the other's;
+//   narrow  one query tile against tiles of 64 keys, two S buffers, and two
+//           CTAs per SM: for up to 128 rows per request, where the time is
+//           that of reading the cache.
+//
+// The work is all (request, key head, query unit, key tile) quadruples in
+// that order, cut into equal ranges, one per CTA: every CTA sums the rows'
+// tiles to find its range, so no length is needed on the host.  A unit that
+// a range's end cuts leaves unnormalised sums in the workspace; the CTA that
+// takes the unit's last ticket joins them, always in the order of the CTAs,
+// so results do not depend on timing and no CTA waits for another.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "sv_paged.cuh"
+#include "sv_tensor.cuh"
 
 namespace sv {
 
-constexpr int kAttnThreads = 256;
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
+constexpr float kSlack = 8.f;        // in log2: probabilities up to 256, exact in both types' range
+constexpr int kAttnMaxCtas = 320;    // resident CTAs that the workspace has room for (narrow)
+constexpr int kAttnRowsPerSlot = 128;
 
 struct AttnArgs {
-  const char* q;            // token pitch in bytes
-  long long q_pitch;
-  const char* k_cache;
-  const char* v_cache;
   const int32_t* block_table;   // [B, max_pages]
   const int32_t* cu_new;        // [B+1]
   const int32_t* kv_len;        // [B]
-  int B, T, Hq, Hk, page_shift, max_pages, n_pages;
-  float scale;
+  int B, T, Hq, Hk, G, page_shift, max_pages, n_pages;
+  int tile_tokens;              // 128 / G
+  float scale_log2;
   char* out;
-  float* lse;               // or nullptr
+  float* lse;                   // or nullptr
+  int* tickets;                 // one per CTA, zero between calls
+  float* partial;               // [CTA][2][rows][D], then [CTA][2][rows][2]
   unsigned* flags;
 };
 
-__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+template <int kD, bool kWide>
+struct AttnShape {
+  static constexpr int kTiles = kWide ? 2 : 1;
+  static constexpr int kKeys = kWide ? 128 : 64;
+  static constexpr int kBufs = kWide ? 1 : 2;        // S buffers per query tile
+  static constexpr int kBlocks = kD / 64;            // 128-byte column blocks of a row
+  static constexpr int kQBytes = 128 * kD * 2;
+  static constexpr int kStageBytes = kKeys * kD * 2;
+  static constexpr int kStages = kD == 128 ? 5 : 8;  // what is left of the shared memory
+  static constexpr int kSoftThreads = 128 * kTiles;
+  static constexpr int kThreads = kSoftThreads + 64;
+  static constexpr int kCtasPerSm = kWide ? 1 : 2;
+  static constexpr int kTmemCols = kWide ? 512 : 256;
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kControlBytes = 512;
+  static constexpr int kSmemBytes = kTiles * kQBytes + kStages * kStageBytes + kControlBytes;
+};
+
+struct AttnControl {   // at the end of the shared memory
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty, drain, met;
+  uint64_t s_full[2][2], p_ready[2][2];
+  uint64_t pv_done[2];
+  uint32_t tmem;
+  int abort_word;
+  int last;
+  int start_row;
+  long long start_off, total;
+  long long sums[10];
+};
+
+static_assert(sizeof(AttnControl) <= 512, "fits kControlBytes");
+
+// A request's lengths, clamped to what its arrays hold; n == 0: nothing to do.
+struct AttnRow {
+  int begin, n, L;
+};
+__device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, int b, bool* bad = nullptr) {
+  const int begin = a.cu_new[b], end = a.cu_new[b + 1];
+  const int most = a.max_pages << a.page_shift;
+  const int len = a.kv_len[b];
+  AttnRow r;
+  r.begin = begin;
+  const bool sound = begin >= 0 && end >= begin && end <= a.T;
+  r.n = sound ? end - begin : 0;
+  r.L = min(max(len, 0), most);
+  if (bad && (!sound || r.L != len)) *bad = true;
+  return r;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
-  return __half22float2(*(const __half2*)&w);
+// Key tiles that tokens up to t1 of a request see.
+template <int kKeys>
+__device__ __forceinline__ int tiles_seen(const AttnRow& r, int t1) {
+  return (max(0, r.L - r.n + t1) + kKeys - 1) / kKeys;
+}
+// Weight of query unit m: its key tiles, one for a unit that sees no key.
+template <typename S>
+__device__ __forceinline__ int unit_tiles(const AttnArgs& a, const AttnRow& r, int m) {
+  const int tokens = S::kTiles * a.tile_tokens;
+  return max(1, tiles_seen<S::kKeys>(r, min(r.n, (m + 1) * tokens)));
+}
+template <typename S>
+__device__ __forceinline__ int units_of(const AttnArgs& a, const AttnRow& r) {
+  const int tokens = S::kTiles * a.tile_tokens;
+  return (r.n + tokens - 1) / tokens;
 }
 
-template <typename E, int D>
-__global__ void __launch_bounds__(kAttnThreads) sv_paged_attention_kernel(AttnArgs a) {
-  wait_for_preceding_grid();
-  allow_dependent_launch();
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < a.B; b += kAttnThreads)
-      if (a.cu_new[b] < 0 || a.cu_new[b + 1] < a.cu_new[b] || a.cu_new[b + 1] > a.T ||
-          a.kv_len[b] < 0 || a.kv_len[b] > (long long)a.max_pages << a.page_shift)
-        set_flag(a.flags, kDevLength);
-  const long long task = ((long long)blockIdx.x * kAttnThreads + threadIdx.x) >> 5;
-  const int t = (int)(task / a.Hq), h = (int)(task % a.Hq);
-  if (t >= a.T) return;
-  // the token's row: the first whose end passes t
-  int lo = 0, hi = a.B;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu_new[mid + 1] > t) hi = mid;
-    else lo = mid + 1;
-  }
-  int visible = 0;
-  if (lo < a.B) {
-    const int begin = a.cu_new[lo], end = a.cu_new[lo + 1];
-    const long long most = (long long)a.max_pages << a.page_shift;
-    long long L = a.kv_len[lo];
-    L = min(max(L, 0ll), most);
-    if (begin < 0 || begin > t || end > a.T) return;
-    visible = (int)max(0ll, L - (end - begin) + (t - begin) + 1);
-  }
-  const int hk = h / (a.Hq / a.Hk);
-  const uint4* q = (const uint4*)(a.q + t * a.q_pitch + (long long)h * D * 2);
-  float qf[D];
+// A CTA's walk over its range of the work; every warp keeps its own.
+template <typename S>
+struct AttnWalk {
+  const AttnArgs& a;
+  AttnRow row;
+  int b, h, m, n_units;
+  int j0, j1;                 // key tiles of the unit that are this CTA's
+  int tiles;                  // all key tiles of the unit
+  long long w, w_end, unit_begin;
+
+  __device__ __forceinline__ AttnWalk(const AttnArgs& args, int start_row, long long off,
+                                      long long w0, long long w1)
+      : a(args), b(start_row), w(w0), w_end(w1) {
+    row = attn_row(a, b);
+    n_units = units_of<S>(a, row);
+    long long head = 0;       // weight of one head's units
+    const int lane = threadIdx.x & 31;
+    for (int i = lane; i < n_units; i += 32) head += unit_tiles<S>(a, row, i);
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
-    const uint4 w = q[i];
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack2(ws[j], E());
-      qf[8 * i + 2 * j] = f.x;
-      qf[8 * i + 2 * j + 1] = f.y;
+    for (int o = 16; o > 0; o >>= 1) head += __shfl_xor_sync(0xffffffffu, head, o);
+    h = (int)(off / head);
+    off -= h * head;
+    m = 0;
+    tiles = unit_tiles<S>(a, row, 0);
+    while (off >= tiles) {
+      off -= tiles;
+      tiles = unit_tiles<S>(a, row, ++m);
     }
+    j0 = (int)off;
+    unit_begin = w - off;
+    clip();
   }
-  constexpr int W = D / 32;   // dimensions per lane
-  float o[W] = {}, m = SV_NEG_INF, l = 0.f;
-  for (int j0 = 0; j0 < visible; j0 += 32) {
-    const int j = j0 + lane;
-    long long at = -1;
-    float s = SV_NEG_INF;
-    if (j < visible) {
-      const int id = a.block_table[(long long)lo * a.max_pages + (j >> a.page_shift)];
-      s = 0.f;
-      if (id >= 0 && id < a.n_pages) {
-        at = ((((long long)id * a.Hk + hk) << a.page_shift) + (j & ((1 << a.page_shift) - 1))) * D;
-        const uint4* k = (const uint4*)(a.k_cache + at * 2);
+  __device__ __forceinline__ void clip() {
+    j1 = (int)min((long long)tiles, j0 + (w_end - w));
+  }
+  // The next unit; false at the end of the range.
+  __device__ __forceinline__ bool next() {
+    w += j1 - j0;
+    if (w >= w_end) return false;
+    if (++m == n_units) {
+      m = 0;
+      if (++h == a.Hk) {
+        h = 0;
+        next_row();
+      }
+    }
+    tiles = unit_tiles<S>(a, row, m);
+    j0 = 0;
+    unit_begin = w;
+    clip();
+    return true;
+  }
+  // The next request with tokens (there is one: the range has not ended).
+  __device__ __forceinline__ void next_row() {
+    const int lane = threadIdx.x & 31;
+    for (++b; b < a.B; b += 32) {
+      const int mine = b + lane;
+      const unsigned some = __ballot_sync(0xffffffffu, mine < a.B && attn_row(a, mine).n > 0);
+      if (some) {
+        b += __ffs(some) - 1;
+        break;
+      }
+    }
+    row = attn_row(a, b);
+    n_units = units_of<S>(a, row);
+  }
+  // Query tile t of the unit: its tokens [first, last) within the request,
+  // and how many of the unit's key tiles it needs of this CTA.
+  __device__ __forceinline__ int first(int t) const { return (m * S::kTiles + t) * a.tile_tokens; }
+  __device__ __forceinline__ int last(int t) const { return min(row.n, first(t) + a.tile_tokens); }
+  __device__ __forceinline__ int count(int t) const {
+    if (first(t) >= row.n) return 0;
+    return max(0, min(j1, tiles_seen<S::kKeys>(row, last(t))) - j0);
+  }
+  __device__ __forceinline__ int most() const {
+    int c = count(0);
+    if (S::kTiles > 1) c = max(c, count(1));
+    return c;
+  }
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// ------------------------------------------------------------------- loader
+// One warp.  A key or value tile is kKeys rows of one head, a box of
+// min(page, kKeys) rows per page and 128-byte column block; each lane brings
+// one box.  Rows of pages past the request's length stay as they are.
+template <typename S>
+__device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
+                                          uint32_t q_smem, uint32_t ring, const CUtensorMap* q_map,
+                                          const CUtensorMap* k_map, const CUtensorMap* v_map) {
+  const int lane = threadIdx.x & 31;
+  const int page = 1 << a.page_shift;
+  const int box = min(page, S::kKeys);
+  const int boxes = S::kKeys / box;              // pages of a tile
+  const int my_page = lane / S::kBlocks, my_block = lane % S::kBlocks;
+  int it = 0, units = 0;
+  bool ok = true, bad = false;
+
+  auto tile = [&](const CUtensorMap* map, int j) -> bool {
+    const int stage = it % S::kStages, lap = it / S::kStages;
+    if (lap > 0 && !mbar_wait(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word))
+      return false;
+    const uint32_t bar = smem_addr(&c->full[stage]);
+    const int key = j * S::kKeys + my_page * box;
+    const bool mine = my_page < boxes && key < u.row.L;
+    int y = 0;
+    if (mine) {
+      const int id = a.block_table[(long long)u.b * a.max_pages + (key >> a.page_shift)];
+      const bool inside = id >= 0 && id < a.n_pages;
+      bad |= !inside;
+      // past the last row of the cache the box fills with zeros
+      y = ((inside ? id * a.Hk + u.h : a.n_pages * a.Hk) << a.page_shift) + (key & (page - 1));
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) mbar_arrive_expect(bar, __popc(who) * box * 128);
+    __syncwarp();
+    if (mine)
+      tma_load_2d(ring + stage * S::kStageBytes + (my_block * S::kKeys + my_page * box) * 128, map,
+                  my_block * 64, y, bar);
+    ++it;
+    return true;
+  };
+
+  do {
+    const int n = u.most();
+    if (n == 0) continue;
+    if (units > 0 && !(ok = mbar_wait(smem_addr(&c->q_empty), (units - 1) & 1, &c->abort_word)))
+      break;
+    ++units;
+    const uint32_t bar = smem_addr(&c->q_full);
+    const int q_tile = lane / S::kBlocks;
+    const bool mine = q_tile < S::kTiles && u.count(q_tile) > 0;
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) mbar_arrive_expect(bar, __popc(who) * a.tile_tokens * a.G * 128);
+    __syncwarp();
+    if (mine)
+      tma_load_3d(q_smem + q_tile * S::kQBytes + my_block * 128 * 128, q_map, my_block * 64,
+                  u.h * a.G, u.row.begin + u.first(q_tile), bar);
+    for (int i = 0; ok && i < min(n, S::kBufs); ++i) ok = tile(k_map, u.j0 + i);
+    for (int i = 0; ok && i < n; ++i) {
+      ok = tile(v_map, u.j0 + i);
+      if (ok && i + S::kBufs < n) ok = tile(k_map, u.j0 + i + S::kBufs);
+    }
+  } while (ok && u.next());
+  if (bad) set_flag(a.flags, kDevBadPage);
+  if (!ok) {   // given up: the copies in flight still land in this CTA's memory
+    for (int i = max(0, it - S::kStages); i < it; ++i)
+      (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, nullptr);
+    if (units > 0) (void)mbar_poll(smem_addr(&c->q_full), (units - 1) & 1, nullptr);
+  }
+}
+
+// ----------------------------------------------------------------- products
+// One warp; lane 0 issues.  Columns of tensor memory: kBufs S buffers per
+// query tile, then one O per query tile.
+template <typename E, int kD, typename S>
+__device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
+                                              uint32_t q_smem, uint32_t ring, char* ring_ptr,
+                                              uint32_t tmem) {
+  constexpr bool kBf16 = sizeof(E) == 2 && std::is_same<E, __nv_bfloat16>::value;
+  constexpr uint32_t s_desc = mma_desc(kBf16, 128, S::kKeys, false);
+  constexpr uint32_t o_desc = mma_desc(kBf16, 128, kD, true);
+  const int lane = threadIdx.x & 31;
+  int it = 0, units = 0;
+  int done[2] = {0, 0};   // tiles of S issued before this unit, per query tile
+  bool ok = true;
+
+  auto s_col = [&](int t, int k) { return tmem + (t * S::kBufs + k % S::kBufs) * S::kKeys; };
+  auto wait_stage = [&](int i) {
+    return mbar_wait(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->abort_word);
+  };
+  auto scores = [&](int t, int k, int stage) {   // S(t) = Q(t) K^T, the k-th of query tile t
+    if (lane == 0) {
+      const uint32_t q0 = q_smem + t * S::kQBytes, k0 = ring + stage * S::kStageBytes;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 w = k[i];
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      for (int d = 0; d < kD / 16; ++d)
+        mma_smem(s_col(t, k), tile_desc(q0 + (d / 4) * 128 * 128 + (d % 4) * 32, 16, 1024),
+                 tile_desc(k0 + (d / 4) * S::kKeys * 128 + (d % 4) * 32, 16, 1024), s_desc, d > 0);
+      tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]));
+    }
+  };
+  auto release = [&](uint64_t* bar) {
+    if (lane == 0) tc_commit(smem_addr(bar));
+  };
+
+  do {
+    const int n = u.most();
+    if (n == 0) continue;
+    int cnt[2] = {u.count(0), S::kTiles > 1 ? u.count(1) : 0};
+    if (!(ok = mbar_wait(smem_addr(&c->q_full), units & 1, &c->abort_word))) break;
+    ++units;
+    tc_fence_after();
+    for (int i = 0; i < min(n, S::kBufs); ++i) {
+      if (!(ok = wait_stage(it))) break;
+      tc_fence_after();
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = unpack2(ws[e], E());
-            s = fmaf(qf[8 * i + 2 * e], f.x, s);
-            s = fmaf(qf[8 * i + 2 * e + 1], f.y, s);
+      for (int t = 0; t < S::kTiles; ++t)
+        if (i < cnt[t]) scores(t, done[t] + i, it % S::kStages);
+      release(&c->empty[it % S::kStages]);
+      ++it;
+    }
+    if (ok && n <= S::kBufs) release(&c->q_empty);
+    for (int i = 0; ok && i < n; ++i) {
+      const int v_it = it++;
+      const bool more = i + S::kBufs < n;
+      const int next_it = more ? it++ : 0;
+      if (!(ok = wait_stage(v_it))) break;
+      // values past the request's length must not reach the sums: 0 * NaN is NaN
+      const int valid = u.row.L - (u.j0 + i) * S::kKeys;
+      if (valid < S::kKeys) {
+        char* v0 = ring_ptr + (v_it % S::kStages) * S::kStageBytes;
+        const int chunks = (S::kKeys - valid) * 8;
+        for (int x = lane; x < chunks * S::kBlocks; x += 32)
+          *(uint4*)(v0 + ((x / chunks) * S::kKeys + valid) * 128 + (x % chunks) * 16) =
+              make_uint4(0, 0, 0, 0);
+        fence_async_shared();
+        __syncwarp();
+      }
+      bool k_here = false;
+#pragma unroll
+      for (int t = 0; t < S::kTiles; ++t) {
+        if (!ok || i >= cnt[t]) continue;
+        const int k = done[t] + i;
+        if (!(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
+                             &c->abort_word)))
+          break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
+          const uint32_t v0 = ring + (v_it % S::kStages) * S::kStageBytes;
+#pragma unroll
+          for (int x = 0; x < S::kKeys / 16; ++x)
+            mma_tmem(o, s_col(t, k) + x * 8, tile_desc(v0 + x * 16 * 128, S::kKeys * 128, 1024),
+                     o_desc, i > 0 || x > 0);
+          tc_commit(smem_addr(&c->pv_done[t]));
+        }
+        if (i + S::kBufs < cnt[t]) {
+          if (!k_here) {
+            if (!(ok = wait_stage(next_it))) break;
+            tc_fence_after();
+            k_here = true;
+          }
+          scores(t, k + S::kBufs, next_it % S::kStages);
+        }
+      }
+      if (!ok) break;
+      release(&c->empty[v_it % S::kStages]);
+      if (more) {
+        release(&c->empty[next_it % S::kStages]);
+        if (i + S::kBufs + 1 == n) release(&c->q_empty);
+      }
+    }
+    done[0] += cnt[0];
+    done[1] += cnt[1];
+  } while (ok && u.next());
+  // everything issued is done before the CTA's memory goes
+  release(&c->drain);
+  (void)mbar_poll(smem_addr(&c->drain), 0, nullptr);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax
+// All softmax warps meet (their `phase`-th meeting); false if it was given up.
+__device__ __forceinline__ bool soft_meet(AttnControl* c, int phase) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&c->met));
+  return mbar_wait(smem_addr(&c->met), phase & 1, &c->abort_word);
+}
+
+template <typename E>
+__device__ __forceinline__ void store_row32(char* to, const float (&o)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *(uint4*)(to + i * 16) =
+        make_uint4(pack2(o[8 * i], o[8 * i + 1], E()), pack2(o[8 * i + 2], o[8 * i + 3], E()),
+                   pack2(o[8 * i + 4], o[8 * i + 5], E()), pack2(o[8 * i + 6], o[8 * i + 7], E()));
+}
+
+// Joins the partial sums of the unit's CTAs, a row per warp, its columns over
+// the lanes.
+template <typename E, int kD, typename S>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& u, int c_first,
+                                          int parts, bool begins_late) {
+  constexpr int W = kD / 32;
+  const int lane = threadIdx.x & 31;
+  const size_t slots = (size_t)gridDim.x * 2;
+  const float* sums = a.partial;
+  const float2* stats = (const float2*)(a.partial + slots * S::kRows * kD);
+  for (int r = threadIdx.x >> 5; r < S::kRows; r += S::kSoftThreads / 32) {
+    const int t = r / 128, at = r % 128;
+    const int token = u.first(t) + at / a.G;
+    if (at >= a.tile_tokens * a.G || token >= u.row.n) continue;
+    float top = SV_NEG_INF;
+    for (int p = lane; p < parts; p += 32) {
+      const size_t slot = (size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0);
+      top = fmaxf(top, __ldcg(&stats[slot * S::kRows + r]).x);
+    }
+    top = warp_max(top);
+    float o[W] = {}, l = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      const int p = p0 + lane;
+      float weight = 0.f, mine = 0.f;
+      if (p < parts) {
+        const size_t slot = (size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0);
+        const float2 ml = __ldcg(&stats[slot * S::kRows + r]);
+        weight = ml.x == SV_NEG_INF ? 0.f : ex2_approx(ml.x - top);
+        mine = ml.y * weight;
+      }
+      l += warp_sum(mine);
+      const int here = min(32, parts - p0);
+#pragma unroll 4
+      for (int i = 0; i < here; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, weight, i);
+        const size_t slot = (size_t)(c_first + p0 + i) * 2 + (p0 + i == 0 && begins_late ? 1 : 0);
+        const float* from = sums + (slot * S::kRows + r) * kD + lane * W;
+        float x[W];
+        if constexpr (W == 4) {
+          const float4 f = __ldcg((const float4*)from);
+          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+        } else {
+          const float2 f = __ldcg((const float2*)from);
+          x[0] = f.x, x[1] = f.y;
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) o[w] += wi > 0.f ? wi * x[w] : 0.f;
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const long long to = (long long)(u.row.begin + token) * a.Hq + u.h * a.G + at % a.G;
+    uint32_t packed[W / 2];
+#pragma unroll
+    for (int w = 0; w < W / 2; ++w) packed[w] = pack2(o[2 * w] * inv, o[2 * w + 1] * inv, E());
+    char* dst = a.out + (to * kD + lane * W) * 2;
+    if constexpr (W == 4) *(uint2*)dst = make_uint2(packed[0], packed[1]);
+    else *(uint32_t*)dst = packed[0];
+    if (a.lse && lane == 0) a.lse[to] = l > 0.f ? (top + log2f(l)) * kLn2 : SV_NEG_INF;
+  }
+}
+
+template <typename E, int kD, typename S>
+__device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
+                                             uint32_t tmem, long long quota) {
+  const int warp = threadIdx.x >> 5, t = warp / 4;
+  const int r = threadIdx.x % 128;                 // the thread's row of its query tile
+  const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
+  const uint32_t o_col = tmem + lanes + S::kTiles * S::kBufs * S::kKeys + t * kD;
+  int done = 0;                                    // tiles of S taken before this unit
+  int meetings = 0;
+  bool ok = true;
+  do {
+    const int n = u.count(t);
+    const int token = u.first(t) + r / a.G;
+    const bool mine = r < a.tile_tokens * a.G && token < u.row.n;
+    const bool any = __any_sync(0xffffffffu, mine);
+    // keys that the row sees; rows without a token see none
+    const int seen = mine ? max(0, u.row.L - u.row.n + token + 1) : 0;
+    // the warp's first row sees the fewest of those with a token
+    const int fewest = __shfl_sync(0xffffffffu, seen, 0);
+    float m = SV_NEG_INF, l = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const int k = done + i, buf = k % S::kBufs;
+      if (!(ok = mbar_wait(smem_addr(&c->s_full[t][buf]), (k / S::kBufs) & 1, &c->abort_word)))
+        break;
+      tc_fence_after();
+      if (any) {
+        const uint32_t s_col = tmem + lanes + (t * S::kBufs + buf) * S::kKeys;
+        uint32_t bits[S::kKeys];
+#pragma unroll
+        for (int x = 0; x < S::kKeys; x += 32) tmem_load32(s_col + x, bits + x);
+        tmem_wait_load();
+        tmem_pin<S::kKeys>(bits);
+        const int base = (u.j0 + i) * S::kKeys;
+        if (base + S::kKeys > fewest) {
+          const int left = seen - base;
+#pragma unroll
+          for (int x = 0; x < S::kKeys; ++x)
+            if (x >= left) bits[x] = 0xff800000u;
+        }
+        float top[4] = {SV_NEG_INF, SV_NEG_INF, SV_NEG_INF, SV_NEG_INF};
+#pragma unroll
+        for (int x = 0; x < S::kKeys; ++x) top[x % 4] = fmaxf(top[x % 4], __uint_as_float(bits[x]));
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        const bool raise = mine && (i == 0 ? high > m : high > m + kSlack);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? (m == SV_NEG_INF ? 0.f : ex2_approx(m - high)) : 1.f;
+          if (raise) m = high;
+          l *= f;
+          if (i > 0) {   // what was summed before, once the products are done
+            if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int x = 0; x < kD; x += 32) {
+              uint32_t o[32];
+              tmem_load32(o_col + x, o);
+              tmem_wait_load();
+              tmem_pin<32>(o);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_store32(o_col + x, o);
+            }
           }
         }
-        s *= a.scale * kLog2e;
-      } else {
-        set_flag(a.flags, kDevBadPage);
-      }
-    }
-    const float mn = fmaxf(m, warp_max(s));
-    const float p = exp2f(s - mn);
-    const float c = exp2f(m - mn);
-    l = l * c + warp_sum(p);
-    m = mn;
+        const float ref = m == SV_NEG_INF ? 0.f : m;
+        float sum[4] = {};
 #pragma unroll
-    for (int w = 0; w < W; ++w) o[w] *= c;
-    const int n = min(32, visible - j0);
-    for (int i = 0; i < n; ++i) {
-      const long long vat = __shfl_sync(0xffffffffu, at, i);
-      const float pi = __shfl_sync(0xffffffffu, p, i);
-      if (vat < 0) continue;
-      const uint32_t* v = (const uint32_t*)(a.v_cache + vat * 2) + lane * (W / 2);
+        for (int x = 0; x < S::kKeys; x += 32) {
+          uint32_t p[16];
 #pragma unroll
-      for (int w = 0; w < W / 2; ++w) {
-        const float2 f = unpack2(v[w], E());
-        o[2 * w] = fmaf(pi, f.x, o[2 * w]);
-        o[2 * w + 1] = fmaf(pi, f.y, o[2 * w + 1]);
+          for (int y = 0; y < 32; y += 2) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(bits[x + y]), a.scale_log2, -ref));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(bits[x + y + 1]), a.scale_log2, -ref));
+            sum[(y / 2) % 4] += p0 + p1;
+            p[y / 2] = pack2(p0, p1, E());
+          }
+          tmem_store16(s_col + x / 2, p);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_wait_store();
       }
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&c->p_ready[t][buf]));
     }
+    if (!ok) break;
+    done += n;
+    // The last scores came with the products kBufs tiles before done; a wait
+    // sees a phase's parity alone, so those after them are waited for one by one.
+    for (int k = done - min(n, S::kBufs); ok && k < done; ++k)
+      ok = mbar_wait(smem_addr(&c->pv_done[t]), k & 1, &c->abort_word);
+    if (!ok) break;
+    tc_fence_after();
+    const bool whole = u.j0 == 0 && u.j1 == u.tiles;
+    if (whole) {
+      if (any) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const long long to = (long long)(u.row.begin + token) * a.Hq + u.h * a.G + r % a.G;
+#pragma unroll
+        for (int x = 0; x < kD; x += 32) {
+          uint32_t bits[32] = {};
+          if (n > 0) {
+            tmem_load32(o_col + x, bits);
+            tmem_wait_load();
+            tmem_pin<32>(bits);
+          }
+          float o[32];
+#pragma unroll
+          for (int y = 0; y < 32; ++y) o[y] = l > 0.f ? __uint_as_float(bits[y]) * inv : 0.f;
+          if (mine) store_row32<E>(a.out + (to * kD + x) * 2, o);
+        }
+        if (mine && a.lse) a.lse[to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
+      }
+      tc_fence_before();
+      continue;
+    }
+    // a part of the unit: unnormalised sums to the workspace
+    const int c_first = (int)(u.unit_begin / quota);
+    const int c_last = (int)((u.unit_begin + u.tiles - 1) / quota);
+    const bool begins_late = u.unit_begin != (long long)c_first * quota;
+    const size_t slots = (size_t)gridDim.x * 2;
+    const size_t slot = (size_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first && begins_late ? 1 : 0);
+    if (any) {
+      float* to = a.partial + (slot * S::kRows + t * 128 + r) * kD;
+#pragma unroll
+      for (int x = 0; x < kD; x += 32) {
+        uint32_t bits[32] = {};
+        if (n > 0) {
+          tmem_load32(o_col + x, bits);
+          tmem_wait_load();
+          tmem_pin<32>(bits);
+        }
+        if (mine)
+#pragma unroll
+          for (int y = 0; y < 32; y += 4)
+            *(uint4*)(to + x + y) = make_uint4(bits[y], bits[y + 1], bits[y + 2], bits[y + 3]);
+      }
+      if (mine)
+        ((float2*)(a.partial + slots * S::kRows * kD))[slot * S::kRows + t * 128 + r] =
+            make_float2(m, l);
+    }
+    tc_fence_before();
+    __threadfence();
+    if (!(ok = soft_meet(c, meetings++))) break;
+    if (threadIdx.x == 0) {
+      const int before = atomicAdd(&a.tickets[c_first], 1);
+      const bool last = before == c_last - c_first;
+      if (last) a.tickets[c_first] = 0;
+      __threadfence();
+      c->last = last;
+    }
+    if (!(ok = soft_meet(c, meetings++))) break;
+    if (c->last) attn_join<E, kD, S>(a, u, c_first, c_last - c_first + 1, begins_late);
+  } while (u.next());
+}
+
+template <typename E, int kD, bool kWide>
+__global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, kWide>::kCtasPerSm)
+    sv_paged_attention_kernel(const __grid_constant__ AttnArgs a,
+                              const __grid_constant__ CUtensorMap q_map,
+                              const __grid_constant__ CUtensorMap k_map,
+                              const __grid_constant__ CUtensorMap v_map) {
+  using S = AttnShape<kD, kWide>;
+  extern __shared__ __align__(1024) char smem[];
+  char* ring_ptr = smem + S::kTiles * S::kQBytes;
+  AttnControl* c = (AttnControl*)(ring_ptr + S::kStages * S::kStageBytes);
+  const uint32_t q_smem = smem_addr(smem), ring = smem_addr(ring_ptr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kLoader = S::kSoftThreads / 32, kIssuer = kLoader + 1;
+
+  // -------- set-up that reads nothing of the caller's
+  if (warp == kLoader && lane == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(smem_addr(&c->full[i]), 1);
+      mbar_init(smem_addr(&c->empty[i]), 1);
+    }
+    mbar_init(smem_addr(&c->q_full), 1);
+    mbar_init(smem_addr(&c->q_empty), 1);
+    mbar_init(smem_addr(&c->drain), 1);
+    mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
+    for (int t = 0; t < S::kTiles; ++t) {
+      for (int k = 0; k < S::kBufs; ++k) {
+        mbar_init(smem_addr(&c->s_full[t][k]), 1);
+        mbar_init(smem_addr(&c->p_ready[t][k]), 4);
+      }
+      mbar_init(smem_addr(&c->pv_done[t]), 1);
+    }
+    mbar_init_fence();
+    c->abort_word = 0;
+    c->start_row = -1;
+    tma_prefetch_map(&q_map);
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  E* out = (E*)a.out + ((long long)t * a.Hq + h) * D + lane * W;
+  if (warp == kIssuer) tmem_alloc<S::kTmemCols>(smem_addr(&c->tmem));
+  wait_for_preceding_grid();
+  allow_dependent_launch();
+
+  // -------- weights of all requests, summed: thread i has rows [r0, r1)
+  const int per = (a.B + S::kThreads - 1) / S::kThreads;
+  const int r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
+  auto weight = [&](int b, bool* bad) -> long long {
+    const AttnRow row = attn_row(a, b, bad);
+    const int units = units_of<S>(a, row);
+    long long sum = 0;
+    for (int m = 0; m < units; ++m) sum += unit_tiles<S>(a, row, m);
+    return sum * a.Hk;
+  };
+  bool bad = false;
+  long long mine = 0;
+  for (int b = r0; b < r1; ++b) mine += weight(b, &bad);
+  if (bad && blockIdx.x == 0) set_flag(a.flags, kDevLength);
+  long long inc = mine;
 #pragma unroll
-  for (int w = 0; w < W; ++w) out[w] = E(o[w] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(long long)t * a.Hq + h] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) c->sums[warp] = inc;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < S::kThreads / 32; ++w) {
+    if (w < warp) before += c->sums[w];
+    total += c->sums[w];
+  }
+  const long long quota = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+  const long long w0 = blockIdx.x * quota, w1 = min(total, w0 + quota);
+  long long begin = before + inc - mine;
+  if (w0 < w1 && begin <= w0 && w0 < begin + mine) {   // one thread: the range starts in its rows
+    int b = r0;
+    for (;; ++b) {
+      const long long wb = weight(b, nullptr);
+      if (w0 < begin + wb) break;
+      begin += wb;
+    }
+    c->start_row = b;
+    c->start_off = w0 - begin;
+  }
+  __syncthreads();
+  const uint32_t tmem = c->tmem;
+
+  if (w0 < w1) {
+    const AttnWalk<S> u(a, c->start_row, c->start_off, w0, w1);
+    if (warp == kLoader) attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map);
+    else if (warp == kIssuer) attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem);
+    else attn_softmax<E, kD, S>(a, u, c, tmem, quota);
+  }
+  // tokens past the last request's
+  const int used = min(max(a.cu_new[a.B], 0), a.T);
+  const long long spare = (long long)(a.T - used) * a.Hq;
+  if (spare > 0) {
+    const long long first = (long long)used * a.Hq;
+    for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < spare * (kD / 8);
+         x += (long long)gridDim.x * blockDim.x)
+      ((uint4*)a.out)[first * (kD / 8) + x] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < spare;
+           x += (long long)gridDim.x * blockDim.x)
+        a.lse[first + x] = SV_NEG_INF;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0 && c->abort_word) set_flag(a.flags, kDevTimeout);
+  if (warp == kIssuer) tmem_free<S::kTmemCols>(tmem);
 }
 
 }  // namespace sv
