@@ -69,8 +69,10 @@ struct AttnShape {
   static constexpr int kQBytes = 128 * kD * 2;
   static constexpr int kStageBytes = kKeys * kD * 2;
   static constexpr int kStages = kD == 128 ? 5 : 8;  // what is left of the shared memory
+  static constexpr int kParts = kWide ? 2 : 1;       // P is handed over in this many pieces
   static constexpr int kSoftThreads = 128 * kTiles;
-  static constexpr int kThreads = kSoftThreads + 64;
+  // wide: whole warpgroups, so that the softmax can take registers from the rest
+  static constexpr int kThreads = kSoftThreads + (kWide ? 128 : 64);
   static constexpr int kCtasPerSm = kWide ? 1 : 2;
   static constexpr int kTmemCols = kWide ? 512 : 256;
   static constexpr int kRows = 128 * kTiles;
@@ -81,14 +83,14 @@ struct AttnShape {
 struct AttnControl {   // at the end of the shared memory
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty, drain, met;
-  uint64_t s_full[2][2], p_ready[2][2];
+  uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer], [tile][buffer or part]
   uint64_t pv_done[2];
   uint32_t tmem;
   int abort_word;
   int last;
   int start_row;
   long long start_off, total;
-  long long sums[10];
+  long long sums[12];
 };
 
 static_assert(sizeof(AttnControl) <= 512, "fits kControlBytes");
@@ -359,19 +361,24 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       for (int t = 0; t < S::kTiles; ++t) {
         if (!ok || i >= cnt[t]) continue;
         const int k = done[t] + i;
-        if (!(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
-                             &c->abort_word)))
-          break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
-          const uint32_t v0 = ring + (v_it % S::kStages) * S::kStageBytes;
+        const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
+        const uint32_t v0 = ring + (v_it % S::kStages) * S::kStageBytes;
+        constexpr int kSteps = S::kKeys / 16 / S::kParts;
 #pragma unroll
-          for (int x = 0; x < S::kKeys / 16; ++x)
-            mma_tmem(o, s_col(t, k) + x * 8, tile_desc(v0 + x * 16 * 128, S::kKeys * 128, 1024),
-                     o_desc, i > 0 || x > 0);
-          tc_commit(smem_addr(&c->pv_done[t]));
+        for (int part = 0; part < S::kParts; ++part) {
+          if (!(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs + part]), (k / S::kBufs) & 1,
+                               &c->abort_word)))
+            break;
+          tc_fence_after();
+          if (lane == 0) {
+#pragma unroll
+            for (int x = part * kSteps; x < (part + 1) * kSteps; ++x)
+              mma_tmem(o, s_col(t, k) + x * 8, tile_desc(v0 + x * 16 * 128, S::kKeys * 128, 1024),
+                       o_desc, i > 0 || x > 0);
+          }
         }
+        if (!ok) break;
+        release(&c->pv_done[t]);
         if (i + S::kBufs < cnt[t]) {
           if (!k_here) {
             if (!(ok = wait_stage(next_it))) break;
@@ -414,65 +421,74 @@ __device__ __forceinline__ void store_row32(char* to, const float (&o)[32]) {
                    pack2(o[8 * i + 4], o[8 * i + 5], E()), pack2(o[8 * i + 6], o[8 * i + 7], E()));
 }
 
-// Joins the partial sums of the unit's CTAs, a row per warp, its columns over
-// the lanes.
+// Joins the partial sums of the unit's CTAs in their order.  A thread takes
+// four columns of a row, kItems of them at a time, so that the loads of all
+// their parts are in flight together.
 template <typename E, int kD, typename S>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& u, int c_first,
                                           int parts, bool begins_late) {
-  constexpr int W = kD / 32;
-  const int lane = threadIdx.x & 31;
+  constexpr int kItems = 4, kCols = kD / 4;
   const size_t slots = (size_t)gridDim.x * 2;
-  const float* sums = a.partial;
+  const float4* sums = (const float4*)a.partial;
   const float2* stats = (const float2*)(a.partial + slots * S::kRows * kD);
-  for (int r = threadIdx.x >> 5; r < S::kRows; r += S::kSoftThreads / 32) {
-    const int t = r / 128, at = r % 128;
-    const int token = u.first(t) + at / a.G;
-    if (at >= a.tile_tokens * a.G || token >= u.row.n) continue;
-    float top = SV_NEG_INF;
-    for (int p = lane; p < parts; p += 32) {
-      const size_t slot = (size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0);
-      top = fmaxf(top, __ldcg(&stats[slot * S::kRows + r]).x);
-    }
-    top = warp_max(top);
-    float o[W] = {}, l = 0.f;
-    for (int p0 = 0; p0 < parts; p0 += 32) {
-      const int p = p0 + lane;
-      float weight = 0.f, mine = 0.f;
-      if (p < parts) {
-        const size_t slot = (size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0);
-        const float2 ml = __ldcg(&stats[slot * S::kRows + r]);
-        weight = ml.x == SV_NEG_INF ? 0.f : ex2_approx(ml.x - top);
-        mine = ml.y * weight;
-      }
-      l += warp_sum(mine);
-      const int here = min(32, parts - p0);
-#pragma unroll 4
-      for (int i = 0; i < here; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, weight, i);
-        const size_t slot = (size_t)(c_first + p0 + i) * 2 + (p0 + i == 0 && begins_late ? 1 : 0);
-        const float* from = sums + (slot * S::kRows + r) * kD + lane * W;
-        float x[W];
-        if constexpr (W == 4) {
-          const float4 f = __ldcg((const float4*)from);
-          x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
-        } else {
-          const float2 f = __ldcg((const float2*)from);
-          x[0] = f.x, x[1] = f.y;
-        }
+  const int rows0 = max(0, u.last(0) - u.first(0)) * a.G;
+  const int rows1 = S::kTiles > 1 ? max(0, u.last(1) - u.first(1)) * a.G : 0;
+  const int items = (rows0 + rows1) * kCols;
+  for (int x0 = threadIdx.x; x0 < items; x0 += kItems * S::kSoftThreads) {
+    int at[kItems];   // row of the slot
+    float4 o[kItems];
+    float m[kItems], l[kItems];
 #pragma unroll
-        for (int w = 0; w < W; ++w) o[w] += wi > 0.f ? wi * x[w] : 0.f;
+    for (int i = 0; i < kItems; ++i) {
+      const int r = min(x0 + i * S::kSoftThreads, items - 1) / kCols;
+      at[i] = r < rows0 ? r : 128 + r - rows0;
+      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      m[i] = SV_NEG_INF;
+      l[i] = 0.f;
+    }
+#pragma unroll 2
+    for (int p = 0; p < parts; ++p) {
+      const size_t slot = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows;
+      float2 ml[kItems];
+      float4 f[kItems];
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        ml[i] = __ldcg(&stats[slot + at[i]]);
+        f[i] = __ldcg(&sums[(slot + at[i]) * kCols + x0 % kCols]);
+      }
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        if (ml[i].x == SV_NEG_INF) continue;   // the part sees none of the row's keys
+        const float top = fmaxf(m[i], ml[i].x);
+        const float c0 = ex2_approx(m[i] - top), c1 = ex2_approx(ml[i].x - top);
+        m[i] = top;
+        l[i] = l[i] * c0 + ml[i].y * c1;
+        o[i].x = o[i].x * c0 + f[i].x * c1;
+        o[i].y = o[i].y * c0 + f[i].y * c1;
+        o[i].z = o[i].z * c0 + f[i].z * c1;
+        o[i].w = o[i].w * c0 + f[i].w * c1;
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const long long to = (long long)(u.row.begin + token) * a.Hq + u.h * a.G + at % a.G;
-    uint32_t packed[W / 2];
 #pragma unroll
-    for (int w = 0; w < W / 2; ++w) packed[w] = pack2(o[2 * w] * inv, o[2 * w + 1] * inv, E());
-    char* dst = a.out + (to * kD + lane * W) * 2;
-    if constexpr (W == 4) *(uint2*)dst = make_uint2(packed[0], packed[1]);
-    else *(uint32_t*)dst = packed[0];
-    if (a.lse && lane == 0) a.lse[to] = l > 0.f ? (top + log2f(l)) * kLn2 : SV_NEG_INF;
+    for (int i = 0; i < kItems; ++i) {
+      if (x0 + i * S::kSoftThreads >= items) break;
+      const int r = at[i] % 128;
+      const long long to = (long long)(u.row.begin + u.first(at[i] / 128) + r / a.G) * a.Hq +
+                           u.h * a.G + r % a.G;
+      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
+      *(uint2*)(a.out + (to * kD + x0 % kCols * 4) * 2) =
+          make_uint2(pack2(o[i].x * inv, o[i].y * inv, E()), pack2(o[i].z * inv, o[i].w * inv, E()));
+      if (a.lse && x0 % kCols == 0)
+        a.lse[to] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : SV_NEG_INF;
+    }
   }
+}
+
+// The warp's part of a piece of P (and of a scaled O) is in tensor memory.
+__device__ __forceinline__ void hand_over(uint64_t* bar) {
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(bar));
 }
 
 template <typename E, int kD, typename S>
@@ -539,25 +555,37 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           }
         }
         const float ref = m == SV_NEG_INF ? 0.f : m;
-        float sum[4] = {};
+        const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
+        const unsigned long long ref2 = f2_pack(-ref, -ref);
+        unsigned long long sum[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < S::kKeys; x += 32) {
           uint32_t p[16];
 #pragma unroll
           for (int y = 0; y < 32; y += 2) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(bits[x + y]), a.scale_log2, -ref));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(bits[x + y + 1]), a.scale_log2, -ref));
-            sum[(y / 2) % 4] += p0 + p1;
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(bits[x + y]), __uint_as_float(bits[x + y + 1])),
+                             scale2, ref2),
+                      p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum[(y / 2) % 2] = f2_add(sum[(y / 2) % 2], f2_pack(p0, p1));
             p[y / 2] = pack2(p0, p1, E());
           }
           tmem_store16(s_col + x / 2, p);
+          if (S::kParts == 2 && x + 32 == S::kKeys / 2) {
+            tmem_wait_store();
+            hand_over(&c->p_ready[t][buf]);
+          }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float s0, s1;
+        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
         tmem_wait_store();
+      } else if (S::kParts == 2) {
+        hand_over(&c->p_ready[t][buf]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&c->p_ready[t][buf]));
+      hand_over(&c->p_ready[t][buf + S::kParts - 1]);
     }
     if (!ok) break;
     done += n;
@@ -655,10 +683,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     mbar_init(smem_addr(&c->drain), 1);
     mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
     for (int t = 0; t < S::kTiles; ++t) {
-      for (int k = 0; k < S::kBufs; ++k) {
-        mbar_init(smem_addr(&c->s_full[t][k]), 1);
-        mbar_init(smem_addr(&c->p_ready[t][k]), 4);
-      }
+      for (int k = 0; k < S::kBufs; ++k) mbar_init(smem_addr(&c->s_full[t][k]), 1);
+      for (int k = 0; k < S::kBufs * S::kParts; ++k) mbar_init(smem_addr(&c->p_ready[t][k]), 4);
       mbar_init(smem_addr(&c->pv_done[t]), 1);
     }
     mbar_init_fence();
@@ -720,9 +746,15 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
 
   if (w0 < w1) {
     const AttnWalk<S> u(a, c->start_row, c->start_off, w0, w1);
-    if (warp == kLoader) attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map);
-    else if (warp == kIssuer) attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem);
-    else attn_softmax<E, kD, S>(a, u, c, tmem, quota);
+    // wide: three warpgroups launched with 168 registers a thread; 2 x 208 + 88 = 3 x 168
+    if (warp >= kLoader) {
+      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (warp == kLoader) attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map);
+      else if (warp == kIssuer) attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem);
+    } else {
+      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+      attn_softmax<E, kD, S>(a, u, c, tmem, quota);
+    }
   }
   // tokens past the last request's
   const int used = min(max(a.cu_new[a.B], 0), a.T);

@@ -52,7 +52,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 }
 // Polls until the phase is over; false if that took too long or, with an
 // abort word, if the CTA has given up.
-__device__ __noinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_word) {
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_word) {
   const unsigned long long start = clock_ns();
   for (int i = 0; i < kSpinLimit; ++i) {
     if (mbar_try(bar, parity)) return true;
