@@ -301,6 +301,8 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   constexpr uint32_t s_desc = mma_desc(kBf16, 128, S::kKeys, false);
   constexpr uint32_t o_desc = mma_desc(kBf16, 128, kD, true);
   const int lane = threadIdx.x & 31;
+  const uint32_t issue = lane == 0;
+  tmem = __shfl_sync(0xffffffffu, tmem, 0);
   int it = 0, units = 0;
   int done[2] = {0, 0};   // tiles of S issued before this unit, per query tile
   bool ok = true;
@@ -309,19 +311,19 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   auto wait_stage = [&](int i) {
     return mbar_wait(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->abort_word);
   };
+  // Descriptors step by addresses / 16, and never out of their field.
+  const uint64_t q_desc = tile_desc(q_smem, 16, 1024);
+  const uint64_t k_desc = tile_desc(ring, 16, 1024);
+  const uint64_t v_desc = tile_desc(ring, S::kKeys * 128, 1024);
   auto scores = [&](int t, int k, int stage) {   // S(t) = Q(t) K^T, the k-th of query tile t
-    if (lane == 0) {
-      const uint32_t q0 = q_smem + t * S::kQBytes, k0 = ring + stage * S::kStageBytes;
+    const uint64_t q0 = q_desc + t * (S::kQBytes / 16), k0 = k_desc + stage * (S::kStageBytes / 16);
 #pragma unroll
-      for (int d = 0; d < kD / 16; ++d)
-        mma_smem(s_col(t, k), tile_desc(q0 + (d / 4) * 128 * 128 + (d % 4) * 32, 16, 1024),
-                 tile_desc(k0 + (d / 4) * S::kKeys * 128 + (d % 4) * 32, 16, 1024), s_desc, d > 0);
-      tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]));
-    }
+    for (int d = 0; d < kD / 16; ++d)
+      mma_smem(s_col(t, k), q0 + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
+               k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0, issue);
+    tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]), issue);
   };
-  auto release = [&](uint64_t* bar) {
-    if (lane == 0) tc_commit(smem_addr(bar));
-  };
+  auto release = [&](uint64_t* bar) { tc_commit(smem_addr(bar), issue); };
 
   do {
     const int n = u.most();
@@ -362,7 +364,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
         if (!ok || i >= cnt[t]) continue;
         const int k = done[t] + i;
         const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
-        const uint32_t v0 = ring + (v_it % S::kStages) * S::kStageBytes;
+        const uint64_t v0 = v_desc + (v_it % S::kStages) * (S::kStageBytes / 16);
         constexpr int kSteps = S::kKeys / 16 / S::kParts;
 #pragma unroll
         for (int part = 0; part < S::kParts; ++part) {
@@ -370,12 +372,9 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
                                &c->abort_word)))
             break;
           tc_fence_after();
-          if (lane == 0) {
 #pragma unroll
-            for (int x = part * kSteps; x < (part + 1) * kSteps; ++x)
-              mma_tmem(o, s_col(t, k) + x * 8, tile_desc(v0 + x * 16 * 128, S::kKeys * 128, 1024),
-                       o_desc, i > 0 || x > 0);
-          }
+          for (int x = part * kSteps; x < (part + 1) * kSteps; ++x)
+            mma_tmem(o, s_col(t, k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0, issue);
         }
         if (!ok) break;
         release(&c->pv_done[t]);

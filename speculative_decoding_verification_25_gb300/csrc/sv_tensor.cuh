@@ -113,10 +113,13 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// Arrives on `bar` once every tcgen05 operation that this thread issued is done.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
+// Arrives on `bar` once every tcgen05 operation of the issuing lane is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar, uint32_t issue) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(issue)
       : "memory");
 }
 
@@ -184,24 +187,28 @@ __host__ __device__ constexpr uint32_t mma_desc(bool bf16, int m, int n, bool b_
          (uint32_t)(n / 8) << 17 | (uint32_t)(m / 16) << 24;
 }
 
-// d (+)= a b over 16 terms; one thread issues it.
+// d (+)= a b over 16 terms.  The whole warp comes here and the lane with
+// `issue` set issues it: the flow stays uniform, so the descriptors are
+// formed in uniform registers, where the instruction reads them.
 __device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
-                                         bool add) {
+                                         bool add, uint32_t issue) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "r"(issue)
       : "memory");
 }
 // The same with a in tensor memory (two consecutive terms per column).
 __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc,
-                                         bool add) {
+                                         bool add, uint32_t issue) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "r"(issue)
       : "memory");
 }
 
