@@ -13,8 +13,8 @@
 // operands' type, in the place of S, and O += P V reads P from there.  Rows
 // never meet: no shuffle, and unused rows may hold anything.
 //
-// A CTA is one loader warp (TMA into a ring of key and value tiles), one
-// warp that issues the products, and four softmax warps per query tile.
+// A CTA is one loader warp (TMA into a ring of key and value tiles) and, per
+// query tile, one warp that issues the products and four softmax warps.
 // Two forms:
 //   wide    two query tiles of one unit against tiles of 128 keys: while one
 //           tile's softmax runs, the tensor core works on the other's;
@@ -84,7 +84,7 @@ struct AttnControl {   // at the end of the shared memory
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty, drain, met;
   uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer], [tile][buffer or part]
-  uint64_t pv_done[2];
+  uint64_t pv_done[2], turn[2];
   uint32_t tmem;
   int abort_word;
   int last;
@@ -209,6 +209,11 @@ struct AttnWalk {
   }
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -291,79 +296,96 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
 }
 
 // ----------------------------------------------------------------- products
-// One warp; lane 0 issues.  Columns of tensor memory: kBufs S buffers per
-// query tile, then one O per query tile.
+// One warp per query tile.  A product's issue lasts as long as the tensor core
+// takes to accept it, so what a warp does between products (waits, commits)
+// would leave the tensor core idle; the other tile's warp fills that.  The
+// two take turns, O += P V and the next scores at a time: left to themselves
+// they fall into step, both tiles' softmax and then both tiles' products.
+// The products of one warp run in the order of their issue: S of the next
+// keys follows O += P V, whose P lies where S goes.
+// Columns of tensor memory: kBufs S buffers per query tile, then one O per
+// query tile.
 template <typename E, int kD, typename S>
 __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
                                               uint32_t q_smem, uint32_t ring, char* ring_ptr,
-                                              uint32_t tmem) {
-  constexpr bool kBf16 = sizeof(E) == 2 && std::is_same<E, __nv_bfloat16>::value;
+                                              uint32_t tmem, int t) {
+  constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
   constexpr uint32_t s_desc = mma_desc(kBf16, 128, S::kKeys, false);
   constexpr uint32_t o_desc = mma_desc(kBf16, 128, kD, true);
   const int lane = threadIdx.x & 31;
   const uint32_t issue = lane == 0;
   tmem = __shfl_sync(0xffffffffu, tmem, 0);
+  t = __shfl_sync(0xffffffffu, t, 0);
+  const uint32_t s_base = tmem + t * S::kBufs * S::kKeys;
+  const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
   int it = 0, units = 0;
-  int done[2] = {0, 0};   // tiles of S issued before this unit, per query tile
+  int done = 0;   // tiles of S issued before this unit
+  int turns = 0;
   bool ok = true;
 
-  auto s_col = [&](int t, int k) { return tmem + (t * S::kBufs + k % S::kBufs) * S::kKeys; };
+  auto s_col = [&](int k) { return s_base + (k % S::kBufs) * S::kKeys; };
   auto wait_stage = [&](int i) {
     return mbar_wait(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->abort_word);
   };
   // Descriptors step by addresses / 16, and never out of their field.
-  const uint64_t q_desc = tile_desc(q_smem, 16, 1024);
+  const uint64_t q_desc = tile_desc(q_smem + t * S::kQBytes, 16, 1024);
   const uint64_t k_desc = tile_desc(ring, 16, 1024);
   const uint64_t v_desc = tile_desc(ring, S::kKeys * 128, 1024);
-  auto scores = [&](int t, int k, int stage) {   // S(t) = Q(t) K^T, the k-th of query tile t
-    const uint64_t q0 = q_desc + t * (S::kQBytes / 16), k0 = k_desc + stage * (S::kStageBytes / 16);
+  auto scores = [&](int k, int stage) {   // S = Q K^T, the tile's k-th
+    const uint64_t k0 = k_desc + stage * (S::kStageBytes / 16);
 #pragma unroll
     for (int d = 0; d < kD / 16; ++d)
-      mma_smem(s_col(t, k), q0 + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
+      mma_smem(s_col(k), q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
                k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0, issue);
     tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]), issue);
   };
-  auto release = [&](uint64_t* bar) { tc_commit(smem_addr(bar), issue); };
+  auto my_turn = [&]() {   // tile 0 has the first
+    const int before = turns++ - (t == 0 ? 1 : 0);
+    return S::kTiles == 1 || before < 0 ||
+           mbar_wait(smem_addr(&c->turn[t]), before & 1, &c->abort_word);
+  };
+  auto pass_turn = [&]() {
+    if (S::kTiles > 1 && lane == 0) mbar_arrive(smem_addr(&c->turn[1 - t]));
+  };
+  // A slot is free once every issuer's products with it are done; one that
+  // has none waits for the slot to be full all the same, so that its arrivals
+  // keep to the slot's laps.
+  auto release = [&](uint64_t* bar, bool used) {
+    if (used) tc_commit(smem_addr(bar), issue);
+    else if (lane == 0) mbar_arrive(smem_addr(bar));
+  };
 
   do {
-    const int n = u.most();
+    const int n = u.most(), cnt = u.count(t);
     if (n == 0) continue;
-    int cnt[2] = {u.count(0), S::kTiles > 1 ? u.count(1) : 0};
     if (!(ok = mbar_wait(smem_addr(&c->q_full), units & 1, &c->abort_word))) break;
     ++units;
     tc_fence_after();
     for (int i = 0; i < min(n, S::kBufs); ++i) {
       if (!(ok = wait_stage(it))) break;
       tc_fence_after();
-#pragma unroll
-      for (int t = 0; t < S::kTiles; ++t)
-        if (i < cnt[t]) scores(t, done[t] + i, it % S::kStages);
-      release(&c->empty[it % S::kStages]);
+      if (i < cnt) scores(done + i, it % S::kStages);
+      release(&c->empty[it % S::kStages], i < cnt);
       ++it;
     }
-    if (ok && n <= S::kBufs) release(&c->q_empty);
+    if (ok && cnt <= S::kBufs) release(&c->q_empty, cnt > 0);
     for (int i = 0; ok && i < n; ++i) {
-      const int v_it = it++;
-      const bool more = i + S::kBufs < n;
-      const int next_it = more ? it++ : 0;
+      const int v_it = it++, k = done + i;
+      const bool more = i + S::kBufs < n, active = i < cnt, next = i + S::kBufs < cnt;
       if (!(ok = wait_stage(v_it))) break;
-      // values past the request's length must not reach the sums: 0 * NaN is NaN
-      const int valid = u.row.L - (u.j0 + i) * S::kKeys;
-      if (valid < S::kKeys) {
-        char* v0 = ring_ptr + (v_it % S::kStages) * S::kStageBytes;
-        const int chunks = (S::kKeys - valid) * 8;
-        for (int x = lane; x < chunks * S::kBlocks; x += 32)
-          *(uint4*)(v0 + ((x / chunks) * S::kKeys + valid) * 128 + (x % chunks) * 16) =
-              make_uint4(0, 0, 0, 0);
-        fence_async_shared();
-        __syncwarp();
-      }
-      bool k_here = false;
-#pragma unroll
-      for (int t = 0; t < S::kTiles; ++t) {
-        if (!ok || i >= cnt[t]) continue;
-        const int k = done[t] + i;
-        const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
+      if (active) {
+        // values past the request's length must not reach the sums: 0 * NaN is NaN
+        // (the other tile's warp writes the same zeros)
+        const int valid = u.row.L - (u.j0 + i) * S::kKeys;
+        if (valid < S::kKeys) {
+          char* v0 = ring_ptr + (v_it % S::kStages) * S::kStageBytes;
+          const int chunks = (S::kKeys - valid) * 8;
+          for (int x = lane; x < chunks * S::kBlocks; x += 32)
+            *(uint4*)(v0 + ((x / chunks) * S::kKeys + valid) * 128 + (x % chunks) * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+          __syncwarp();
+        }
         const uint64_t v0 = v_desc + (v_it % S::kStages) * (S::kStageBytes / 16);
         constexpr int kSteps = S::kKeys / 16 / S::kParts;
 #pragma unroll
@@ -371,34 +393,35 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
           if (!(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs + part]), (k / S::kBufs) & 1,
                                &c->abort_word)))
             break;
+          if (part == 0 && !(ok = my_turn())) break;
           tc_fence_after();
 #pragma unroll
           for (int x = part * kSteps; x < (part + 1) * kSteps; ++x)
-            mma_tmem(o, s_col(t, k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0, issue);
+            mma_tmem(o, s_col(k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0, issue);
         }
         if (!ok) break;
-        release(&c->pv_done[t]);
-        if (i + S::kBufs < cnt[t]) {
-          if (!k_here) {
-            if (!(ok = wait_stage(next_it))) break;
-            tc_fence_after();
-            k_here = true;
-          }
-          scores(t, k + S::kBufs, next_it % S::kStages);
-        }
+      } else if (!(ok = my_turn())) {
+        break;
       }
-      if (!ok) break;
-      release(&c->empty[v_it % S::kStages]);
+      const int k_it = more ? it++ : 0;
       if (more) {
-        release(&c->empty[next_it % S::kStages]);
-        if (i + S::kBufs + 1 == n) release(&c->q_empty);
+        if (!(ok = wait_stage(k_it))) break;
+        tc_fence_after();
+        if (next) scores(k + S::kBufs, k_it % S::kStages);
+      }
+      pass_turn();
+      // with one S buffer the next scores tell that O is up to date
+      if (active && (S::kBufs > 1 || !next)) release(&c->pv_done[t], true);
+      release(&c->empty[v_it % S::kStages], active);
+      if (more) {
+        release(&c->empty[k_it % S::kStages], next);
+        if (i + S::kBufs + 1 == cnt) release(&c->q_empty, true);
       }
     }
-    done[0] += cnt[0];
-    done[1] += cnt[1];
+    done += cnt;
   } while (ok && u.next());
   // everything issued is done before the CTA's memory goes
-  release(&c->drain);
+  release(&c->drain, true);
   (void)mbar_poll(smem_addr(&c->drain), 0, nullptr);
   __syncwarp();
 }
@@ -498,7 +521,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
   const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
   const uint32_t o_col = tmem + lanes + S::kTiles * S::kBufs * S::kKeys + t * kD;
   int done = 0;                                    // tiles of S taken before this unit
-  int meetings = 0;
+  int meetings = 0, rounds = 0;
   bool ok = true;
   do {
     const int n = u.count(t);
@@ -529,18 +552,29 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           for (int x = 0; x < S::kKeys; ++x)
             if (x >= left) bits[x] = 0xff800000u;
         }
-        float top[4] = {SV_NEG_INF, SV_NEG_INF, SV_NEG_INF, SV_NEG_INF};
+        float top[8];
 #pragma unroll
-        for (int x = 0; x < S::kKeys; ++x) top[x % 4] = fmaxf(top[x % 4], __uint_as_float(bits[x]));
-        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        for (int x = 0; x < 8; ++x) top[x] = __uint_as_float(bits[x]);
+#pragma unroll
+        for (int x = 8; x < S::kKeys; x += 16)
+#pragma unroll
+          for (int y = 0; y < 8 && x + 8 + y < S::kKeys + 8; ++y)
+            top[y] = x + 8 + y < S::kKeys ? max3(top[y], __uint_as_float(bits[x + y]),
+                                                 __uint_as_float(bits[x + 8 + y]))
+                                          : fmaxf(top[y], __uint_as_float(bits[x + y]));
+        const float high =
+            max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) *
+            a.scale_log2;
         const bool raise = mine && (i == 0 ? high > m : high > m + kSlack);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (m == SV_NEG_INF ? 0.f : ex2_approx(m - high)) : 1.f;
           if (raise) m = high;
           l *= f;
           if (i > 0) {   // what was summed before, once the products are done
-            if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
-            tc_fence_after();
+            if (S::kBufs > 1) {
+              if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
+              tc_fence_after();
+            }
 #pragma unroll
             for (int x = 0; x < kD; x += 32) {
               uint32_t o[32];
@@ -588,10 +622,14 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     }
     if (!ok) break;
     done += n;
-    // The last scores came with the products kBufs tiles before done; a wait
-    // sees a phase's parity alone, so those after them are waited for one by one.
-    for (int k = done - min(n, S::kBufs); ok && k < done; ++k)
-      ok = mbar_wait(smem_addr(&c->pv_done[t]), k & 1, &c->abort_word);
+    if (S::kBufs == 1) {   // one arrival per unit
+      if (n > 0) ok = mbar_wait(smem_addr(&c->pv_done[t]), rounds++ & 1, &c->abort_word);
+    } else {
+      // The last scores came with the products kBufs tiles before done; a wait
+      // sees a phase's parity alone, so those after them are waited for one by one.
+      for (int k = done - min(n, S::kBufs); ok && k < done; ++k)
+        ok = mbar_wait(smem_addr(&c->pv_done[t]), k & 1, &c->abort_word);
+    }
     if (!ok) break;
     tc_fence_after();
     const bool whole = u.j0 == 0 && u.j1 == u.tiles;
@@ -675,16 +713,17 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   if (warp == kLoader && lane == 0) {
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(smem_addr(&c->full[i]), 1);
-      mbar_init(smem_addr(&c->empty[i]), 1);
+      mbar_init(smem_addr(&c->empty[i]), S::kTiles);
     }
     mbar_init(smem_addr(&c->q_full), 1);
-    mbar_init(smem_addr(&c->q_empty), 1);
-    mbar_init(smem_addr(&c->drain), 1);
+    mbar_init(smem_addr(&c->q_empty), S::kTiles);
+    mbar_init(smem_addr(&c->drain), S::kTiles);
     mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
     for (int t = 0; t < S::kTiles; ++t) {
       for (int k = 0; k < S::kBufs; ++k) mbar_init(smem_addr(&c->s_full[t][k]), 1);
       for (int k = 0; k < S::kBufs * S::kParts; ++k) mbar_init(smem_addr(&c->p_ready[t][k]), 4);
       mbar_init(smem_addr(&c->pv_done[t]), 1);
+      mbar_init(smem_addr(&c->turn[t]), 1);
     }
     mbar_init_fence();
     c->abort_word = 0;
@@ -749,7 +788,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     if (warp >= kLoader) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
       if (warp == kLoader) attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map);
-      else if (warp == kIssuer) attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem);
+      else if (warp < kIssuer + S::kTiles)
+        attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem, warp - kIssuer);
     } else {
       if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
       attn_softmax<E, kD, S>(a, u, c, tmem, quota);
