@@ -69,7 +69,6 @@ struct AttnShape {
   static constexpr int kQBytes = 128 * kD * 2;
   static constexpr int kStageBytes = kKeys * kD * 2;
   static constexpr int kStages = kD == 128 ? 5 : 8;  // what is left of the shared memory
-  static constexpr int kParts = kWide ? 2 : 1;       // P is handed over in this many pieces
   static constexpr int kSoftThreads = 128 * kTiles;
   // wide: whole warpgroups, so that the softmax can take registers from the rest
   static constexpr int kThreads = kSoftThreads + (kWide ? 128 : 64);
@@ -83,7 +82,7 @@ struct AttnShape {
 struct AttnControl {   // at the end of the shared memory
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty, drain, met;
-  uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer], [tile][buffer or part]
+  uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer]
   uint64_t pv_done[2], turn[2];
   uint32_t tmem;
   int abort_word;
@@ -331,14 +330,6 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   const uint64_t q_desc = tile_desc(q_smem + t * S::kQBytes, 16, 1024);
   const uint64_t k_desc = tile_desc(ring, 16, 1024);
   const uint64_t v_desc = tile_desc(ring, S::kKeys * 128, 1024);
-  auto scores = [&](int k, int stage) {   // S = Q K^T, the tile's k-th
-    const uint64_t k0 = k_desc + stage * (S::kStageBytes / 16);
-#pragma unroll
-    for (int d = 0; d < kD / 16; ++d)
-      mma_smem(s_col(k), q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
-               k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0, issue);
-    tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]), issue);
-  };
   auto my_turn = [&]() {   // tile 0 has the first
     const int before = turns++ - (t == 0 ? 1 : 0);
     return S::kTiles == 1 || before < 0 ||
@@ -346,6 +337,18 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   };
   auto pass_turn = [&]() {
     if (S::kTiles > 1 && lane == 0) mbar_arrive(smem_addr(&c->turn[1 - t]));
+  };
+  // S = Q K^T, the tile's k-th; the turn passes before the last two products,
+  // which last about as long as the other warp takes to see it
+  auto scores = [&](int k, int stage, bool pass) {
+    const uint64_t k0 = k_desc + stage * (S::kStageBytes / 16);
+#pragma unroll
+    for (int d = 0; d < kD / 16; ++d) {
+      if (d == kD / 16 - 2 && pass) pass_turn();
+      mma_smem(s_col(k), q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
+               k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0, issue);
+    }
+    tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]), issue);
   };
   // A slot is free once every issuer's products with it are done; one that
   // has none waits for the slot to be full all the same, so that its arrivals
@@ -364,7 +367,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
     for (int i = 0; i < min(n, S::kBufs); ++i) {
       if (!(ok = wait_stage(it))) break;
       tc_fence_after();
-      if (i < cnt) scores(done + i, it % S::kStages);
+      if (i < cnt) scores(done + i, it % S::kStages, false);
       release(&c->empty[it % S::kStages], i < cnt);
       ++it;
     }
@@ -372,6 +375,8 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
     for (int i = 0; ok && i < n; ++i) {
       const int v_it = it++, k = done + i;
       const bool more = i + S::kBufs < n, active = i < cnt, next = i + S::kBufs < cnt;
+      const int k_it = more ? it++ : 0;
+      // every wait comes before the products: the tensor core's queue is short
       if (!(ok = wait_stage(v_it))) break;
       if (active) {
         // values past the request's length must not reach the sums: 0 * NaN is NaN
@@ -386,32 +391,23 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
           fence_async_shared();
           __syncwarp();
         }
-        const uint64_t v0 = v_desc + (v_it % S::kStages) * (S::kStageBytes / 16);
-        constexpr int kSteps = S::kKeys / 16 / S::kParts;
-#pragma unroll
-        for (int part = 0; part < S::kParts; ++part) {
-          if (!(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs + part]), (k / S::kBufs) & 1,
-                               &c->abort_word)))
-            break;
-          if (part == 0 && !(ok = my_turn())) break;
-          tc_fence_after();
-#pragma unroll
-          for (int x = part * kSteps; x < (part + 1) * kSteps; ++x)
-            mma_tmem(o, s_col(k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0, issue);
-        }
-        if (!ok) break;
-      } else if (!(ok = my_turn())) {
+      }
+      if (more && !(ok = wait_stage(k_it))) break;
+      if (active && !(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
+                                     &c->abort_word)))
         break;
+      if (!(ok = my_turn())) break;
+      tc_fence_after();
+      if (active) {
+        const uint64_t v0 = v_desc + (v_it % S::kStages) * (S::kStageBytes / 16);
+#pragma unroll
+        for (int x = 0; x < S::kKeys / 16; ++x)
+          mma_tmem(o, s_col(k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0, issue);
       }
-      const int k_it = more ? it++ : 0;
-      if (more) {
-        if (!(ok = wait_stage(k_it))) break;
-        tc_fence_after();
-        if (next) scores(k + S::kBufs, k_it % S::kStages);
-      }
-      pass_turn();
       // with one S buffer the next scores tell that O is up to date
       if (active && (S::kBufs > 1 || !next)) release(&c->pv_done[t], true);
+      if (next) scores(k + S::kBufs, k_it % S::kStages, true);
+      else pass_turn();
       release(&c->empty[v_it % S::kStages], active);
       if (more) {
         release(&c->empty[k_it % S::kStages], next);
@@ -427,6 +423,21 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
 }
 
 // ------------------------------------------------------------------ softmax
+template <int kCount>
+__device__ __forceinline__ float row_max(const uint32_t* bits) {
+  float top[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) top[x] = __uint_as_float(bits[x]);
+#pragma unroll
+  for (int x = 8; x + 8 < kCount; x += 16)
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      top[y] = max3(top[y], __uint_as_float(bits[x + y]), __uint_as_float(bits[x + 8 + y]));
+#pragma unroll
+  for (int y = 0; y < 8; ++y) top[y] = fmaxf(top[y], __uint_as_float(bits[kCount - 8 + y]));
+  return max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
+}
+
 // All softmax warps meet (their `phase`-th meeting); false if it was given up.
 __device__ __forceinline__ bool soft_meet(AttnControl* c, int phase) {
   __syncwarp();
@@ -506,7 +517,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
   }
 }
 
-// The warp's part of a piece of P (and of a scaled O) is in tensor memory.
+// The warp's part of P (and of a scaled O) is in tensor memory.
 __device__ __forceinline__ void hand_over(uint64_t* bar) {
   tc_fence_before();
   __syncwarp();
@@ -552,84 +563,80 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           for (int x = 0; x < S::kKeys; ++x)
             if (x >= left) bits[x] = 0xff800000u;
         }
-        float top[8];
+        // The unit's first tile sets the reference; a later one assumes that it
+        // holds, looks for its maximum on the way (another pipe than the
+        // exponentials'), and starts over in the rare case that it does not.
+        float high;
+        if (i == 0) {
+          high = row_max<S::kKeys>(bits) * a.scale_log2;
+          if (mine) m = high;
+        }
+        float sum;
+        while (true) {
+          const float ref = m == SV_NEG_INF ? 0.f : m;
+          const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
+          const unsigned long long ref2 = f2_pack(-ref, -ref);
+          unsigned long long sums[2] = {0, 0};
 #pragma unroll
-        for (int x = 0; x < 8; ++x) top[x] = __uint_as_float(bits[x]);
+          for (int x = 0; x < S::kKeys; x += 32) {
+            uint32_t p[16];
 #pragma unroll
-        for (int x = 8; x < S::kKeys; x += 16)
-#pragma unroll
-          for (int y = 0; y < 8 && x + 8 + y < S::kKeys + 8; ++y)
-            top[y] = x + 8 + y < S::kKeys ? max3(top[y], __uint_as_float(bits[x + y]),
-                                                 __uint_as_float(bits[x + 8 + y]))
-                                          : fmaxf(top[y], __uint_as_float(bits[x + y]));
-        const float high =
-            max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) *
-            a.scale_log2;
-        const bool raise = mine && (i == 0 ? high > m : high > m + kSlack);
-        if (__any_sync(0xffffffffu, raise)) {
+            for (int y = 0; y < 32; y += 2) {
+              float p0, p1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(bits[x + y]), __uint_as_float(bits[x + y + 1])),
+                               scale2, ref2),
+                        p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              sums[(y / 2) % 2] = f2_add(sums[(y / 2) % 2], f2_pack(p0, p1));
+              p[y / 2] = pack2(p0, p1, E());
+            }
+            tmem_store16(s_col + x / 2, p);
+          }
+          float s0, s1;
+          f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
+          sum = s0 + s1;
+          if (i == 0) break;
+          high = row_max<S::kKeys>(bits) * a.scale_log2;
+          const bool raise = mine && high > m + kSlack;
+          if (!__any_sync(0xffffffffu, raise)) break;
+          // scale what was summed before, once the products are done
           const float f = raise ? (m == SV_NEG_INF ? 0.f : ex2_approx(m - high)) : 1.f;
           if (raise) m = high;
           l *= f;
-          if (i > 0) {   // what was summed before, once the products are done
-            if (S::kBufs > 1) {
-              if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
-              tc_fence_after();
-            }
+          if (S::kBufs > 1 && i > 0) {
+            if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int x = 0; x < kD; x += 32) {
+            uint32_t o[32];
+            tmem_load32(o_col + x, o);
+            tmem_wait_load();
+            tmem_pin<32>(o);
 #pragma unroll
-            for (int x = 0; x < kD; x += 32) {
-              uint32_t o[32];
-              tmem_load32(o_col + x, o);
-              tmem_wait_load();
-              tmem_pin<32>(o);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-              tmem_store32(o_col + x, o);
-            }
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+            tmem_store32(o_col + x, o);
           }
         }
-        const float ref = m == SV_NEG_INF ? 0.f : m;
-        const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
-        const unsigned long long ref2 = f2_pack(-ref, -ref);
-        unsigned long long sum[2] = {0, 0};
-#pragma unroll
-        for (int x = 0; x < S::kKeys; x += 32) {
-          uint32_t p[16];
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            float p0, p1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(bits[x + y]), __uint_as_float(bits[x + y + 1])),
-                             scale2, ref2),
-                      p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            sum[(y / 2) % 2] = f2_add(sum[(y / 2) % 2], f2_pack(p0, p1));
-            p[y / 2] = pack2(p0, p1, E());
-          }
-          tmem_store16(s_col + x / 2, p);
-          if (S::kParts == 2 && x + 32 == S::kKeys / 2) {
-            tmem_wait_store();
-            hand_over(&c->p_ready[t][buf]);
-          }
-        }
-        float s0, s1;
-        f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
-        l += s0 + s1;
+        if (!ok) break;
+        l += sum;
         tmem_wait_store();
-      } else if (S::kParts == 2) {
-        hand_over(&c->p_ready[t][buf]);
       }
-      hand_over(&c->p_ready[t][buf + S::kParts - 1]);
+      // With two S buffers the scores do not tell that the last O += P V is
+      // done; the wait keeps at most one of them open, as a wait that sees a
+      // phase's parity alone needs.
+      if (S::kBufs > 1 && i > 0 &&
+          !(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word)))
+        break;
+      hand_over(&c->p_ready[t][buf]);
     }
     if (!ok) break;
     done += n;
-    if (S::kBufs == 1) {   // one arrival per unit
-      if (n > 0) ok = mbar_wait(smem_addr(&c->pv_done[t]), rounds++ & 1, &c->abort_word);
-    } else {
-      // The last scores came with the products kBufs tiles before done; a wait
-      // sees a phase's parity alone, so those after them are waited for one by one.
-      for (int k = done - min(n, S::kBufs); ok && k < done; ++k)
-        ok = mbar_wait(smem_addr(&c->pv_done[t]), k & 1, &c->abort_word);
-    }
+    // one S buffer: one arrival per unit, else one per tile
+    if (n > 0)
+      ok = mbar_wait(smem_addr(&c->pv_done[t]), (S::kBufs > 1 ? done - 1 : rounds++) & 1,
+                     &c->abort_word);
     if (!ok) break;
     tc_fence_after();
     const bool whole = u.j0 == 0 && u.j1 == u.tiles;
@@ -637,7 +644,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       if (any) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const long long to = (long long)(u.row.begin + token) * a.Hq + u.h * a.G + r % a.G;
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < kD; x += 32) {
           uint32_t bits[32] = {};
           if (n > 0) {
@@ -663,7 +670,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     const size_t slot = (size_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first && begins_late ? 1 : 0);
     if (any) {
       float* to = a.partial + (slot * S::kRows + t * 128 + r) * kD;
-#pragma unroll
+#pragma unroll 1
       for (int x = 0; x < kD; x += 32) {
         uint32_t bits[32] = {};
         if (n > 0) {
@@ -720,8 +727,10 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     mbar_init(smem_addr(&c->drain), S::kTiles);
     mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
     for (int t = 0; t < S::kTiles; ++t) {
-      for (int k = 0; k < S::kBufs; ++k) mbar_init(smem_addr(&c->s_full[t][k]), 1);
-      for (int k = 0; k < S::kBufs * S::kParts; ++k) mbar_init(smem_addr(&c->p_ready[t][k]), 4);
+      for (int k = 0; k < S::kBufs; ++k) {
+        mbar_init(smem_addr(&c->s_full[t][k]), 1);
+        mbar_init(smem_addr(&c->p_ready[t][k]), 4);
+      }
       mbar_init(smem_addr(&c->pv_done[t]), 1);
       mbar_init(smem_addr(&c->turn[t]), 1);
     }

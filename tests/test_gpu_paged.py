@@ -178,6 +178,9 @@ CASES = {
     "all_empty": ([(0, 2), (0, 0)], 2, 1, 64, 8, "bf16"),
     "many": ([(1 + b % 90, 1 + b % 3) for b in range(700)], 2, 1, 64, 8, "bf16"),
     "mixed": ([(2000, 1), (600, 600), (1500, 5), (31, 31), (4000, 1)], 8, 2, 128, 64, "bf16"),
+    "many_tiles": (_rows(8, 60, 3000, 5), 16, 8, 128, 16, "bf16"),
+    "many_tiles_64": (_rows(9, 150, 2500, 3), 8, 8, 64, 64, "f16"),
+    "many_tiles_wide": (_rows(10, 40, 1500, 70), 8, 4, 64, 32, "bf16"),
     "split": ([(20011, 1)], 8, 1, 128, 64, "bf16"),
     "split_wide": ([(9000, 300)], 4, 1, 64, 32, "bf16"),
 }
@@ -268,7 +271,7 @@ def test_attention_flags_bad_lengths_and_pages():
     assert flags.item() & N.SV_DEV_BAD_LENGTH
 
 
-@pytest.mark.parametrize("name", ["verify", "mixed", "split", "split_wide", "empty_rows"])
+@pytest.mark.parametrize("name", ["verify", "many_tiles", "many_tiles_64", "mixed", "split", "split_wide", "empty_rows"])
 def test_attention_gives_the_same_bits_every_time(name):
     import torch
     rows, *shape = CASES[name]
