@@ -79,21 +79,6 @@ struct AttnShape {
   static constexpr int kSmemBytes = kTiles * kQBytes + kStages * kStageBytes + kControlBytes;
 };
 
-struct AttnControl {   // at the end of the shared memory
-  uint64_t full[8], empty[8];
-  uint64_t q_full, q_empty, drain, met;
-  uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer]
-  uint64_t pv_done[2], turn[2];
-  uint32_t tmem;
-  int abort_word;
-  int last;
-  int start_row;
-  long long start_off, total;
-  long long sums[12];
-};
-
-static_assert(sizeof(AttnControl) <= 512, "fits kControlBytes");
-
 // A request's lengths, clamped to what its arrays hold; n == 0: nothing to do.
 struct AttnRow {
   int begin, n, L;
@@ -110,73 +95,104 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, int b, bool* bad 
   if (bad && (!sound || r.L != len)) *bad = true;
   return r;
 }
-// Key tiles that tokens up to t1 of a request see.
-template <int kKeys>
-__device__ __forceinline__ int tiles_seen(const AttnRow& r, int t1) {
-  return (max(0, r.L - r.n + t1) + kKeys - 1) / kKeys;
+// sum of floor((a i + b) / m) for i in [0, n), by the Euclidean algorithm on
+// (a, m).  n a + b stays below 2^32.
+__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  long long sum = 0;
+  while (n > 0) {
+    sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
+    a %= m;
+    b %= m;
+    const unsigned top = a * n + b;
+    if (top < m) break;
+    n = top / m;
+    b = top % m;
+    const unsigned swap = m;
+    m = a;
+    a = swap;
+  }
+  return sum;
 }
-// Weight of query unit m: its key tiles, one for a unit that sees no key.
+
+// The query units of a request: kTiles tiles of tile_tokens tokens each.  A
+// unit's weight is the number of key tiles that its last token sees, one for
+// a unit that sees no key.
 template <typename S>
-__device__ __forceinline__ int unit_tiles(const AttnArgs& a, const AttnRow& r, int m) {
-  const int tokens = S::kTiles * a.tile_tokens;
-  return max(1, tiles_seen<S::kKeys>(r, min(r.n, (m + 1) * tokens)));
-}
-template <typename S>
-__device__ __forceinline__ int units_of(const AttnArgs& a, const AttnRow& r) {
-  const int tokens = S::kTiles * a.tile_tokens;
-  return (r.n + tokens - 1) / tokens;
-}
+struct AttnUnits {
+  AttnRow row;
+  int step;      // tokens per unit
+  int count;     // units
+
+  __device__ __forceinline__ AttnUnits() {}
+  __device__ __forceinline__ AttnUnits(const AttnArgs& a, const AttnRow& r)
+      : row(r), step(S::kTiles * a.tile_tokens), count((r.n + step - 1) / step) {}
+  // key tiles that the request's tokens up to t1 see
+  __device__ __forceinline__ int seen(int t1) const {
+    return (max(0, row.L - row.n + t1) + S::kKeys - 1) / S::kKeys;
+  }
+  __device__ __forceinline__ int tiles(int m) const {
+    return max(1, seen(min(row.n, (m + 1) * step)));
+  }
+  // weight of the first `units` units
+  __device__ __forceinline__ long long before(int units) const {
+    if (units == 0) return 0;
+    const int full = units == count ? units - 1 : units;   // the last may be short
+    const int context = row.L - row.n;
+    const int blind = context < 0 ? min(full, -context / step) : 0;
+    return blind + (units - full) * (long long)tiles(count - 1) +
+           floor_sum(full - blind, S::kKeys, step, context + (blind + 1) * step + S::kKeys - 1);
+  }
+};
+
+// Where a CTA's range starts.
+struct AttnStart {
+  AttnRow row;
+  int b, h, m, j0;
+};
+
+struct AttnControl {   // at the end of the shared memory
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty, drain, met;
+  uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer]
+  uint64_t pv_done[2], turn[2];
+  uint32_t tmem;
+  int abort_word;
+  int last;
+  AttnStart start;
+  long long sums[12];
+};
+
+static_assert(sizeof(AttnControl) <= 512, "fits kControlBytes");
 
 // A CTA's walk over its range of the work; every warp keeps its own.
 template <typename S>
 struct AttnWalk {
   const AttnArgs& a;
-  AttnRow row;
-  int b, h, m, n_units;
+  AttnUnits<S> units;
+  int b, h, m;
   int j0, j1;                 // key tiles of the unit that are this CTA's
   int tiles;                  // all key tiles of the unit
-  long long w, w_end, unit_begin;
+  int left;                   // of the range, this unit's included
 
-  __device__ __forceinline__ AttnWalk(const AttnArgs& args, int start_row, long long off,
-                                      long long w0, long long w1)
-      : a(args), b(start_row), w(w0), w_end(w1) {
-    row = attn_row(a, b);
-    n_units = units_of<S>(a, row);
-    long long head = 0;       // weight of one head's units
-    const int lane = threadIdx.x & 31;
-    for (int i = lane; i < n_units; i += 32) head += unit_tiles<S>(a, row, i);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) head += __shfl_xor_sync(0xffffffffu, head, o);
-    h = (int)(off / head);
-    off -= h * head;
-    m = 0;
-    tiles = unit_tiles<S>(a, row, 0);
-    while (off >= tiles) {
-      off -= tiles;
-      tiles = unit_tiles<S>(a, row, ++m);
-    }
-    j0 = (int)off;
-    unit_begin = w - off;
-    clip();
-  }
-  __device__ __forceinline__ void clip() {
-    j1 = (int)min((long long)tiles, j0 + (w_end - w));
+  __device__ __forceinline__ AttnWalk(const AttnArgs& args, const AttnStart& s, int length)
+      : a(args), units(args, s.row), b(s.b), h(s.h), m(s.m), j0(s.j0), left(length) {
+    tiles = units.tiles(m);
+    j1 = min(tiles, j0 + left);
   }
   // The next unit; false at the end of the range.
   __device__ __forceinline__ bool next() {
-    w += j1 - j0;
-    if (w >= w_end) return false;
-    if (++m == n_units) {
+    left -= j1 - j0;
+    if (left <= 0) return false;
+    if (++m == units.count) {
       m = 0;
       if (++h == a.Hk) {
         h = 0;
         next_row();
       }
     }
-    tiles = unit_tiles<S>(a, row, m);
+    tiles = units.tiles(m);
     j0 = 0;
-    unit_begin = w;
-    clip();
+    j1 = min(tiles, left);
     return true;
   }
   // The next request with tokens (there is one: the range has not ended).
@@ -190,16 +206,20 @@ struct AttnWalk {
         break;
       }
     }
-    row = attn_row(a, b);
-    n_units = units_of<S>(a, row);
+    units = AttnUnits<S>(a, attn_row(a, b));
   }
   // Query tile t of the unit: its tokens [first, last) within the request,
   // and how many of the unit's key tiles it needs of this CTA.
   __device__ __forceinline__ int first(int t) const { return (m * S::kTiles + t) * a.tile_tokens; }
-  __device__ __forceinline__ int last(int t) const { return min(row.n, first(t) + a.tile_tokens); }
+  __device__ __forceinline__ int last(int t) const {
+    return min(units.row.n, first(t) + a.tile_tokens);
+  }
   __device__ __forceinline__ int count(int t) const {
-    if (first(t) >= row.n) return 0;
-    return max(0, min(j1, tiles_seen<S::kKeys>(row, last(t))) - j0);
+    if (first(t) >= units.row.n) return 0;
+    return max(0, min(j1, units.seen(last(t))) - j0);
+  }
+  __device__ __forceinline__ int rows() const {   // query rows of the unit
+    return (last(S::kTiles - 1 > 0 && first(1) < units.row.n ? 1 : 0) - first(0)) * a.G;
   }
   __device__ __forceinline__ int most() const {
     int c = count(0);
@@ -207,6 +227,10 @@ struct AttnWalk {
     return c;
   }
 };
+
+__device__ __forceinline__ long long divide(long long x, long long y) {   // x >= 0, y > 0
+  return ((x | y) >> 32) == 0 ? (unsigned)x / (unsigned)y : x / y;
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -237,30 +261,29 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
   const int box = min(page, S::kKeys);
   const int boxes = S::kKeys / box;              // pages of a tile
   const int my_page = lane / S::kBlocks, my_block = lane % S::kBlocks;
-  int it = 0, units = 0;
+  const uint32_t my_dst = ring + (my_block * S::kKeys + my_page * box) * 128;
+  int it = 0, rounds = 0;
   bool ok = true, bad = false;
 
-  auto tile = [&](const CUtensorMap* map, int j) -> bool {
+  // First row, in the cache, of the lane's box of key tile j; -1 if it has none.
+  auto box_row = [&](int j) -> int {
+    const int key = j * S::kKeys + my_page * box;
+    if (my_page >= boxes || key >= u.units.row.L) return -1;
+    const int id = a.block_table[(long long)u.b * a.max_pages + (key >> a.page_shift)];
+    const bool inside = id >= 0 && id < a.n_pages;
+    bad |= !inside;
+    // past the last row of the cache the box fills with zeros
+    return ((inside ? id * a.Hk + u.h : a.n_pages * a.Hk) << a.page_shift) + (key & (page - 1));
+  };
+  auto bring = [&](const CUtensorMap* map, int y) -> bool {
     const int stage = it % S::kStages, lap = it / S::kStages;
     if (lap > 0 && !mbar_wait(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word))
       return false;
     const uint32_t bar = smem_addr(&c->full[stage]);
-    const int key = j * S::kKeys + my_page * box;
-    const bool mine = my_page < boxes && key < u.row.L;
-    int y = 0;
-    if (mine) {
-      const int id = a.block_table[(long long)u.b * a.max_pages + (key >> a.page_shift)];
-      const bool inside = id >= 0 && id < a.n_pages;
-      bad |= !inside;
-      // past the last row of the cache the box fills with zeros
-      y = ((inside ? id * a.Hk + u.h : a.n_pages * a.Hk) << a.page_shift) + (key & (page - 1));
-    }
-    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    const unsigned who = __ballot_sync(0xffffffffu, y >= 0);
     if (lane == 0) mbar_arrive_expect(bar, __popc(who) * box * 128);
     __syncwarp();
-    if (mine)
-      tma_load_2d(ring + stage * S::kStageBytes + (my_block * S::kKeys + my_page * box) * 128, map,
-                  my_block * 64, y, bar);
+    if (y >= 0) tma_load_2d(my_dst + stage * S::kStageBytes, map, my_block * 64, y, bar);
     ++it;
     return true;
   };
@@ -268,9 +291,12 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
   do {
     const int n = u.most();
     if (n == 0) continue;
-    if (units > 0 && !(ok = mbar_wait(smem_addr(&c->q_empty), (units - 1) & 1, &c->abort_word)))
+    int y[S::kBufs + 1];   // tiles i .. i + kBufs
+#pragma unroll
+    for (int i = 0; i < S::kBufs; ++i) y[i] = box_row(u.j0 + i);
+    if (rounds > 0 && !(ok = mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1, &c->abort_word)))
       break;
-    ++units;
+    ++rounds;
     const uint32_t bar = smem_addr(&c->q_full);
     const int q_tile = lane / S::kBlocks;
     const bool mine = q_tile < S::kTiles && u.count(q_tile) > 0;
@@ -279,18 +305,24 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
     __syncwarp();
     if (mine)
       tma_load_3d(q_smem + q_tile * S::kQBytes + my_block * 128 * 128, q_map, my_block * 64,
-                  u.h * a.G, u.row.begin + u.first(q_tile), bar);
-    for (int i = 0; ok && i < min(n, S::kBufs); ++i) ok = tile(k_map, u.j0 + i);
+                  u.h * a.G, u.units.row.begin + u.first(q_tile), bar);
+#pragma unroll
+    for (int i = 0; i < S::kBufs; ++i)
+      if (ok && i < n) ok = bring(k_map, y[i]);
     for (int i = 0; ok && i < n; ++i) {
-      ok = tile(v_map, u.j0 + i);
-      if (ok && i + S::kBufs < n) ok = tile(k_map, u.j0 + i + S::kBufs);
+      const bool more = i + S::kBufs < n;
+      y[S::kBufs] = more ? box_row(u.j0 + i + S::kBufs) : -1;
+      ok = bring(v_map, y[0]);
+      if (ok && more) ok = bring(k_map, y[S::kBufs]);
+#pragma unroll
+      for (int x = 0; x < S::kBufs; ++x) y[x] = y[x + 1];
     }
   } while (ok && u.next());
   if (bad) set_flag(a.flags, kDevBadPage);
   if (!ok) {   // given up: the copies in flight still land in this CTA's memory
     for (int i = max(0, it - S::kStages); i < it; ++i)
       (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, nullptr);
-    if (units > 0) (void)mbar_poll(smem_addr(&c->q_full), (units - 1) & 1, nullptr);
+    if (rounds > 0) (void)mbar_poll(smem_addr(&c->q_full), (rounds - 1) & 1, nullptr);
   }
 }
 
@@ -317,7 +349,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   t = __shfl_sync(0xffffffffu, t, 0);
   const uint32_t s_base = tmem + t * S::kBufs * S::kKeys;
   const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
-  int it = 0, units = 0;
+  int it = 0, rounds = 0;
   int done = 0;   // tiles of S issued before this unit
   int turns = 0;
   bool ok = true;
@@ -361,8 +393,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   do {
     const int n = u.most(), cnt = u.count(t);
     if (n == 0) continue;
-    if (!(ok = mbar_wait(smem_addr(&c->q_full), units & 1, &c->abort_word))) break;
-    ++units;
+    if (!(ok = mbar_wait(smem_addr(&c->q_full), rounds++ & 1, &c->abort_word))) break;
     tc_fence_after();
     for (int i = 0; i < min(n, S::kBufs); ++i) {
       if (!(ok = wait_stage(it))) break;
@@ -376,12 +407,11 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       const int v_it = it++, k = done + i;
       const bool more = i + S::kBufs < n, active = i < cnt, next = i + S::kBufs < cnt;
       const int k_it = more ? it++ : 0;
-      // every wait comes before the products: the tensor core's queue is short
       if (!(ok = wait_stage(v_it))) break;
       if (active) {
         // values past the request's length must not reach the sums: 0 * NaN is NaN
         // (the other tile's warp writes the same zeros)
-        const int valid = u.row.L - (u.j0 + i) * S::kKeys;
+        const int valid = u.units.row.L - (u.j0 + i) * S::kKeys;
         if (valid < S::kKeys) {
           char* v0 = ring_ptr + (v_it % S::kStages) * S::kStageBytes;
           const int chunks = (S::kKeys - valid) * 8;
@@ -392,7 +422,9 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
           __syncwarp();
         }
       }
-      if (more && !(ok = wait_stage(k_it))) break;
+      // wide: every wait comes before the products, since the tensor core's queue
+      // is short; narrow: O += P V does not wait for keys that are still to come
+      if (S::kTiles > 1 && more && !(ok = wait_stage(k_it))) break;
       if (active && !(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
                                      &c->abort_word)))
         break;
@@ -406,6 +438,10 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       }
       // with one S buffer the next scores tell that O is up to date
       if (active && (S::kBufs > 1 || !next)) release(&c->pv_done[t], true);
+      if (S::kTiles == 1 && more) {
+        if (!(ok = wait_stage(k_it))) break;
+        tc_fence_after();
+      }
       if (next) scores(k + S::kBufs, k_it % S::kStages, true);
       else pass_turn();
       release(&c->empty[v_it % S::kStages], active);
@@ -445,6 +481,12 @@ __device__ __forceinline__ bool soft_meet(AttnControl* c, int phase) {
   return mbar_wait(smem_addr(&c->met), phase & 1, &c->abort_word);
 }
 
+__device__ __forceinline__ int take_ticket(int* ticket) {
+  int before;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+  return before;
+}
+
 template <typename E>
 __device__ __forceinline__ void store_row32(char* to, const float (&o)[32]) {
 #pragma unroll
@@ -455,18 +497,18 @@ __device__ __forceinline__ void store_row32(char* to, const float (&o)[32]) {
 }
 
 // Joins the partial sums of the unit's CTAs in their order.  A thread takes
-// four columns of a row, kItems of them at a time, so that the loads of all
-// their parts are in flight together.
-template <typename E, int kD, typename S>
+// four columns of a row, kItems of them at a time, and kAhead parts of each,
+// so that enough loads are in flight: many rows have few parts (a prompt's
+// unit that a range's end cuts), few rows many (a long context).
+template <typename E, int kD, typename S, int kItems, int kAhead>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& u, int c_first,
                                           int parts, bool begins_late) {
-  constexpr int kItems = 4, kCols = kD / 4;
+  constexpr int kCols = kD / 4;
   const size_t slots = (size_t)gridDim.x * 2;
   const float4* sums = (const float4*)a.partial;
   const float2* stats = (const float2*)(a.partial + slots * S::kRows * kD);
-  const int rows0 = max(0, u.last(0) - u.first(0)) * a.G;
-  const int rows1 = S::kTiles > 1 ? max(0, u.last(1) - u.first(1)) * a.G : 0;
-  const int items = (rows0 + rows1) * kCols;
+  const int rows0 = (u.last(0) - u.first(0)) * a.G;   // a second tile only where the first is full
+  const int items = u.rows() * kCols;
   for (int x0 = threadIdx.x; x0 < items; x0 += kItems * S::kSoftThreads) {
     int at[kItems];   // row of the slot
     float4 o[kItems];
@@ -479,7 +521,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
       m[i] = SV_NEG_INF;
       l[i] = 0.f;
     }
-#pragma unroll 2
+#pragma unroll kAhead
     for (int p = 0; p < parts; ++p) {
       const size_t slot = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows;
       float2 ml[kItems];
@@ -506,7 +548,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
     for (int i = 0; i < kItems; ++i) {
       if (x0 + i * S::kSoftThreads >= items) break;
       const int r = at[i] % 128;
-      const long long to = (long long)(u.row.begin + u.first(at[i] / 128) + r / a.G) * a.Hq +
+      const long long to = (long long)(u.units.row.begin + u.first(at[i] / 128) + r / a.G) * a.Hq +
                            u.h * a.G + r % a.G;
       const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
       *(uint2*)(a.out + (to * kD + x0 % kCols * 4) * 2) =
@@ -526,7 +568,7 @@ __device__ __forceinline__ void hand_over(uint64_t* bar) {
 
 template <typename E, int kD, typename S>
 __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
-                                             uint32_t tmem, long long quota) {
+                                             uint32_t tmem, long long quota, long long w1) {
   const int warp = threadIdx.x >> 5, t = warp / 4;
   const int r = threadIdx.x % 128;                 // the thread's row of its query tile
   const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
@@ -537,10 +579,10 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
   do {
     const int n = u.count(t);
     const int token = u.first(t) + r / a.G;
-    const bool mine = r < a.tile_tokens * a.G && token < u.row.n;
+    const bool mine = r < a.tile_tokens * a.G && token < u.units.row.n;
     const bool any = __any_sync(0xffffffffu, mine);
     // keys that the row sees; rows without a token see none
-    const int seen = mine ? max(0, u.row.L - u.row.n + token + 1) : 0;
+    const int seen = mine ? max(0, u.units.row.L - u.units.row.n + token + 1) : 0;
     // the warp's first row sees the fewest of those with a token
     const int fewest = __shfl_sync(0xffffffffu, seen, 0);
     float m = SV_NEG_INF, l = 0.f;
@@ -643,7 +685,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     if (whole) {
       if (any) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const long long to = (long long)(u.row.begin + token) * a.Hq + u.h * a.G + r % a.G;
+        const long long to = (long long)(u.units.row.begin + token) * a.Hq + u.h * a.G + r % a.G;
 #pragma unroll 1
         for (int x = 0; x < kD; x += 32) {
           uint32_t bits[32] = {};
@@ -663,11 +705,13 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       continue;
     }
     // a part of the unit: unnormalised sums to the workspace
-    const int c_first = (int)(u.unit_begin / quota);
-    const int c_last = (int)((u.unit_begin + u.tiles - 1) / quota);
-    const bool begins_late = u.unit_begin != (long long)c_first * quota;
+    const int cta = blockIdx.x;
+    const long long begins = w1 - u.left - u.j0, w0 = cta * quota;   // the unit's first tile, ours
+    const int c_first = begins >= w0 ? cta : (int)divide(begins, quota);
+    const int c_last = u.j1 == u.tiles ? cta : (int)divide(begins + u.tiles - 1, quota);
+    const bool begins_late = begins != c_first * quota;
     const size_t slots = (size_t)gridDim.x * 2;
-    const size_t slot = (size_t)blockIdx.x * 2 + ((int)blockIdx.x == c_first && begins_late ? 1 : 0);
+    const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
     if (any) {
       float* to = a.partial + (slot * S::kRows + t * 128 + r) * kD;
 #pragma unroll 1
@@ -688,17 +732,22 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
             make_float2(m, l);
     }
     tc_fence_before();
-    __threadfence();
+    // what all warps wrote is released by one thread's ticket, and what other
+    // CTAs wrote is acquired by it
     if (!(ok = soft_meet(c, meetings++))) break;
     if (threadIdx.x == 0) {
-      const int before = atomicAdd(&a.tickets[c_first], 1);
-      const bool last = before == c_last - c_first;
+      const bool last = take_ticket(&a.tickets[c_first]) == c_last - c_first;
       if (last) a.tickets[c_first] = 0;
-      __threadfence();
       c->last = last;
     }
     if (!(ok = soft_meet(c, meetings++))) break;
-    if (c->last) attn_join<E, kD, S>(a, u, c_first, c_last - c_first + 1, begins_late);
+    if (c->last) {
+      const int parts = c_last - c_first + 1;
+      if (u.rows() * (kD / 4) <= S::kSoftThreads)
+        attn_join<E, kD, S, 1, 8>(a, u, c_first, parts, begins_late);
+      else
+        attn_join<E, kD, S, 4, 2>(a, u, c_first, parts, begins_late);
+    }
   } while (u.next());
 }
 
@@ -736,7 +785,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     }
     mbar_init_fence();
     c->abort_word = 0;
-    c->start_row = -1;
     tma_prefetch_map(&q_map);
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
@@ -749,11 +797,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   const int per = (a.B + S::kThreads - 1) / S::kThreads;
   const int r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
   auto weight = [&](int b, bool* bad) -> long long {
-    const AttnRow row = attn_row(a, b, bad);
-    const int units = units_of<S>(a, row);
-    long long sum = 0;
-    for (int m = 0; m < units; ++m) sum += unit_tiles<S>(a, row, m);
-    return sum * a.Hk;
+    const AttnUnits<S> units(a, attn_row(a, b, bad));
+    return units.before(units.count) * a.Hk;
   };
   bool bad = false;
   long long mine = 0;
@@ -775,7 +820,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     if (w < warp) before += c->sums[w];
     total += c->sums[w];
   }
-  const long long quota = max(1ll, (total + gridDim.x - 1) / gridDim.x);
+  const long long quota = max(1ll, divide(total + gridDim.x - 1, gridDim.x));
   const long long w0 = blockIdx.x * quota, w1 = min(total, w0 + quota);
   long long begin = before + inc - mine;
   if (w0 < w1 && begin <= w0 && w0 < begin + mine) {   // one thread: the range starts in its rows
@@ -785,14 +830,27 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
       if (w0 < begin + wb) break;
       begin += wb;
     }
-    c->start_row = b;
-    c->start_off = w0 - begin;
+    const AttnUnits<S> units(a, attn_row(a, b));
+    long long off = w0 - begin;
+    const long long head = units.before(units.count);
+    c->start.row = units.row;
+    c->start.b = b;
+    c->start.h = (int)divide(off, head);
+    off -= c->start.h * head;
+    int lo = 0, hi = units.count - 1;   // the last unit that starts at or before off
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (units.before(mid) <= off) lo = mid;
+      else hi = mid - 1;
+    }
+    c->start.m = lo;
+    c->start.j0 = (int)(off - units.before(lo));
   }
   __syncthreads();
   const uint32_t tmem = c->tmem;
 
   if (w0 < w1) {
-    const AttnWalk<S> u(a, c->start_row, c->start_off, w0, w1);
+    const AttnWalk<S> u(a, c->start, (int)(w1 - w0));
     // wide: three warpgroups launched with 168 registers a thread; 2 x 208 + 88 = 3 x 168
     if (warp >= kLoader) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -801,7 +859,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
         attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem, warp - kIssuer);
     } else {
       if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-      attn_softmax<E, kD, S>(a, u, c, tmem, quota);
+      attn_softmax<E, kD, S>(a, u, c, tmem, quota, w1);
     }
   }
   // tokens past the last request's
