@@ -68,7 +68,8 @@ struct AttnShape {
   static constexpr int kBlocks = kD / 64;            // 128-byte column blocks of a row
   static constexpr int kQBytes = 128 * kD * 2;
   static constexpr int kStageBytes = kKeys * kD * 2;
-  static constexpr int kStages = kD == 128 ? 5 : 8;  // what is left of the shared memory
+  static constexpr int kStages = kD == 128 ? 4 : 8;  // what is left of the shared memory
+  static constexpr int kStagingBytes = 32 * 128;     // of a warp: rows on their way out
   static constexpr int kSoftThreads = 128 * kTiles;
   // wide: whole warpgroups, so that the softmax can take registers from the rest
   static constexpr int kThreads = kSoftThreads + (kWide ? 128 : 64);
@@ -76,7 +77,8 @@ struct AttnShape {
   static constexpr int kTmemCols = kWide ? 512 : 256;
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kControlBytes = 512;
-  static constexpr int kSmemBytes = kTiles * kQBytes + kStages * kStageBytes + kControlBytes;
+  static constexpr int kSmemBytes =
+      kTiles * (kQBytes + 4 * kStagingBytes) + kStages * kStageBytes + kControlBytes;
 };
 
 // A request's lengths, clamped to what its arrays hold; n == 0: nothing to do.
@@ -95,28 +97,9 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, int b, bool* bad 
   if (bad && (!sound || r.L != len)) *bad = true;
   return r;
 }
-// sum of floor((a i + b) / m) for i in [0, n), by the Euclidean algorithm on
-// (a, m).  n a + b stays below 2^32.
-__device__ __forceinline__ long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  long long sum = 0;
-  while (n > 0) {
-    sum += (long long)n * (n - 1) / 2 * (a / m) + (long long)n * (b / m);
-    a %= m;
-    b %= m;
-    const unsigned top = a * n + b;
-    if (top < m) break;
-    n = top / m;
-    b = top % m;
-    const unsigned swap = m;
-    m = a;
-    a = swap;
-  }
-  return sum;
-}
-
 // The query units of a request: kTiles tiles of tile_tokens tokens each.  A
-// unit's weight is the number of key tiles that its last token sees, one for
-// a unit that sees no key.
+// unit's weight is the number of keys that its last token sees, or one key
+// tile where that is more, so that weights sum in closed form.
 template <typename S>
 struct AttnUnits {
   AttnRow row;
@@ -126,28 +109,27 @@ struct AttnUnits {
   __device__ __forceinline__ AttnUnits() {}
   __device__ __forceinline__ AttnUnits(const AttnArgs& a, const AttnRow& r)
       : row(r), step(S::kTiles * a.tile_tokens), count((r.n + step - 1) / step) {}
-  // key tiles that the request's tokens up to t1 see
-  __device__ __forceinline__ int seen(int t1) const {
-    return (max(0, row.L - row.n + t1) + S::kKeys - 1) / S::kKeys;
-  }
-  __device__ __forceinline__ int tiles(int m) const {
-    return max(1, seen(min(row.n, (m + 1) * step)));
+  // keys that the request's tokens up to t1 see
+  __device__ __forceinline__ int seen(int t1) const { return max(0, row.L - row.n + t1); }
+  __device__ __forceinline__ int weight(int m) const {
+    return max(S::kKeys, seen(min(row.n, (m + 1) * step)));
   }
   // weight of the first `units` units
   __device__ __forceinline__ long long before(int units) const {
-    if (units == 0) return 0;
-    const int full = units == count ? units - 1 : units;   // the last may be short
+    const int full = min(units, count - 1);   // the last may be short
     const int context = row.L - row.n;
-    const int blind = context < 0 ? min(full, -context / step) : 0;
-    return blind + (units - full) * (long long)tiles(count - 1) +
-           floor_sum(full - blind, S::kKeys, step, context + (blind + 1) * step + S::kKeys - 1);
+    // units of less than a key tile
+    const int few = context < S::kKeys ? min(full, (S::kKeys - 1 - context) / step) : 0;
+    const long long i0 = few + 1, i1 = full;
+    return (long long)few * S::kKeys + (i1 - few) * context + (i1 - few) * (i0 + i1) / 2 * step +
+           (units > full ? weight(count - 1) : 0);
   }
 };
 
-// Where a CTA's range starts.
+// Where a CTA's range starts: `pos` keys into a unit.
 struct AttnStart {
   AttnRow row;
-  int b, h, m, j0;
+  int b, h, m, pos;
 };
 
 struct AttnControl {   // at the end of the shared memory
@@ -157,6 +139,7 @@ struct AttnControl {   // at the end of the shared memory
   uint64_t pv_done[2], turn[2];
   uint32_t tmem;
   int abort_word;
+  int calm;                   // an abort word that stays 0, for the waits of a CTA that gives up
   int last;
   AttnStart start;
   long long sums[12];
@@ -164,43 +147,53 @@ struct AttnControl {   // at the end of the shared memory
 
 static_assert(sizeof(AttnControl) <= 512, "fits kControlBytes");
 
-// A CTA's walk over its range of the work; every warp keeps its own.
+// A CTA's walk over its range of the work; every warp keeps its own.  A key
+// tile is the CTA's whose range holds the tile's first key.
 template <typename S>
 struct AttnWalk {
   const AttnArgs& a;
   AttnUnits<S> units;
   int b, h, m;
+  int pos;                    // where the range enters the unit
   int j0, j1;                 // key tiles of the unit that are this CTA's
   int tiles;                  // all key tiles of the unit
-  int left;                   // of the range, this unit's included
+  long long left;             // of the range, this unit's part included
 
-  __device__ __forceinline__ AttnWalk(const AttnArgs& args, const AttnStart& s, int length)
-      : a(args), units(args, s.row), b(s.b), h(s.h), m(s.m), j0(s.j0), left(length) {
-    tiles = units.tiles(m);
-    j1 = min(tiles, j0 + left);
-  }
-  // The next unit; false at the end of the range.
-  __device__ __forceinline__ bool next() {
-    left -= j1 - j0;
-    if (left <= 0) return false;
-    if (++m == units.count) {
-      m = 0;
-      if (++h == a.Hk) {
-        h = 0;
-        next_row();
+  __device__ __forceinline__ AttnWalk(const AttnArgs& args, const AttnStart& s, long long length)
+      : a(args), units(args, s.row), b(s.b), h(s.h), m(s.m), pos(s.pos), left(length) {}
+  // To the next unit of which the CTA has a tile, first of all to the first;
+  // false at the end of the range.
+  __device__ __forceinline__ bool next(bool first_of_all) {
+#pragma unroll 1
+    while (true) {
+      if (!first_of_all) {
+        left -= units.weight(m) - pos;
+        if (left <= 0) return false;
+        pos = 0;
+        if (++m == units.count) {
+          m = 0;
+          if (++h == a.Hk) {
+            h = 0;
+            next_row();
+          }
+        }
       }
+      first_of_all = false;
+      const int weight = units.weight(m);
+      tiles = (weight + S::kKeys - 1) / S::kKeys;
+      j0 = (pos + S::kKeys - 1) / S::kKeys;
+      j1 = left >= weight - pos ? tiles : (pos + (int)left + S::kKeys - 1) / S::kKeys;
+      if (j0 < j1) return true;
     }
-    tiles = units.tiles(m);
-    j0 = 0;
-    j1 = min(tiles, left);
-    return true;
   }
   // The next request with tokens (there is one: the range has not ended).
   __device__ __forceinline__ void next_row() {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
     for (++b; b < a.B; b += 32) {
       const int mine = b + lane;
-      const unsigned some = __ballot_sync(0xffffffffu, mine < a.B && attn_row(a, mine).n > 0);
+      const unsigned some =
+          __ballot_sync(0xffffffffu, mine < a.B && attn_row(a, min(mine, a.B - 1)).n > 0);
       if (some) {
         b += __ffs(some) - 1;
         break;
@@ -216,10 +209,10 @@ struct AttnWalk {
   }
   __device__ __forceinline__ int count(int t) const {
     if (first(t) >= units.row.n) return 0;
-    return max(0, min(j1, units.seen(last(t))) - j0);
+    return max(0, min(j1, (units.seen(last(t)) + S::kKeys - 1) / S::kKeys) - j0);
   }
   __device__ __forceinline__ int rows() const {   // query rows of the unit
-    return (last(S::kTiles - 1 > 0 && first(1) < units.row.n ? 1 : 0) - first(0)) * a.G;
+    return (last(S::kTiles > 1 && first(1) < units.row.n ? 1 : 0) - first(0)) * a.G;
   }
   __device__ __forceinline__ int most() const {
     int c = count(0);
@@ -227,10 +220,6 @@ struct AttnWalk {
     return c;
   }
 };
-
-__device__ __forceinline__ long long divide(long long x, long long y) {   // x >= 0, y > 0
-  return ((x | y) >> 32) == 0 ? (unsigned)x / (unsigned)y : x / y;
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -288,13 +277,18 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
     return true;
   };
 
-  do {
+#pragma unroll 1
+  for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.most();
     if (n == 0) continue;
     int y[S::kBufs + 1];   // tiles i .. i + kBufs
 #pragma unroll
     for (int i = 0; i < S::kBufs; ++i) y[i] = box_row(u.j0 + i);
-    if (rounds > 0 && !(ok = mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1, &c->abort_word)))
+#pragma unroll
+    for (int i = 0; i < S::kBufs; ++i)
+      if (ok && i < n) ok = bring(k_map, y[i]);
+    if (!ok || (rounds > 0 && !(ok = mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1,
+                                               &c->abort_word))))
       break;
     ++rounds;
     const uint32_t bar = smem_addr(&c->q_full);
@@ -306,23 +300,22 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
     if (mine)
       tma_load_3d(q_smem + q_tile * S::kQBytes + my_block * 128 * 128, q_map, my_block * 64,
                   u.h * a.G, u.units.row.begin + u.first(q_tile), bar);
-#pragma unroll
-    for (int i = 0; i < S::kBufs; ++i)
-      if (ok && i < n) ok = bring(k_map, y[i]);
+#pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
-      const bool more = i + S::kBufs < n;
-      y[S::kBufs] = more ? box_row(u.j0 + i + S::kBufs) : -1;
+      const bool another = i + S::kBufs < n;
+      y[S::kBufs] = another ? box_row(u.j0 + i + S::kBufs) : -1;
       ok = bring(v_map, y[0]);
-      if (ok && more) ok = bring(k_map, y[S::kBufs]);
+      if (ok && another) ok = bring(k_map, y[S::kBufs]);
 #pragma unroll
       for (int x = 0; x < S::kBufs; ++x) y[x] = y[x + 1];
     }
-  } while (ok && u.next());
+  }
   if (bad) set_flag(a.flags, kDevBadPage);
   if (!ok) {   // given up: the copies in flight still land in this CTA's memory
+#pragma unroll 1
     for (int i = max(0, it - S::kStages); i < it; ++i)
-      (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, nullptr);
-    if (rounds > 0) (void)mbar_poll(smem_addr(&c->q_full), (rounds - 1) & 1, nullptr);
+      (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->calm);
+    if (rounds > 0) (void)mbar_poll(smem_addr(&c->q_full), (rounds - 1) & 1, &c->calm);
   }
 }
 
@@ -390,11 +383,13 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
     else if (lane == 0) mbar_arrive(smem_addr(bar));
   };
 
-  do {
+#pragma unroll 1
+  for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.most(), cnt = u.count(t);
     if (n == 0) continue;
     if (!(ok = mbar_wait(smem_addr(&c->q_full), rounds++ & 1, &c->abort_word))) break;
     tc_fence_after();
+#pragma unroll 1
     for (int i = 0; i < min(n, S::kBufs); ++i) {
       if (!(ok = wait_stage(it))) break;
       tc_fence_after();
@@ -403,10 +398,11 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       ++it;
     }
     if (ok && cnt <= S::kBufs) release(&c->q_empty, cnt > 0);
+#pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
       const int v_it = it++, k = done + i;
-      const bool more = i + S::kBufs < n, active = i < cnt, next = i + S::kBufs < cnt;
-      const int k_it = more ? it++ : 0;
+      const bool another = i + S::kBufs < n, active = i < cnt, next = i + S::kBufs < cnt;
+      const int k_it = another ? it++ : 0;
       if (!(ok = wait_stage(v_it))) break;
       if (active) {
         // values past the request's length must not reach the sums: 0 * NaN is NaN
@@ -415,6 +411,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
         if (valid < S::kKeys) {
           char* v0 = ring_ptr + (v_it % S::kStages) * S::kStageBytes;
           const int chunks = (S::kKeys - valid) * 8;
+#pragma unroll 1
           for (int x = lane; x < chunks * S::kBlocks; x += 32)
             *(uint4*)(v0 + ((x / chunks) * S::kKeys + valid) * 128 + (x % chunks) * 16) =
                 make_uint4(0, 0, 0, 0);
@@ -424,7 +421,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       }
       // wide: every wait comes before the products, since the tensor core's queue
       // is short; narrow: O += P V does not wait for keys that are still to come
-      if (S::kTiles > 1 && more && !(ok = wait_stage(k_it))) break;
+      if (S::kTiles > 1 && another && !(ok = wait_stage(k_it))) break;
       if (active && !(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
                                      &c->abort_word)))
         break;
@@ -438,23 +435,21 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       }
       // with one S buffer the next scores tell that O is up to date
       if (active && (S::kBufs > 1 || !next)) release(&c->pv_done[t], true);
-      if (S::kTiles == 1 && more) {
+      if (S::kTiles == 1 && another) {
         if (!(ok = wait_stage(k_it))) break;
         tc_fence_after();
       }
       if (next) scores(k + S::kBufs, k_it % S::kStages, true);
       else pass_turn();
       release(&c->empty[v_it % S::kStages], active);
-      if (more) {
-        release(&c->empty[k_it % S::kStages], next);
-        if (i + S::kBufs + 1 == cnt) release(&c->q_empty, true);
-      }
+      if (another) release(&c->empty[k_it % S::kStages], next);
+      if (next && i + S::kBufs + 1 == cnt) release(&c->q_empty, true);
     }
     done += cnt;
-  } while (ok && u.next());
+  }
   // everything issued is done before the CTA's memory goes
   release(&c->drain, true);
-  (void)mbar_poll(smem_addr(&c->drain), 0, nullptr);
+  (void)mbar_poll(smem_addr(&c->drain), 0, &c->calm);
   __syncwarp();
 }
 
@@ -487,13 +482,26 @@ __device__ __forceinline__ int take_ticket(int* ticket) {
   return before;
 }
 
-template <typename E>
-__device__ __forceinline__ void store_row32(char* to, const float (&o)[32]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *(uint4*)(to + i * 16) =
-        make_uint4(pack2(o[8 * i], o[8 * i + 1], E()), pack2(o[8 * i + 2], o[8 * i + 3], E()),
-                   pack2(o[8 * i + 4], o[8 * i + 5], E()), pack2(o[8 * i + 6], o[8 * i + 7], E()));
+// 128 bytes of each of a warp's 32 rows, a row per lane, to global memory with
+// four whole segments per instruction: they pass through shared memory, their
+// 16-byte pieces placed so that neither side meets bank conflicts.  `to` is
+// the lane's segment, nullptr for none.
+__device__ __forceinline__ void stage_piece(char* stage, int piece, uint32_t x, uint32_t y,
+                                            uint32_t z, uint32_t w) {
+  const int lane = threadIdx.x & 31;
+  *(uint4*)(stage + lane * 128 + (piece ^ (lane & 7)) * 16) = make_uint4(x, y, z, w);
+}
+__device__ __forceinline__ void store_staged(const char* stage, char* to) {
+  const int lane = threadIdx.x & 31, piece = lane % 8;
+  __syncwarp();
+#pragma unroll 2
+  for (int i = 0; i < 8; ++i) {
+    const int row = i * 4 + lane / 8;
+    char* dst = (char*)__shfl_sync(0xffffffffu, (unsigned long long)to, row);
+    if (dst)
+      *(uint4*)(dst + piece * 16) = *(const uint4*)(stage + row * 128 + (piece ^ (row & 7)) * 16);
+  }
+  __syncwarp();
 }
 
 // Joins the partial sums of the unit's CTAs in their order.  A thread takes
@@ -509,6 +517,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
   const float2* stats = (const float2*)(a.partial + slots * S::kRows * kD);
   const int rows0 = (u.last(0) - u.first(0)) * a.G;   // a second tile only where the first is full
   const int items = u.rows() * kCols;
+#pragma unroll 1
   for (int x0 = threadIdx.x; x0 < items; x0 += kItems * S::kSoftThreads) {
     int at[kItems];   // row of the slot
     float4 o[kItems];
@@ -521,28 +530,36 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
       m[i] = SV_NEG_INF;
       l[i] = 0.f;
     }
-#pragma unroll kAhead
-    for (int p = 0; p < parts; ++p) {
-      const size_t slot = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows;
-      float2 ml[kItems];
-      float4 f[kItems];
+#pragma unroll 1
+    for (int p0 = 0; p0 < parts; p0 += kAhead) {
+      float2 ml[kAhead][kItems];
+      float4 f[kAhead][kItems];
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        ml[i] = __ldcg(&stats[slot + at[i]]);
-        f[i] = __ldcg(&sums[(slot + at[i]) * kCols + x0 % kCols]);
+      for (int q = 0; q < kAhead; ++q) {
+        const int p = min(p0 + q, parts - 1);
+        const size_t slot = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows;
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          ml[q][i] = __ldcg(&stats[slot + at[i]]);
+          f[q][i] = __ldcg(&sums[(slot + at[i]) * kCols + x0 % kCols]);
+          if (p0 + q >= parts) ml[q][i].x = SV_NEG_INF;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kItems; ++i) {
-        if (ml[i].x == SV_NEG_INF) continue;   // the part sees none of the row's keys
-        const float top = fmaxf(m[i], ml[i].x);
-        const float c0 = ex2_approx(m[i] - top), c1 = ex2_approx(ml[i].x - top);
-        m[i] = top;
-        l[i] = l[i] * c0 + ml[i].y * c1;
-        o[i].x = o[i].x * c0 + f[i].x * c1;
-        o[i].y = o[i].y * c0 + f[i].y * c1;
-        o[i].z = o[i].z * c0 + f[i].z * c1;
-        o[i].w = o[i].w * c0 + f[i].w * c1;
-      }
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int i = 0; i < kItems; ++i) {
+          // a part that sees none of the row's keys has -inf and zeros
+          const float2 e = ml[q][i];
+          const float top = fmaxf(m[i], e.x), ref = top == SV_NEG_INF ? 0.f : top;
+          const float c0 = ex2_approx(m[i] - ref), c1 = ex2_approx(e.x - ref);
+          m[i] = top;
+          l[i] = l[i] * c0 + e.y * c1;
+          o[i].x = o[i].x * c0 + f[q][i].x * c1;
+          o[i].y = o[i].y * c0 + f[q][i].y * c1;
+          o[i].z = o[i].z * c0 + f[q][i].z * c1;
+          o[i].w = o[i].w * c0 + f[q][i].w * c1;
+        }
     }
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
@@ -568,15 +585,18 @@ __device__ __forceinline__ void hand_over(uint64_t* bar) {
 
 template <typename E, int kD, typename S>
 __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
-                                             uint32_t tmem, long long quota, long long w1) {
+                                             uint32_t tmem, char* staging, long long quota,
+                                             long long w1) {
   const int warp = threadIdx.x >> 5, t = warp / 4;
   const int r = threadIdx.x % 128;                 // the thread's row of its query tile
   const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
   const uint32_t o_col = tmem + lanes + S::kTiles * S::kBufs * S::kKeys + t * kD;
+  char* stage = staging + warp * S::kStagingBytes;
   int done = 0;                                    // tiles of S taken before this unit
   int meetings = 0, rounds = 0;
   bool ok = true;
-  do {
+#pragma unroll 1
+  for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.count(t);
     const int token = u.first(t) + r / a.G;
     const bool mine = r < a.tile_tokens * a.G && token < u.units.row.n;
@@ -586,6 +606,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     // the warp's first row sees the fewest of those with a token
     const int fewest = __shfl_sync(0xffffffffu, seen, 0);
     float m = SV_NEG_INF, l = 0.f;
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int k = done + i, buf = k % S::kBufs;
       if (!(ok = mbar_wait(smem_addr(&c->s_full[t][buf]), (k / S::kBufs) & 1, &c->abort_word)))
@@ -614,6 +635,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           if (mine) m = high;
         }
         float sum;
+#pragma unroll 1
         while (true) {
           const float ref = m == SV_NEG_INF ? 0.f : m;
           const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
@@ -681,39 +703,23 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
                      &c->abort_word);
     if (!ok) break;
     tc_fence_after();
+    // A unit that is all this CTA's is written out; a part of one goes to the
+    // workspace as it is, to one of two places: a range has at most one part at
+    // its start and one at its end.
     const bool whole = u.j0 == 0 && u.j1 == u.tiles;
-    if (whole) {
-      if (any) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const long long to = (long long)(u.units.row.begin + token) * a.Hq + u.h * a.G + r % a.G;
-#pragma unroll 1
-        for (int x = 0; x < kD; x += 32) {
-          uint32_t bits[32] = {};
-          if (n > 0) {
-            tmem_load32(o_col + x, bits);
-            tmem_wait_load();
-            tmem_pin<32>(bits);
-          }
-          float o[32];
-#pragma unroll
-          for (int y = 0; y < 32; ++y) o[y] = l > 0.f ? __uint_as_float(bits[y]) * inv : 0.f;
-          if (mine) store_row32<E>(a.out + (to * kD + x) * 2, o);
-        }
-        if (mine && a.lse) a.lse[to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
-      }
-      tc_fence_before();
-      continue;
-    }
-    // a part of the unit: unnormalised sums to the workspace
     const int cta = blockIdx.x;
-    const long long begins = w1 - u.left - u.j0, w0 = cta * quota;   // the unit's first tile, ours
-    const int c_first = begins >= w0 ? cta : (int)divide(begins, quota);
-    const int c_last = u.j1 == u.tiles ? cta : (int)divide(begins + u.tiles - 1, quota);
-    const bool begins_late = begins != c_first * quota;
+    // from the start of this range to the unit's, in keys; the unit's first CTA
+    const long long ahead = w1 - u.left - u.pos - cta * quota;
+    const int c_first =
+        u.pos == 0 ? cta : cta - (quota >= u.pos ? 1 : (u.pos + (int)quota - 1) / (int)quota);
+    const bool begins_late = ahead + (cta - c_first) * quota != 0;   // after its range's start
     const size_t slots = (size_t)gridDim.x * 2;
     const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
     if (any) {
-      float* to = a.partial + (slot * S::kRows + t * 128 + r) * kD;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const long long to = (long long)(u.units.row.begin + token) * a.Hq + u.h * a.G + r % a.G;
+      const size_t part = slot * S::kRows + t * 128 + r;
+      char* dst = whole ? a.out + to * kD * 2 : (char*)(a.partial + part * kD);
 #pragma unroll 1
       for (int x = 0; x < kD; x += 32) {
         uint32_t bits[32] = {};
@@ -722,16 +728,37 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           tmem_wait_load();
           tmem_pin<32>(bits);
         }
-        if (mine)
+        if (whole) {   // 64 columns make a segment
+          uint32_t p[16];
 #pragma unroll
-          for (int y = 0; y < 32; y += 4)
-            *(uint4*)(to + x + y) = make_uint4(bits[y], bits[y + 1], bits[y + 2], bits[y + 3]);
+          for (int y = 0; y < 16; ++y)
+            p[y] = l > 0.f ? pack2(__uint_as_float(bits[2 * y]) * inv,
+                                   __uint_as_float(bits[2 * y + 1]) * inv, E())
+                           : 0u;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            stage_piece(stage, x / 8 % 8 + y, p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
+          if (x % 64 == 0) continue;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            stage_piece(stage, y, bits[4 * y], bits[4 * y + 1], bits[4 * y + 2], bits[4 * y + 3]);
+        }
+        store_staged(stage, mine ? dst : nullptr);
+        dst += 128;
       }
-      if (mine)
-        ((float2*)(a.partial + slots * S::kRows * kD))[slot * S::kRows + t * 128 + r] =
-            make_float2(m, l);
+      if (mine) {
+        if (!whole) ((float2*)(a.partial + slots * S::kRows * kD))[part] = make_float2(m, l);
+        else if (a.lse) a.lse[to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
+      }
     }
     tc_fence_before();
+    if (whole) continue;
+    // the CTA that has the unit's last tile
+    const long long end = ahead + (long long)(u.tiles - 1) * S::kKeys;
+    const int c_last =
+        u.j1 == u.tiles ? cta
+        : cta + (int)(end >> 32 == 0 ? (unsigned)end / (unsigned)quota : end / quota);
     // what all warps wrote is released by one thread's ticket, and what other
     // CTAs wrote is acquired by it
     if (!(ok = soft_meet(c, meetings++))) break;
@@ -748,7 +775,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       else
         attn_join<E, kD, S, 4, 2>(a, u, c_first, parts, begins_late);
     }
-  } while (u.next());
+  }
 }
 
 template <typename E, int kD, bool kWide>
@@ -760,13 +787,15 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   using S = AttnShape<kD, kWide>;
   extern __shared__ __align__(1024) char smem[];
   char* ring_ptr = smem + S::kTiles * S::kQBytes;
-  AttnControl* c = (AttnControl*)(ring_ptr + S::kStages * S::kStageBytes);
+  char* staging = ring_ptr + S::kStages * S::kStageBytes;
+  AttnControl* c = (AttnControl*)(staging + S::kTiles * 4 * S::kStagingBytes);
   const uint32_t q_smem = smem_addr(smem), ring = smem_addr(ring_ptr);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kLoader = S::kSoftThreads / 32, kIssuer = kLoader + 1;
 
   // -------- set-up that reads nothing of the caller's
   if (warp == kLoader && lane == 0) {
+#pragma unroll 1
     for (int i = 0; i < S::kStages; ++i) {
       mbar_init(smem_addr(&c->full[i]), 1);
       mbar_init(smem_addr(&c->empty[i]), S::kTiles);
@@ -775,6 +804,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     mbar_init(smem_addr(&c->q_empty), S::kTiles);
     mbar_init(smem_addr(&c->drain), S::kTiles);
     mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
+#pragma unroll 1
     for (int t = 0; t < S::kTiles; ++t) {
       for (int k = 0; k < S::kBufs; ++k) {
         mbar_init(smem_addr(&c->s_full[t][k]), 1);
@@ -784,7 +814,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
       mbar_init(smem_addr(&c->turn[t]), 1);
     }
     mbar_init_fence();
-    c->abort_word = 0;
+    c->abort_word = c->calm = 0;
     tma_prefetch_map(&q_map);
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
@@ -802,6 +832,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   };
   bool bad = false;
   long long mine = 0;
+#pragma unroll 1
   for (int b = r0; b < r1; ++b) mine += weight(b, &bad);
   if (bad && blockIdx.x == 0) set_flag(a.flags, kDevLength);
   long long inc = mine;
@@ -815,42 +846,64 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   __syncthreads();
   tc_fence_after();
   long long before = 0, total = 0;
-#pragma unroll
+#pragma unroll 1
   for (int w = 0; w < S::kThreads / 32; ++w) {
     if (w < warp) before += c->sums[w];
     total += c->sums[w];
   }
-  const long long quota = max(1ll, divide(total + gridDim.x - 1, gridDim.x));
-  const long long w0 = blockIdx.x * quota, w1 = min(total, w0 + quota);
+  const unsigned ctas = gridDim.x;
+  const long long quota = max((long long)S::kKeys, total >> 32 == 0
+                                                       ? (long long)(((unsigned)total + ctas - 1) / ctas)
+                                                       : (total + ctas - 1) / ctas);
+  const long long w0 = (long long)blockIdx.x * quota, w1 = min(total, w0 + quota);
   long long begin = before + inc - mine;
-  if (w0 < w1 && begin <= w0 && w0 < begin + mine) {   // one thread: the range starts in its rows
+  // One thread's rows hold the start of the range; its warp finds the place.
+  const unsigned holds = __ballot_sync(0xffffffffu, w0 < w1 && begin <= w0 && w0 < begin + mine);
+  if (holds) {
     int b = r0;
-    for (;; ++b) {
-      const long long wb = weight(b, nullptr);
-      if (w0 < begin + wb) break;
-      begin += wb;
+    if (per > 1 && (holds >> lane & 1)) {
+#pragma unroll 1
+      for (;; ++b) {
+        const long long wb = weight(b, nullptr);
+        if (w0 < begin + wb) break;
+        begin += wb;
+      }
     }
+    const int from = __ffs(holds) - 1;
+    b = __shfl_sync(0xffffffffu, b, from);
+    long long off = w0 - __shfl_sync(0xffffffffu, begin, from);
     const AttnUnits<S> units(a, attn_row(a, b));
-    long long off = w0 - begin;
     const long long head = units.before(units.count);
-    c->start.row = units.row;
-    c->start.b = b;
-    c->start.h = (int)divide(off, head);
-    off -= c->start.h * head;
-    int lo = 0, hi = units.count - 1;   // the last unit that starts at or before off
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (units.before(mid) <= off) lo = mid;
-      else hi = mid - 1;
+    int h = min(a.Hk - 1, (int)((float)off / (float)head));
+#pragma unroll 1
+    while (h * head > off) --h;
+#pragma unroll 1
+    while ((h + 1) * head <= off) ++h;
+    off -= h * head;
+    // the last unit that starts at or before off, 32 candidates at a time
+    int lo = 0, span = units.count;
+#pragma unroll 1
+    while (span > 1) {
+      const int step = (span + 31) / 32, at = lo + lane * step;
+      const unsigned under =
+          __ballot_sync(0xffffffffu, at < lo + span && units.before(at) <= off);
+      const int last = 31 - __clz(under);   // lane 0 is always under
+      span = min(step, span - last * step);
+      lo += last * step;
     }
-    c->start.m = lo;
-    c->start.j0 = (int)(off - units.before(lo));
+    if (lane == 0) {
+      c->start.row = units.row;
+      c->start.b = b;
+      c->start.h = h;
+      c->start.m = lo;
+      c->start.pos = (int)(off - units.before(lo));
+    }
   }
   __syncthreads();
   const uint32_t tmem = c->tmem;
 
   if (w0 < w1) {
-    const AttnWalk<S> u(a, c->start, (int)(w1 - w0));
+    const AttnWalk<S> u(a, c->start, w1 - w0);
     // wide: three warpgroups launched with 168 registers a thread; 2 x 208 + 88 = 3 x 168
     if (warp >= kLoader) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -859,7 +912,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
         attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem, warp - kIssuer);
     } else {
       if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-      attn_softmax<E, kD, S>(a, u, c, tmem, quota, w1);
+      attn_softmax<E, kD, S>(a, u, c, tmem, staging, quota, w1);
     }
   }
   // tokens past the last request's
@@ -867,10 +920,12 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   const long long spare = (long long)(a.T - used) * a.Hq;
   if (spare > 0) {
     const long long first = (long long)used * a.Hq;
+#pragma unroll 1
     for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < spare * (kD / 8);
          x += (long long)gridDim.x * blockDim.x)
       ((uint4*)a.out)[first * (kD / 8) + x] = make_uint4(0, 0, 0, 0);
     if (a.lse)
+#pragma unroll 1
       for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < spare;
            x += (long long)gridDim.x * blockDim.x)
         a.lse[first + x] = SV_NEG_INF;

@@ -2,8 +2,8 @@
 // (tcgen05) as inline PTX, for kernels whose operands lie in 128-byte
 // swizzled shared memory tiles.
 //
-// Every wait is bounded: after kWaitLimitNs (or kSpinLimit polls) it gives up
-// and raises the CTA's abort word, which the other waits see.
+// Every wait is bounded: after kNaps polls it gives up and raises the CTA's
+// abort word, which the other waits see.
 #pragma once
 
 #include <cuda.h>
@@ -11,14 +11,8 @@
 
 namespace sv {
 
-constexpr int kSpinLimit = 1 << 24;
-constexpr unsigned long long kWaitLimitNs = 1000000000ull;
-
-__device__ __forceinline__ unsigned long long clock_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
+constexpr unsigned kNapNs = 100000;   // longest sleep of one poll that is asked for
+constexpr int kNaps = 1 << 20;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -39,32 +33,32 @@ __device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes)
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
+// Whether the phase is over; may sleep until it is, up to about kNapNs.
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "n"(kNapNs)
       : "memory");
   return ok != 0;
 }
-// Polls until the phase is over; false if that took too long or, with an
-// abort word, if the CTA has given up.
+// Waits until the phase is over; false if the wait was given up, after kNaps
+// polls or once the CTA has given up elsewhere.  Kept short: waits are many,
+// and the instruction cache is small.
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_word) {
-  const unsigned long long start = clock_ns();
-  for (int i = 0; i < kSpinLimit; ++i) {
+#pragma unroll 1
+  for (int i = 0; i < kNaps; ++i) {
     if (mbar_try(bar, parity)) return true;
-    if ((i & 63) == 63 && ((abort_word && *abort_word) || clock_ns() - start > kWaitLimitNs)) break;
+    if (*abort_word) break;
   }
-  return mbar_try(bar, parity);
+  return false;
 }
 // All lanes of a warp wait; false (for all of them) if the wait was given up.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_word) {
-  bool ok = mbar_try(bar, parity);
-  if (!ok) ok = mbar_poll(bar, parity, abort_word);
-  ok = __all_sync(0xffffffffu, ok);
+  const bool ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_word));
   if (!ok) *abort_word = 1;
   return ok;
 }
