@@ -99,7 +99,8 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, int b, bool* bad 
 }
 // The query units of a request: kTiles tiles of tile_tokens tokens each.  A
 // unit's weight is the number of keys that its last token sees, or one key
-// tile where that is more, so that weights sum in closed form.
+// tile where that is more, so that weights sum in closed form; the last unit's
+// is rounded up to key tiles, so that short contexts are cut between tiles.
 template <typename S>
 struct AttnUnits {
   AttnRow row;
@@ -112,7 +113,8 @@ struct AttnUnits {
   // keys that the request's tokens up to t1 see
   __device__ __forceinline__ int seen(int t1) const { return max(0, row.L - row.n + t1); }
   __device__ __forceinline__ int weight(int m) const {
-    return max(S::kKeys, seen(min(row.n, (m + 1) * step)));
+    if (m < count - 1) return max(S::kKeys, seen((m + 1) * step));
+    return max(S::kKeys, (seen(row.n) + S::kKeys - 1) / S::kKeys * S::kKeys);
   }
   // weight of the first `units` units
   __device__ __forceinline__ long long before(int units) const {
@@ -136,7 +138,7 @@ struct AttnControl {   // at the end of the shared memory
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty, drain, met;
   uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer]
-  uint64_t pv_done[2], turn[2];
+  uint64_t pv_done[2];
   uint32_t tmem;
   int abort_word;
   int calm;                   // an abort word that stays 0, for the waits of a CTA that gives up
@@ -344,7 +346,6 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   const uint32_t o = tmem + S::kTiles * S::kBufs * S::kKeys + t * kD;
   int it = 0, rounds = 0;
   int done = 0;   // tiles of S issued before this unit
-  int turns = 0;
   bool ok = true;
 
   auto s_col = [&](int k) { return s_base + (k % S::kBufs) * S::kKeys; };
@@ -355,13 +356,9 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   const uint64_t q_desc = tile_desc(q_smem + t * S::kQBytes, 16, 1024);
   const uint64_t k_desc = tile_desc(ring, 16, 1024);
   const uint64_t v_desc = tile_desc(ring, S::kKeys * 128, 1024);
-  auto my_turn = [&]() {   // tile 0 has the first
-    const int before = turns++ - (t == 0 ? 1 : 0);
-    return S::kTiles == 1 || before < 0 ||
-           mbar_wait(smem_addr(&c->turn[t]), before & 1, &c->abort_word);
-  };
-  auto pass_turn = [&]() {
-    if (S::kTiles > 1 && lane == 0) mbar_arrive(smem_addr(&c->turn[1 - t]));
+  // The other tile's turn: the last of the arrivals that its P waits for.
+  auto pass_turn = [&](bool pass) {
+    if (pass && lane == 0) mbar_arrive(smem_addr(&c->p_ready[1 - t][0]));
   };
   // S = Q K^T, the tile's k-th; the turn passes before the last two products,
   // which last about as long as the other warp takes to see it
@@ -369,7 +366,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
     const uint64_t k0 = k_desc + stage * (S::kStageBytes / 16);
 #pragma unroll
     for (int d = 0; d < kD / 16; ++d) {
-      if (d == kD / 16 - 2 && pass) pass_turn();
+      if (S::kTiles > 1 && d == kD / 16 - 2) pass_turn(pass);
       mma_smem(s_col(k), q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
                k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0, issue);
     }
@@ -385,7 +382,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
 
 #pragma unroll 1
   for (bool first = true; ok && u.next(first); first = false) {
-    const int n = u.most(), cnt = u.count(t);
+    const int n = u.most(), cnt = u.count(t), other = S::kTiles > 1 ? u.count(1 - t) : 0;
     if (n == 0) continue;
     if (!(ok = mbar_wait(smem_addr(&c->q_full), rounds++ & 1, &c->abort_word))) break;
     tc_fence_after();
@@ -422,11 +419,17 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       // wide: every wait comes before the products, since the tensor core's queue
       // is short; narrow: O += P V does not wait for keys that are still to come
       if (S::kTiles > 1 && another && !(ok = wait_stage(k_it))) break;
-      if (active && !(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
-                                     &c->abort_word)))
-        break;
-      if (!(ok = my_turn())) break;
-      tc_fence_after();
+      if (active) {
+        // no turn to wait for: the other tile has no product before this one
+        if (S::kTiles > 1 && !(t == 0 ? i > 0 && i - 1 < other : i < other) && lane == 0)
+          mbar_arrive(smem_addr(&c->p_ready[t][0]));
+        if (!(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
+                             &c->abort_word)))
+          break;
+        tc_fence_after();
+      }
+      // the other tile's next product, if it has one
+      const bool pass = active && (t == 0 ? i < other : i + 1 < other);
       if (active) {
         const uint64_t v0 = v_desc + (v_it % S::kStages) * (S::kStageBytes / 16);
 #pragma unroll
@@ -439,8 +442,8 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
         if (!(ok = wait_stage(k_it))) break;
         tc_fence_after();
       }
-      if (next) scores(k + S::kBufs, k_it % S::kStages, true);
-      else pass_turn();
+      if (next) scores(k + S::kBufs, k_it % S::kStages, pass);
+      else if (S::kTiles > 1) pass_turn(pass);
       release(&c->empty[v_it % S::kStages], active);
       if (another) release(&c->empty[k_it % S::kStages], next);
       if (next && i + S::kBufs + 1 == cnt) release(&c->q_empty, true);
@@ -494,13 +497,17 @@ __device__ __forceinline__ void stage_piece(char* stage, int piece, uint32_t x, 
 __device__ __forceinline__ void store_staged(const char* stage, char* to) {
   const int lane = threadIdx.x & 31, piece = lane % 8;
   __syncwarp();
-#pragma unroll 2
+  uint4 v[8];
+  unsigned long long dst[8];
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = i * 4 + lane / 8;
-    char* dst = (char*)__shfl_sync(0xffffffffu, (unsigned long long)to, row);
-    if (dst)
-      *(uint4*)(dst + piece * 16) = *(const uint4*)(stage + row * 128 + (piece ^ (row & 7)) * 16);
+    v[i] = *(const uint4*)(stage + row * 128 + (piece ^ (row & 7)) * 16);
+    dst[i] = __shfl_sync(0xffffffffu, (unsigned long long)to, row);
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (dst[i]) *(uint4*)(dst[i] + piece * 16) = v[i];
   __syncwarp();
 }
 
@@ -808,10 +815,9 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     for (int t = 0; t < S::kTiles; ++t) {
       for (int k = 0; k < S::kBufs; ++k) {
         mbar_init(smem_addr(&c->s_full[t][k]), 1);
-        mbar_init(smem_addr(&c->p_ready[t][k]), 4);
+        mbar_init(smem_addr(&c->p_ready[t][k]), S::kTiles > 1 ? 5 : 4);   // with the turn
       }
       mbar_init(smem_addr(&c->pv_done[t]), 1);
-      mbar_init(smem_addr(&c->turn[t]), 1);
     }
     mbar_init_fence();
     c->abort_word = c->calm = 0;
