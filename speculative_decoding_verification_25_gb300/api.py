@@ -15,6 +15,7 @@ tokens' keys and values and attends.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import NamedTuple, Optional
 
 import torch
@@ -262,11 +263,26 @@ class PagedPlan(NamedTuple):
     free_count: torch.Tensor   # [1] int32: pages on the stack now
 
 
+def _ints(t, name, shape, dev):
+    """The address of a contiguous int32 tensor of this shape on ``dev``."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape
+            and t.device == dev and t.is_cuda and t.is_contiguous()):
+        _check(t, name, dtype=torch.int32, shape=shape, device=dev)   # says what is wrong
+    return t.data_ptr()
+
+
 def _flags_ptr(flags, dev):
-    if flags is None:
-        return None
-    _check(flags, "flags", dtype=torch.int32, shape=(1,), device=dev)
-    return flags.data_ptr()
+    return None if flags is None else _ints(flags, "flags", (1,), dev)
+
+
+def _stream_handle(stream, dev):
+    """The raw handle of ``stream``, the device's current one if None."""
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _on(stream):
+    """Makes what is allocated inside belong to ``stream`` (None: the current one)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def paged_plan(seq_len: torch.Tensor, num_new: torch.Tensor, page_count: torch.Tensor,
@@ -283,35 +299,25 @@ def paged_plan(seq_len: torch.Tensor, num_new: torch.Tensor, page_count: torch.T
     updated in place.  The counts come back in the result, whose tensors may
     be ``page_count`` and ``free_count`` themselves (pass them in ``out``).
     All tensors are int32; ``flags`` (one int32) collects SV_DEV_* bits."""
-    B = seq_len.shape[0] if seq_len.dim() else 0
-    dev = seq_len.device
-    _check(seq_len, "seq_len", dtype=torch.int32, shape=(B,))
-    _check(num_new, "num_new", dtype=torch.int32, shape=(B,), device=dev)
-    _check(page_count, "page_count", dtype=torch.int32, shape=(B,), device=dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    max_pages = block_table.shape[1]
-    _check(block_table, "block_table", dtype=torch.int32, shape=(B, max_pages), device=dev)
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be [n_pages]")
-    _check(free_pages, "free_pages", dtype=torch.int32, device=dev)
-    _check(free_count, "free_count", dtype=torch.int32, shape=(1,), device=dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    if seq_len.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("seq_len must be [B], block_table [B, max_pages], free_pages [n_pages]")
+    B, max_pages, n_pages, dev = seq_len.shape[0], block_table.shape[1], free_pages.shape[0], seq_len.device
+    ins = (_ints(seq_len, "seq_len", (B,), dev), _ints(num_new, "num_new", (B,), dev),
+           _ints(page_count, "page_count", (B,), dev),
+           _ints(block_table, "block_table", (B, max_pages), dev),
+           _ints(free_pages, "free_pages", (n_pages,), dev), _ints(free_count, "free_count", (1,), dev))
+    sizes = (B + 1, B, max_tokens, max_tokens, B, 1)
     if out is None:
         if max_tokens < 0:
             raise ValueError("max_tokens must not be negative")
-        with torch.cuda.stream(st):   # outputs belong to the stream that writes them
-            out = PagedPlan(*(torch.empty(n, dtype=torch.int32, device=dev)
-                              for n in (B + 1, B, max_tokens, max_tokens, B, 1)))
+        with _on(stream):   # outputs belong to the stream that writes them
+            out = PagedPlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
+        outs = [t.data_ptr() for t in out]
     else:
-        for name, n in zip(PagedPlan._fields, (B + 1, B, max_tokens, max_tokens, B, 1)):
-            _check(getattr(out, name), "out." + name, dtype=torch.int32, shape=(n,), device=dev)
-    status = N.spec_paged_plan_raw(
-        seq_len.data_ptr(), num_new.data_ptr(), page_count.data_ptr(), block_table.data_ptr(),
-        free_pages.data_ptr(), free_count.data_ptr(), B, page_size, max_pages, free_pages.shape[0],
-        max_tokens, out.cu_new.data_ptr(), out.kv_len.data_ptr(), out.slot_map.data_ptr(),
-        out.positions.data_ptr(), out.page_count.data_ptr(), out.free_count.data_ptr(),
-        _flags_ptr(flags, dev), st.cuda_stream)
+        outs = [_ints(t, "out." + name, (n,), dev)
+                for t, name, n in zip(out, PagedPlan._fields, sizes)]
+    status = N.spec_paged_plan_raw(*ins, B, page_size, max_pages, n_pages, max_tokens, *outs,
+                                   _flags_ptr(flags, dev), _stream_handle(stream, dev))
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_plan")
     return out
@@ -321,29 +327,32 @@ def _check_cache(k_cache, v_cache):
     """(dtype code, n_pages, Hk, page_size, D) of a paged cache."""
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [n_pages, Hk, page_size, D]")
-    if k_cache.dtype not in _CACHE_DTYPES:
+    dt = _CACHE_DTYPES.get(k_cache.dtype)
+    if dt is None:
         raise TypeError(f"k_cache dtype {k_cache.dtype} is not bfloat16 or float16")
-    _check(k_cache, "k_cache")
-    _check(v_cache, "v_cache", dtype=k_cache.dtype, shape=k_cache.shape, device=k_cache.device)
-    return (_CACHE_DTYPES[k_cache.dtype], *k_cache.shape)
+    if not (k_cache.is_cuda and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and v_cache.dtype is k_cache.dtype and v_cache.shape == k_cache.shape
+            and v_cache.device == k_cache.device):
+        _check(k_cache, "k_cache")
+        _check(v_cache, "v_cache", dtype=k_cache.dtype, shape=k_cache.shape, device=k_cache.device)
+    return (dt, *k_cache.shape)
 
 
 def _check_packed(t, name, dtype, shape, dev):
     """A packed [T, heads, D] tensor whose heads are dense; its token stride."""
-    if t.dim() != 3 or tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.numel() == 0:
-        return shape[1] * shape[2]
+    T, heads, D = shape
+    if T * heads == 0:
+        return heads * D
     stride_t, stride_h, stride_d = t.stride()
-    if shape[0] == 1:
-        stride_t = max(stride_t, shape[1] * shape[2])
-    if stride_d != 1 or (stride_h != shape[2] and shape[1] > 1):
-        raise ValueError(f"{name} must have dense heads (strides [any, {shape[2]}, 1])")
-    return stride_t
+    if stride_d != 1 or (stride_h != D and heads > 1):
+        raise ValueError(f"{name} must have dense heads (strides [any, {D}, 1])")
+    return stride_t if T > 1 else heads * D
 
 
 def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tensor,
@@ -358,14 +367,13 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tenso
     if slot_map.dim() != 1:
         raise ValueError("slot_map must be [T]")
     T = slot_map.shape[0]
-    _check(slot_map, "slot_map", dtype=torch.int32, device=dev)
+    slots = _ints(slot_map, "slot_map", (T,), dev)
     k_stride = _check_packed(k_new, "k_new", k_cache.dtype, (T, Hk, D), dev)
     v_stride = _check_packed(v_new, "v_new", k_cache.dtype, (T, Hk, D), dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
     status = N.spec_paged_append_raw(
-        k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, slot_map.data_ptr(), dt, T, Hk, D,
-        page_size, n_pages, k_cache.data_ptr(), v_cache.data_ptr(), _flags_ptr(flags, dev),
-        st.cuda_stream)
+        k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, slots, dt, T, Hk, D, page_size,
+        n_pages, k_cache.data_ptr(), v_cache.data_ptr(), _flags_ptr(flags, dev),
+        _stream_handle(stream, dev))
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_append")
 
@@ -384,9 +392,9 @@ def attention_workspace(D: int, device: torch.device,
         raise ValueError(f"invalid head dimension {D}")
     index = device.index if device.index is not None else torch.cuda.current_device()
     st = stream if stream is not None else torch.cuda.current_stream(index)
-    key = (index, st.cuda_stream)
+    key = (index, st.cuda_stream, D)
     ws = _attention_workspaces.get(key)
-    if ws is None or ws.numel() < need:
+    if ws is None:
         with torch.cuda.stream(st):   # allocated and zeroed on the stream that uses it
             ws = torch.empty(need, dtype=torch.uint8, device=device)
             ws[:N.SV_ATTENTION_COUNTER_BYTES].zero_()
@@ -407,19 +415,17 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     zeros.  ``scale`` defaults to D ** -0.5."""
     dt, n_pages, Hk, page_size, D = _check_cache(k_cache, v_cache)
     dev = k_cache.device
-    if q.dim() != 3 or q.shape[2] != D:
+    if q.dim() != 3:
         raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
     T, Hq, _ = q.shape
     q_stride = _check_packed(q, "q", k_cache.dtype, (T, Hq, D), dev)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
     B, max_pages = block_table.shape
-    _check(block_table, "block_table", dtype=torch.int32, device=dev)
-    _check(cu_new, "cu_new", dtype=torch.int32, shape=(B + 1,), device=dev)
-    _check(kv_len, "kv_len", dtype=torch.int32, shape=(B,), device=dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    tables = (_ints(block_table, "block_table", (B, max_pages), dev),
+              _ints(cu_new, "cu_new", (B + 1,), dev), _ints(kv_len, "kv_len", (B,), dev))
     if out is None:
-        with torch.cuda.stream(st):   # outputs belong to the stream that writes them
+        with _on(stream):   # outputs belong to the stream that writes them
             out = AttentionResult(
                 torch.empty(T, Hq, D, dtype=q.dtype, device=dev),
                 torch.empty(T, Hq, dtype=torch.float32, device=dev) if want_lse else None)
@@ -427,14 +433,17 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _check(out.out, "out.out", dtype=q.dtype, shape=(T, Hq, D), device=dev)
         if out.lse is not None:
             _check(out.lse, "out.lse", dtype=torch.float32, shape=(T, Hq), device=dev)
+    handle = _stream_handle(stream, dev)
     if workspace is None:
-        workspace = attention_workspace(D, dev, st)
+        workspace = _attention_workspaces.get((dev.index, handle, D))
+        if workspace is None:
+            workspace = attention_workspace(D, dev, stream)
     status = N.spec_paged_attention_raw(
-        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, block_table.data_ptr(),
-        cu_new.data_ptr(), kv_len.data_ptr(), B, T, Hq, Hk, D, page_size, max_pages, n_pages,
-        D ** -0.5 if scale is None else scale, out.out.data_ptr(),
-        out.lse.data_ptr() if out.lse is not None else None, workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _flags_ptr(flags, dev), st.cuda_stream)
+        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, *tables, B, T, Hq, Hk,
+        D, page_size, max_pages, n_pages, D ** -0.5 if scale is None else scale,
+        out.out.data_ptr(), out.lse.data_ptr() if out.lse is not None else None,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _flags_ptr(flags, dev),
+        handle)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_attention")
     return out

@@ -128,7 +128,6 @@ int spec_paged_plan(const int32_t* seq_len, const int32_t* num_new, const int32_
                         (const void*)page_count_out, (const void*)free_count_out,
                         (const void*)flags})
     if (!aligned_to(p, 4)) return SV_ERR_ALIGN;
-  if (!paged_device()) return SV_ERR_CUDA;
   sv::PlanArgs a;
   a.seq_len = seq_len;
   a.num_new = num_new;
@@ -148,13 +147,27 @@ int spec_paged_plan(const int32_t* seq_len, const int32_t* num_new, const int32_
   a.page_count_out = page_count_out;
   a.free_count_out = free_count_out;
   a.flags = flags;
-  // one CTA up to four tokens per thread, then as many as the cluster holds
-  int ctas = 1;
-  while (ctas < kMaxCluster && (long long)ctas * 4 * sv::kPlanThreads < max_tokens) ctas *= 2;
+  a.in_place = page_count_out == page_count || free_count_out == free_count;
+  // One CTA up to a chunk per warp, then as many as the chunks fill: small
+  // plans are a chain of latencies, in which more warps only add to the block
+  // sums (B = 64, 320 tokens: LATENCY_SMALL), large ones store 8 bytes per token.
+  PagedDevice* dev = paged_device();
+  if (!dev) return SV_ERR_CUDA;
+  int threads = 256;
+  while (threads < sv::kPlanThreads &&
+         (threads < B || threads / 32 * sv::kPlanChunk < max_tokens))
+    threads *= 2;
+  const long long chunks = ((long long)max_tokens + sv::kPlanChunk - 1) / sv::kPlanChunk;
+  const long long most = a.in_place ? kMaxCluster : dev->sm_count;
+  long long ctas = (chunks + threads / 32 - 1) / (threads / 32);
+  if (ctas > most) ctas = most;
+  if (a.in_place)
+    while (ctas & (ctas - 1)) ctas &= ctas - 1;   // cluster sizes are powers of two
+  if (ctas < 1) ctas = 1;
   void* args[] = {&a};
   return done(launch_early((const void*)sv::sv_paged_plan_kernel, dim3((unsigned)ctas),
-                           dim3(sv::kPlanThreads), args, (cudaStream_t)stream,
-                           (size_t)B * sv::kPlanRowBytes, (unsigned)ctas));
+                           dim3((unsigned)threads), args, (cudaStream_t)stream,
+                           (size_t)B * sv::kPlanRowBytes, a.in_place ? (unsigned)ctas : 1u));
 }
 
 int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,

@@ -633,65 +633,53 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           for (int x = 0; x < S::kKeys; ++x)
             if (x >= left) bits[x] = 0xff800000u;
         }
-        // The unit's first tile sets the reference; a later one assumes that it
-        // holds, looks for its maximum on the way (another pipe than the
-        // exponentials'), and starts over in the rare case that it does not.
-        float high;
-        if (i == 0) {
-          high = row_max<S::kKeys>(bits) * a.scale_log2;
-          if (mine) m = high;
-        }
-        float sum;
-#pragma unroll 1
-        while (true) {
-          const float ref = m == SV_NEG_INF ? 0.f : m;
-          const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
-          const unsigned long long ref2 = f2_pack(-ref, -ref);
-          unsigned long long sums[2] = {0, 0};
-#pragma unroll
-          for (int x = 0; x < S::kKeys; x += 32) {
-            uint32_t p[16];
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              float p0, p1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(bits[x + y]), __uint_as_float(bits[x + y + 1])),
-                               scale2, ref2),
-                        p0, p1);
-              p0 = ex2_approx(p0);
-              p1 = ex2_approx(p1);
-              sums[(y / 2) % 2] = f2_add(sums[(y / 2) % 2], f2_pack(p0, p1));
-              p[y / 2] = pack2(p0, p1, E());
-            }
-            tmem_store16(s_col + x / 2, p);
-          }
-          float s0, s1;
-          f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
-          sum = s0 + s1;
-          if (i == 0) break;
-          high = row_max<S::kKeys>(bits) * a.scale_log2;
-          const bool raise = mine && high > m + kSlack;
-          if (!__any_sync(0xffffffffu, raise)) break;
-          // scale what was summed before, once the products are done
+        // The reference follows the maximum where that rises by more than kSlack.
+        const float high = row_max<S::kKeys>(bits) * a.scale_log2;
+        const bool raise = mine && (i == 0 ? high > m : high > m + kSlack);
+        if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (m == SV_NEG_INF ? 0.f : ex2_approx(m - high)) : 1.f;
           if (raise) m = high;
           l *= f;
-          if (S::kBufs > 1 && i > 0) {
-            if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
-            tc_fence_after();
-          }
+          if (i > 0) {   // what was summed before, once the products are done
+            if (S::kBufs > 1) {
+              if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
+              tc_fence_after();
+            }
 #pragma unroll 1
-          for (int x = 0; x < kD; x += 32) {
-            uint32_t o[32];
-            tmem_load32(o_col + x, o);
-            tmem_wait_load();
-            tmem_pin<32>(o);
+            for (int x = 0; x < kD; x += 32) {
+              uint32_t o[32];
+              tmem_load32(o_col + x, o);
+              tmem_wait_load();
+              tmem_pin<32>(o);
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
-            tmem_store32(o_col + x, o);
+              for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tmem_store32(o_col + x, o);
+            }
           }
         }
-        if (!ok) break;
-        l += sum;
+        const float ref = m == SV_NEG_INF ? 0.f : m;
+        const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
+        const unsigned long long ref2 = f2_pack(-ref, -ref);
+        unsigned long long sums[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < S::kKeys; x += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(bits[x + y]), __uint_as_float(bits[x + y + 1])),
+                             scale2, ref2),
+                      p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sums[(y / 2) % 2] = f2_add(sums[(y / 2) % 2], f2_pack(p0, p1));
+            p[y / 2] = pack2(p0, p1, E());
+          }
+          tmem_store16(s_col + x / 2, p);
+        }
+        float s0, s1;
+        f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
+        l += s0 + s1;
         tmem_wait_store();
       }
       // With two S buffers the scores do not tell that the last O += P V is

@@ -1,24 +1,26 @@
 // Pages, slots and packed offsets of a step, from the request lengths.
 //
 // Everything follows from three exclusive sums over the rows: new tokens,
-// pages given back, pages taken.  Every CTA of one cluster forms all of them
-// (a thread owns consecutive rows; warp shuffles join the threads) and keeps
-// a row's sums in shared memory; then the CTAs share out the tokens, the
-// taken pages and the pages that go on the stack, each index finding its row
-// by bisection of the sums.  The k-th page taken is a closed form of k, so
-// no CTA waits for another's work.  Counts may be updated in place: they are
-// written after a cluster barrier behind the last read.
+// pages given back, pages taken.  Every CTA forms all of them (a thread owns
+// consecutive rows; warp shuffles join the threads) and keeps a row's sums in
+// shared memory; then the CTAs share out the tokens, the taken pages and the
+// pages that go on the stack, each index finding its row by bisection of the
+// sums.  The k-th page taken is a closed form of k, so no CTA waits for
+// another's work.  Where the counts are updated in place the grid is one
+// cluster, whose barrier stands between the last read and the first write;
+// else it is as large as the tokens ask for.
 //
 // Bound by latency: the chain load lengths -> two block sums -> bisect ->
 // load page -> store, a few microseconds, until the tokens' 8 bytes each
-// take longer, which more CTAs of the cluster share.
+// take longer, which more CTAs share.
 #pragma once
 
 #include "sv_paged.cuh"
 
 namespace sv {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024;     // at most
+constexpr int kPlanChunk = 256;        // consecutive tokens of a warp
 constexpr int kPlanRowBytes = 5 * 4;   // shared memory per row
 
 struct PlanArgs {
@@ -35,6 +37,7 @@ struct PlanArgs {
   int32_t* positions;          // [max_tokens]
   int32_t* page_count_out;     // [B], may be page_count
   int32_t* free_count_out;     // [1], may be free_count
+  bool in_place;               // a count's output is its input: the grid is one cluster
   unsigned* flags;
 };
 
@@ -51,7 +54,7 @@ __device__ __forceinline__ V block_exclusive_sum(V v, V* parts, V* total) {
   }
   if (lane == 31) parts[warp] = inc;
   __syncthreads();
-  V p = lane < kPlanThreads / 32 ? parts[lane] : 0;
+  V p = lane < blockDim.x / 32 ? parts[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const V u = __shfl_up_sync(0xffffffffu, p, o);
@@ -68,7 +71,7 @@ __device__ __forceinline__ int block_max(int v, int* parts) {
   v = __reduce_max_sync(0xffffffffu, v);
   if (lane == 0) parts[warp] = v;
   __syncthreads();
-  v = __reduce_max_sync(0xffffffffu, parts[lane < kPlanThreads / 32 ? lane : 0]);
+  v = __reduce_max_sync(0xffffffffu, parts[lane < blockDim.x / 32 ? lane : 0]);
   __syncthreads();
   return v;
 }
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads) sv_paged_plan_kernel(PlanArgs a)
   int* s_seq = s_have + a.B;
   __shared__ long long parts[32];
   const int tid = threadIdx.x;
-  const int cta = blockIdx.x, n_ctas = gridDim.x;   // the grid is one cluster
+  const int cta = blockIdx.x, n_ctas = gridDim.x, threads = blockDim.x;
   const int page = 1 << a.page_shift;
 
   wait_for_preceding_grid();
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) sv_paged_plan_kernel(PlanArgs a)
     F = F < 0 ? 0 : a.n_pages;
   }
   // -------- new tokens.  Rows of the thread: [r0, r1)
-  const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
+  const int per = (a.B + threads - 1) / threads;
   const int r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
   long long mine = 0;
   for (int r = r0; r < r1; ++r) {
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kPlanThreads) sv_paged_plan_kernel(PlanArgs a)
   };
 
   // -------- the CTAs of the cluster share out what is left
-  const unsigned first = cta * kPlanThreads + tid, step = n_ctas * kPlanThreads;   // sums stay below 2^31
+  const unsigned first = cta * threads + tid, step = n_ctas * threads;   // sums stay below 2^31
   for (unsigned k = first; k < (unsigned)N; k += step) {   // the tables' new entries
     const int r = row_of(s_need, a.B, k);
     a.block_table[(long long)r * a.max_pages + s_have[r] + (k - (r > 0 ? s_need[r - 1] : 0))] =
@@ -201,33 +204,39 @@ __global__ void __launch_bounds__(kPlanThreads) sv_paged_plan_kernel(PlanArgs a)
     else bad |= kDevLength;
   }
   const int tokens = a.B > 0 ? s_cu[a.B - 1] : 0;
-  for (unsigned t = first; t < (unsigned)a.max_tokens; t += step) {
-    int slot = -1, pos = -1;
-    if (t < (unsigned)tokens) {
-      const int r = row_of(s_cu, a.B, t);
-      pos = s_seq[r] + t - (r > 0 ? s_cu[r - 1] : 0);
-      const int have = s_have[r];
-      if (have >= 0) {
-        const int pg = pos >> a.page_shift;
-        const int id = pg < have ? a.block_table[(long long)r * a.max_pages + pg]
-                                 : taken((r > 0 ? s_need[r - 1] : 0) + pg - have);
-        if (id >= 0 && id < a.n_pages) slot = (id << a.page_shift) | (pos & (page - 1));
-        else bad |= kDevBadPage;
+  const int lane = tid & 31;
+  for (unsigned t0 = first / 32 * kPlanChunk; t0 < (unsigned)a.max_tokens; t0 += step / 32 * kPlanChunk) {
+    unsigned t = t0 + lane;
+    int r = t < (unsigned)tokens ? row_of(s_cu, a.B, t) : 0;
+    for (int i = 0; i < kPlanChunk / 32; ++i, t += 32) {
+      if (t >= (unsigned)a.max_tokens) break;
+      int slot = -1, pos = -1;
+      if (t < (unsigned)tokens) {
+        while (s_cu[r] <= (int)t) ++r;
+        pos = s_seq[r] + t - (r > 0 ? s_cu[r - 1] : 0);
+        const int have = s_have[r];
+        if (have >= 0) {
+          const int pg = pos >> a.page_shift;
+          const int id = pg < have ? a.block_table[(long long)r * a.max_pages + pg]
+                                   : taken((r > 0 ? s_need[r - 1] : 0) + pg - have);
+          if (id >= 0 && id < a.n_pages) slot = (id << a.page_shift) | (pos & (page - 1));
+          else bad |= kDevBadPage;
+        }
       }
+      a.slot_map[t] = slot;
+      a.positions[t] = pos;
     }
-    a.slot_map[t] = slot;
-    a.positions[t] = pos;
   }
   if (bad) set_flag(a.flags, bad);
   // -------- lengths and counts, in place if the caller likes: every CTA has read them
-  if (n_ctas > 1) {
+  if (a.in_place && n_ctas > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   } else {
     __syncthreads();
   }
   if (cta == 0) {
-    for (int r = tid; r < a.B; r += kPlanThreads) {
+    for (int r = tid; r < a.B; r += threads) {
       const int begin = r > 0 ? s_cu[r - 1] : 0, fresh = s_cu[r] - begin;
       const int have = s_have[r];
       a.cu_new[r + 1] = s_cu[r];
