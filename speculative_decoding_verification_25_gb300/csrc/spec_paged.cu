@@ -148,18 +148,20 @@ int spec_paged_plan(const int32_t* seq_len, const int32_t* num_new, const int32_
   a.free_count_out = free_count_out;
   a.flags = flags;
   a.in_place = page_count_out == page_count || free_count_out == free_count;
-  // One CTA up to a chunk per warp, then as many as the chunks fill: small
-  // plans are a chain of latencies, in which more warps only add to the block
-  // sums (B = 64, 320 tokens: LATENCY_SMALL), large ones store 8 bytes per token.
+  // Small plans are a chain of latencies: one CTA, a lane per token.  Large
+  // ones store 8 bytes per token: up to kPlanChunk of them in a row per warp,
+  // which then bisects the rows once, and CTAs until the GPU is full.
   PagedDevice* dev = paged_device();
   if (!dev) return SV_ERR_CUDA;
   int threads = 256;
-  while (threads < sv::kPlanThreads &&
-         (threads < B || threads / 32 * sv::kPlanChunk < max_tokens))
-    threads *= 2;
-  const long long chunks = ((long long)max_tokens + sv::kPlanChunk - 1) / sv::kPlanChunk;
+  while (threads < sv::kPlanThreads && (threads < B || threads < max_tokens)) threads *= 2;
   const long long most = a.in_place ? kMaxCluster : dev->sm_count;
-  long long ctas = (chunks + threads / 32 - 1) / (threads / 32);
+  const long long lanes = most * threads;
+  a.chunk = 32 * (int)((max_tokens + lanes - 1) / lanes);
+  if (a.chunk > sv::kPlanChunk) a.chunk = sv::kPlanChunk;
+  if (a.chunk < 32) a.chunk = 32;
+  const long long per_cta = (long long)(threads / 32) * a.chunk;
+  long long ctas = (max_tokens + per_cta - 1) / per_cta;
   if (ctas > most) ctas = most;
   if (a.in_place)
     while (ctas & (ctas - 1)) ctas &= ctas - 1;   // cluster sizes are powers of two

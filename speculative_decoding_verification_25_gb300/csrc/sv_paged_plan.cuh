@@ -20,7 +20,7 @@
 namespace sv {
 
 constexpr int kPlanThreads = 1024;     // at most
-constexpr int kPlanChunk = 256;        // consecutive tokens of a warp
+constexpr int kPlanChunk = 256;        // consecutive tokens of a warp, at most
 constexpr int kPlanRowBytes = 5 * 4;   // shared memory per row
 
 struct PlanArgs {
@@ -31,6 +31,7 @@ struct PlanArgs {
   int32_t* free_pages;         // [n_pages]
   const int32_t* free_count;   // [1]
   int B, page_shift, max_pages, n_pages, max_tokens;
+  int chunk;                   // consecutive tokens of a warp, a multiple of 32
   int32_t* cu_new;             // [B+1]
   int32_t* kv_len;             // [B]
   int32_t* slot_map;           // [max_tokens]
@@ -205,10 +206,10 @@ __global__ void __launch_bounds__(kPlanThreads) sv_paged_plan_kernel(PlanArgs a)
   }
   const int tokens = a.B > 0 ? s_cu[a.B - 1] : 0;
   const int lane = tid & 31;
-  for (unsigned t0 = first / 32 * kPlanChunk; t0 < (unsigned)a.max_tokens; t0 += step / 32 * kPlanChunk) {
+  for (unsigned t0 = first / 32 * a.chunk; t0 < (unsigned)a.max_tokens; t0 += step / 32 * a.chunk) {
     unsigned t = t0 + lane;
     int r = t < (unsigned)tokens ? row_of(s_cu, a.B, t) : 0;
-    for (int i = 0; i < kPlanChunk / 32; ++i, t += 32) {
+    for (int i = 0; i < a.chunk; i += 32, t += 32) {
       if (t >= (unsigned)a.max_tokens) break;
       int slot = -1, pos = -1;
       if (t < (unsigned)tokens) {
