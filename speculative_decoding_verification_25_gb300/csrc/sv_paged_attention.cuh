@@ -626,9 +626,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
         for (int x = 0; x < S::kKeys; x += 32) tmem_load32(s_col + x, bits + x);
         tmem_wait_load();
         tmem_pin<S::kKeys>(bits);
-        const int base = (u.j0 + i) * S::kKeys;
-        if (base + S::kKeys > fewest) {
-          const int left = seen - base;
+        const int left = seen - (u.j0 + i) * S::kKeys;   // keys of the tile that the row sees
+        if (fewest < (u.j0 + i + 1) * S::kKeys) {
 #pragma unroll
           for (int x = 0; x < S::kKeys; ++x)
             if (x >= left) bits[x] = 0xff800000u;
@@ -727,9 +726,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           uint32_t p[16];
 #pragma unroll
           for (int y = 0; y < 16; ++y)
-            p[y] = l > 0.f ? pack2(__uint_as_float(bits[2 * y]) * inv,
-                                   __uint_as_float(bits[2 * y + 1]) * inv, E())
-                           : 0u;
+            p[y] = pack2(__uint_as_float(bits[2 * y]) * inv, __uint_as_float(bits[2 * y + 1]) * inv,
+                         E());
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             stage_piece(stage, x / 8 % 8 + y, p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);

@@ -11,8 +11,7 @@
 
 namespace sv {
 
-constexpr unsigned kNapNs = 100000;   // longest sleep of one poll that is asked for
-constexpr int kNaps = 1 << 20;
+constexpr int kNaps = 1 << 19;   // a poll sleeps about 2 us, so about a second
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -33,15 +32,15 @@ __device__ __forceinline__ void mbar_arrive_expect(uint32_t bar, uint32_t bytes)
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
-// Whether the phase is over; may sleep until it is, up to about kNapNs.
+// Whether the phase is over; may sleep a while until it is.
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "n"(kNapNs)
+      : "r"(bar), "r"(parity)
       : "memory");
   return ok != 0;
 }
