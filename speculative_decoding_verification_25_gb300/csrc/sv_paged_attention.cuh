@@ -487,99 +487,87 @@ __device__ __forceinline__ int take_ticket(int* ticket) {
 
 // 128 bytes of each of a warp's 32 rows, a row per lane, to global memory with
 // four whole segments per instruction: they pass through shared memory, their
-// 16-byte pieces placed so that neither side meets bank conflicts.  `to` is
-// the lane's segment, nullptr for none.
+// 16-byte pieces placed so that neither side meets bank conflicts.  The
+// lane's segment is `to` pitches from `base`, none if negative.
 __device__ __forceinline__ void stage_piece(char* stage, int piece, uint32_t x, uint32_t y,
                                             uint32_t z, uint32_t w) {
   const int lane = threadIdx.x & 31;
   *(uint4*)(stage + lane * 128 + (piece ^ (lane & 7)) * 16) = make_uint4(x, y, z, w);
 }
-__device__ __forceinline__ void store_staged(const char* stage, char* to) {
+__device__ __forceinline__ void store_staged(const char* stage, char* base, int to, int pitch) {
   const int lane = threadIdx.x & 31, piece = lane % 8;
   __syncwarp();
   uint4 v[8];
-  unsigned long long dst[8];
+  int at[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = i * 4 + lane / 8;
     v[i] = *(const uint4*)(stage + row * 128 + (piece ^ (row & 7)) * 16);
-    dst[i] = __shfl_sync(0xffffffffu, (unsigned long long)to, row);
+    at[i] = __shfl_sync(0xffffffffu, to, row);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (dst[i]) *(uint4*)(dst[i] + piece * 16) = v[i];
+    if (at[i] >= 0) *(uint4*)(base + (long long)at[i] * pitch + piece * 16) = v[i];
   __syncwarp();
 }
 
-// Joins the partial sums of the unit's CTAs in their order.  A thread takes
-// four columns of a row, kItems of them at a time, and kAhead parts of each,
-// so that enough loads are in flight: many rows have few parts (a prompt's
-// unit that a range's end cuts), few rows many (a long context).
-template <typename E, int kD, typename S, int kItems, int kAhead>
+// Joins the partial sums of the unit's CTAs in their order.  kSpan threads
+// share a row, each kD / kSpan of its columns, and take kAhead parts at a
+// time, so that their loads are in flight together: many rows have few parts
+// (a prompt's unit that a range's end cuts), few rows many (a long context).
+template <typename E, int kD, typename S, int kSpan, int kAhead>
 __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& u, int c_first,
                                           int parts, bool begins_late) {
-  constexpr int kCols = kD / 4;
+  constexpr int kVecs = kD / 4 / kSpan;   // 16-byte pieces per thread, kSpan apart
   const size_t slots = (size_t)gridDim.x * 2;
   const float4* sums = (const float4*)a.partial;
   const float2* stats = (const float2*)(a.partial + slots * S::kRows * kD);
   const int rows0 = (u.last(0) - u.first(0)) * a.G;   // a second tile only where the first is full
-  const int items = u.rows() * kCols;
+  const int items = u.rows() * kSpan, col = threadIdx.x % kSpan;
 #pragma unroll 1
-  for (int x0 = threadIdx.x; x0 < items; x0 += kItems * S::kSoftThreads) {
-    int at[kItems];   // row of the slot
-    float4 o[kItems];
-    float m[kItems], l[kItems];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      const int r = min(x0 + i * S::kSoftThreads, items - 1) / kCols;
-      at[i] = r < rows0 ? r : 128 + r - rows0;
-      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      m[i] = SV_NEG_INF;
-      l[i] = 0.f;
-    }
+  for (int x = threadIdx.x; x < items; x += S::kSoftThreads) {
+    const int r = x / kSpan;
+    const int at = r < rows0 ? r : 128 + r - rows0;   // row of the slot
+    float m = SV_NEG_INF, l = 0.f;
+    float4 o[kVecs] = {};
 #pragma unroll 1
     for (int p0 = 0; p0 < parts; p0 += kAhead) {
-      float2 ml[kAhead][kItems];
-      float4 f[kAhead][kItems];
+      float2 ml[kAhead];
+      float4 f[kAhead][kVecs];
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int p = min(p0 + q, parts - 1);
-        const size_t slot = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows;
+        const size_t row = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows + at;
+        ml[q] = __ldcg(&stats[row]);
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-          ml[q][i] = __ldcg(&stats[slot + at[i]]);
-          f[q][i] = __ldcg(&sums[(slot + at[i]) * kCols + x0 % kCols]);
-          if (p0 + q >= parts) ml[q][i].x = SV_NEG_INF;
-        }
+        for (int v = 0; v < kVecs; ++v) f[q][v] = __ldcg(&sums[row * (kD / 4) + v * kSpan + col]);
+        if (p0 + q >= parts) ml[q].x = SV_NEG_INF;
       }
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
+      for (int q = 0; q < kAhead; ++q) {
+        // a part that sees none of the row's keys has -inf and zeros
+        const float top = fmaxf(m, ml[q].x), ref = top == SV_NEG_INF ? 0.f : top;
+        const float c0 = ex2_approx(m - ref), c1 = ex2_approx(ml[q].x - ref);
+        m = top;
+        l = l * c0 + ml[q].y * c1;
 #pragma unroll
-        for (int i = 0; i < kItems; ++i) {
-          // a part that sees none of the row's keys has -inf and zeros
-          const float2 e = ml[q][i];
-          const float top = fmaxf(m[i], e.x), ref = top == SV_NEG_INF ? 0.f : top;
-          const float c0 = ex2_approx(m[i] - ref), c1 = ex2_approx(e.x - ref);
-          m[i] = top;
-          l[i] = l[i] * c0 + e.y * c1;
-          o[i].x = o[i].x * c0 + f[q][i].x * c1;
-          o[i].y = o[i].y * c0 + f[q][i].y * c1;
-          o[i].z = o[i].z * c0 + f[q][i].z * c1;
-          o[i].w = o[i].w * c0 + f[q][i].w * c1;
+        for (int v = 0; v < kVecs; ++v) {
+          o[v].x = o[v].x * c0 + f[q][v].x * c1;
+          o[v].y = o[v].y * c0 + f[q][v].y * c1;
+          o[v].z = o[v].z * c0 + f[q][v].z * c1;
+          o[v].w = o[v].w * c0 + f[q][v].w * c1;
         }
+      }
     }
+    const int g = at % 128;
+    const long long to =
+        (long long)(u.units.row.begin + u.first(at / 128) + g / a.G) * a.Hq + u.h * a.G + g % a.G;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-      if (x0 + i * S::kSoftThreads >= items) break;
-      const int r = at[i] % 128;
-      const long long to = (long long)(u.units.row.begin + u.first(at[i] / 128) + r / a.G) * a.Hq +
-                           u.h * a.G + r % a.G;
-      const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-      *(uint2*)(a.out + (to * kD + x0 % kCols * 4) * 2) =
-          make_uint2(pack2(o[i].x * inv, o[i].y * inv, E()), pack2(o[i].z * inv, o[i].w * inv, E()));
-      if (a.lse && x0 % kCols == 0)
-        a.lse[to] = l[i] > 0.f ? (m[i] + log2f(l[i])) * kLn2 : SV_NEG_INF;
-    }
+    for (int v = 0; v < kVecs; ++v)
+      *(uint2*)(a.out + (to * kD + (v * kSpan + col) * 4) * 2) =
+          make_uint2(pack2(o[v].x * inv, o[v].y * inv, E()), pack2(o[v].z * inv, o[v].w * inv, E()));
+    if (a.lse && col == 0) a.lse[to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
   }
 }
 
@@ -711,9 +699,10 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
     if (any) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const long long to = (long long)(u.units.row.begin + token) * a.Hq + u.h * a.G + r % a.G;
-      const size_t part = slot * S::kRows + t * 128 + r;
-      char* dst = whole ? a.out + to * kD * 2 : (char*)(a.partial + part * kD);
+      // rows of `out` from the unit's first token and head, or rows of the slot
+      const long long unit = (long long)(u.units.row.begin + u.first(0)) * a.Hq + u.h * a.G;
+      const int to = !mine ? -1 : whole ? (token - u.first(0)) * a.Hq + r % a.G : t * 128 + r;
+      char* base = whole ? a.out + unit * kD * 2 : (char*)(a.partial + slot * S::kRows * kD);
 #pragma unroll 1
       for (int x = 0; x < kD; x += 32) {
         uint32_t bits[32] = {};
@@ -737,12 +726,13 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           for (int y = 0; y < 8; ++y)
             stage_piece(stage, y, bits[4 * y], bits[4 * y + 1], bits[4 * y + 2], bits[4 * y + 3]);
         }
-        store_staged(stage, mine ? dst : nullptr);
-        dst += 128;
+        store_staged(stage, base, to, whole ? kD * 2 : kD * 4);
+        base += 128;
       }
       if (mine) {
-        if (!whole) ((float2*)(a.partial + slots * S::kRows * kD))[part] = make_float2(m, l);
-        else if (a.lse) a.lse[to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
+        if (!whole)
+          ((float2*)(a.partial + slots * S::kRows * kD))[slot * S::kRows + to] = make_float2(m, l);
+        else if (a.lse) a.lse[unit + to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
       }
     }
     tc_fence_before();
@@ -764,9 +754,9 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     if (c->last) {
       const int parts = c_last - c_first + 1;
       if (u.rows() * (kD / 4) <= S::kSoftThreads)
-        attn_join<E, kD, S, 1, 8>(a, u, c_first, parts, begins_late);
+        attn_join<E, kD, S, kD / 4, 8>(a, u, c_first, parts, begins_late);
       else
-        attn_join<E, kD, S, 4, 2>(a, u, c_first, parts, begins_late);
+        attn_join<E, kD, S, 8, 2>(a, u, c_first, parts, begins_late);
     }
   }
 }
