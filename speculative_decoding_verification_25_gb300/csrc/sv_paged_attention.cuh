@@ -118,6 +118,7 @@ struct AttnUnits {
   }
   // weight of the first `units` units
   __device__ __forceinline__ long long before(int units) const {
+    if (units == 0) return 0;
     const int full = min(units, count - 1);   // the last may be short
     const int context = row.L - row.n;
     // units of less than a key tile
@@ -394,7 +395,6 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       release(&c->empty[it % S::kStages], i < cnt);
       ++it;
     }
-    if (ok && cnt <= S::kBufs) release(&c->q_empty, cnt > 0);
 #pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
       const int v_it = it++, k = done + i;
@@ -446,9 +446,12 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       else if (S::kTiles > 1) pass_turn(pass);
       release(&c->empty[v_it % S::kStages], active);
       if (another) release(&c->empty[k_it % S::kStages], next);
-      if (next && i + S::kBufs + 1 == cnt) release(&c->q_empty, true);
     }
     done += cnt;
+    // The last P came after the last scores, so Q is read no more.  Said no
+    // sooner: the next unit's Q tells both issuers that the other is past its
+    // last wait for P, whose turns the next unit may not count towards.
+    if (lane == 0) mbar_arrive(smem_addr(&c->q_empty));
   }
   // everything issued is done before the CTA's memory goes
   release(&c->drain, true);

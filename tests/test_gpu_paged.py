@@ -157,6 +157,11 @@ def _rows(seed, count, ctx, n):
     return [(int(c + m), int(m)) for c, m in zip(rng.integers(0, ctx + 1, count), new)]
 
 
+def _holes(rows):
+    """Finished requests (no token) and failed ones (no key) among the others."""
+    return [(L - n, 0) if b % 7 == 3 else (0, n) if b % 7 == 5 else (L, n) for b, (L, n) in enumerate(rows)]
+
+
 CASES = {
     "one_key": ([(1, 1)], 1, 1, 64, 8, "bf16"),
     "one_token": ([(1000, 1)], 32, 8, 128, 16, "bf16"),
@@ -181,6 +186,12 @@ CASES = {
     "many_tiles": (_rows(8, 60, 3000, 5), 16, 8, 128, 16, "bf16"),
     "many_tiles_64": (_rows(9, 150, 2500, 3), 8, 8, 64, 64, "f16"),
     "many_tiles_wide": (_rows(10, 40, 1500, 70), 8, 4, 64, 32, "bf16"),
+    "ragged_units": (_rows(11, 37, 1500, 167), 14, 2, 64, 8, "f16"),
+    "ragged_units_128": (_rows(12, 24, 900, 300), 8, 2, 128, 16, "bf16"),
+    "holes": (_holes(_rows(13, 70, 2500, 5)), 32, 8, 128, 32, "bf16"),
+    "holes_one_token": (_holes(_rows(14, 105, 400, 1)), 64, 8, 64, 128, "f16"),
+    "holes_wide": (_holes(_rows(15, 37, 1200, 167)), 14, 2, 64, 8, "f16"),
+    "holes_wide_128": (_holes(_rows(16, 24, 900, 120)), 16, 4, 128, 64, "bf16"),
     "split": ([(20011, 1)], 8, 1, 128, 64, "bf16"),
     "split_wide": ([(9000, 300)], 4, 1, 64, 32, "bf16"),
 }
@@ -188,9 +199,13 @@ CASES = {
 
 @pytest.mark.parametrize("name", CASES)
 def test_attention_matches_the_oracle(name):
+    import torch
+    from speculative_decoding_verification_25_gb300 import _native as N, api
     rows, *shape = CASES[name]
     c = PagedCase(rows, *shape, seed=len(name))
     c.check(c.run())
+    counters = api.attention_workspace(c.D, torch.device("cuda:0"))[:N.SV_ATTENTION_COUNTER_BYTES]
+    assert int(counters.sum()) == 0     # ready for the next call
 
 
 @pytest.mark.parametrize("spread", [0.02, 4.0])
@@ -271,7 +286,8 @@ def test_attention_flags_bad_lengths_and_pages():
     assert flags.item() & N.SV_DEV_BAD_LENGTH
 
 
-@pytest.mark.parametrize("name", ["verify", "many_tiles", "many_tiles_64", "mixed", "split", "split_wide", "empty_rows"])
+@pytest.mark.parametrize("name", ["verify", "many_tiles", "many_tiles_64", "ragged_units",
+                                  "ragged_units_128", "mixed", "split", "split_wide", "empty_rows"])
 def test_attention_gives_the_same_bits_every_time(name):
     import torch
     rows, *shape = CASES[name]
