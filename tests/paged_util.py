@@ -80,5 +80,5 @@ class PagedCase:
         off = np.abs(out - ref.out) - ref.out_tol
         assert (off <= 0).all(), f"out is {off.max():.3g} past its bound at {np.unravel_index(off.argmax(), off.shape)}"
         fine = np.isfinite(ref.lse)
-        off = np.abs(lse - ref.lse)[fine] - ref.lse_tol[fine]
+        off = np.abs(lse[fine] - ref.lse[fine]) - ref.lse_tol[fine]
         assert (off <= 0).all(), f"lse is {off.max():.3g} past its bound"
