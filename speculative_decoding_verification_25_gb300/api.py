@@ -311,7 +311,7 @@ def paged_plan(seq_len: torch.Tensor, num_new: torch.Tensor, page_count: torch.T
         if max_tokens < 0:
             raise ValueError("max_tokens must not be negative")
         with _on(stream):   # outputs belong to the stream that writes them
-            out = PagedPlan(*torch.empty(sum(sizes), dtype=torch.int32, device=dev).split(sizes))
+            out = PagedPlan(*[torch.empty(n, dtype=torch.int32, device=dev) for n in sizes])
         outs = [t.data_ptr() for t in out]
     else:
         outs = [_ints(t, "out." + name, (n,), dev)

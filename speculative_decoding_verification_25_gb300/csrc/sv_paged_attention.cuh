@@ -132,6 +132,7 @@ struct AttnUnits {
 // Where a CTA's range starts: `pos` keys into a unit.
 struct AttnStart {
   AttnRow row;
+  int count;     // units of the request
   int b, h, m, pos;
 };
 
@@ -163,7 +164,11 @@ struct AttnWalk {
   long long left;             // of the range, this unit's part included
 
   __device__ __forceinline__ AttnWalk(const AttnArgs& args, const AttnStart& s, long long length)
-      : a(args), units(args, s.row), b(s.b), h(s.h), m(s.m), pos(s.pos), left(length) {}
+      : a(args), b(s.b), h(s.h), m(s.m), pos(s.pos), left(length) {
+    units.row = s.row;
+    units.step = S::kTiles * a.tile_tokens;
+    units.count = s.count;
+  }
   // To the next unit of which the CTA has a tile, first of all to the first;
   // false at the end of the range.
   __device__ __forceinline__ bool next(bool first_of_all) {
@@ -491,26 +496,31 @@ __device__ __forceinline__ int take_ticket(int* ticket) {
 // 128 bytes of each of a warp's 32 rows, a row per lane, to global memory with
 // four whole segments per instruction: they pass through shared memory, their
 // 16-byte pieces placed so that neither side meets bank conflicts.  The
-// lane's segment is `to` pitches from `base`, none if negative.
+// lane's segment is `to` pitches from `base`, none if negative; the warp's
+// first `rows` have one.
 __device__ __forceinline__ void stage_piece(char* stage, int piece, uint32_t x, uint32_t y,
                                             uint32_t z, uint32_t w) {
   const int lane = threadIdx.x & 31;
   *(uint4*)(stage + lane * 128 + (piece ^ (lane & 7)) * 16) = make_uint4(x, y, z, w);
 }
-__device__ __forceinline__ void store_staged(const char* stage, char* base, int to, int pitch) {
+__device__ __forceinline__ void store_staged(const char* stage, char* base, int to, int pitch,
+                                             int rows) {
   const int lane = threadIdx.x & 31, piece = lane % 8;
   __syncwarp();
-  uint4 v[8];
-  int at[8];
+#pragma unroll 1
+  for (int i0 = 0; i0 < rows; i0 += 16) {
+    uint4 v[4];
+    int at[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = i * 4 + lane / 8;
-    v[i] = *(const uint4*)(stage + row * 128 + (piece ^ (row & 7)) * 16);
-    at[i] = __shfl_sync(0xffffffffu, to, row);
+    for (int i = 0; i < 4; ++i) {
+      const int row = i0 + i * 4 + lane / 8;
+      v[i] = *(const uint4*)(stage + row * 128 + (piece ^ (row & 7)) * 16);
+      at[i] = __shfl_sync(0xffffffffu, to, row);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at[i] >= 0) *(uint4*)(base + (long long)at[i] * pitch + piece * 16) = v[i];
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (at[i] >= 0) *(uint4*)(base + (long long)at[i] * pitch + piece * 16) = v[i];
   __syncwarp();
 }
 
@@ -586,7 +596,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
                                              uint32_t tmem, char* staging, long long quota,
                                              long long w1) {
   const int warp = threadIdx.x >> 5, t = warp / 4;
-  const int r = threadIdx.x % 128;                 // the thread's row of its query tile
+  const int r = threadIdx.x % 128;                 // the thread's row of its query tile:
+  const int r_token = r / a.G, r_head = r - r_token * a.G;   // a token and a head of the group
   const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
   const uint32_t o_col = tmem + lanes + S::kTiles * S::kBufs * S::kKeys + t * kD;
   char* stage = staging + warp * S::kStagingBytes;
@@ -596,9 +607,10 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
 #pragma unroll 1
   for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.count(t);
-    const int token = u.first(t) + r / a.G;
-    const bool mine = r < a.tile_tokens * a.G && token < u.units.row.n;
-    const bool any = __any_sync(0xffffffffu, mine);
+    const int token = u.first(t) + r_token;
+    const bool mine = r_token < a.tile_tokens && token < u.units.row.n;
+    const int rows = __popc(__ballot_sync(0xffffffffu, mine));   // the warp's first ones
+    const bool any = rows > 0;
     // keys that the row sees; rows without a token see none
     const int seen = mine ? max(0, u.units.row.L - u.units.row.n + token + 1) : 0;
     // the warp's first row sees the fewest of those with a token
@@ -704,7 +716,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       const float inv = l > 0.f ? 1.f / l : 0.f;
       // rows of `out` from the unit's first token and head, or rows of the slot
       const long long unit = (long long)(u.units.row.begin + u.first(0)) * a.Hq + u.h * a.G;
-      const int to = !mine ? -1 : whole ? (token - u.first(0)) * a.Hq + r % a.G : t * 128 + r;
+      const int to = !mine ? -1 : whole ? (token - u.first(0)) * a.Hq + r_head : t * 128 + r;
       char* base = whole ? a.out + unit * kD * 2 : (char*)(a.partial + slot * S::kRows * kD);
 #pragma unroll 1
       for (int x = 0; x < kD; x += 32) {
@@ -729,7 +741,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           for (int y = 0; y < 8; ++y)
             stage_piece(stage, y, bits[4 * y], bits[4 * y + 1], bits[4 * y + 2], bits[4 * y + 3]);
         }
-        store_staged(stage, base, to, whole ? kD * 2 : kD * 4);
+        store_staged(stage, base, to, whole ? kD * 2 : kD * 4, rows);
         base += 128;
       }
       if (mine) {
@@ -811,14 +823,15 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   // -------- weights of all requests, summed: thread i has rows [r0, r1)
   const int per = (a.B + S::kThreads - 1) / S::kThreads;
   const int r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
-  auto weight = [&](int b, bool* bad) -> long long {
-    const AttnUnits<S> units(a, attn_row(a, b, bad));
-    return units.before(units.count) * a.Hk;
-  };
   bool bad = false;
-  long long mine = 0;
+  long long mine = 0, head = 0;   // weight of the thread's requests; of one head of the last
+  AttnUnits<S> units;
 #pragma unroll 1
-  for (int b = r0; b < r1; ++b) mine += weight(b, &bad);
+  for (int b = r0; b < r1; ++b) {
+    units = AttnUnits<S>(a, attn_row(a, b, &bad));
+    head = units.before(units.count);
+    mine += head * a.Hk;
+  }
   if (bad && blockIdx.x == 0) set_flag(a.flags, kDevLength);
   long long inc = mine;
 #pragma unroll
@@ -831,7 +844,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   __syncthreads();
   tc_fence_after();
   long long before = 0, total = 0;
-#pragma unroll 1
+#pragma unroll
   for (int w = 0; w < S::kThreads / 32; ++w) {
     if (w < warp) before += c->sums[w];
     total += c->sums[w];
@@ -849,17 +862,22 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     if (per > 1 && (holds >> lane & 1)) {
 #pragma unroll 1
       for (;; ++b) {
-        const long long wb = weight(b, nullptr);
-        if (w0 < begin + wb) break;
-        begin += wb;
+        units = AttnUnits<S>(a, attn_row(a, b));
+        head = units.before(units.count);
+        if (w0 < begin + head * a.Hk) break;
+        begin += head * a.Hk;
       }
     }
     const int from = __ffs(holds) - 1;
     b = __shfl_sync(0xffffffffu, b, from);
+    head = __shfl_sync(0xffffffffu, head, from);
     long long off = w0 - __shfl_sync(0xffffffffu, begin, from);
-    const AttnUnits<S> units(a, attn_row(a, b));
-    const long long head = units.before(units.count);
-    int h = min(a.Hk - 1, (int)((float)off / (float)head));
+    units.row.begin = __shfl_sync(0xffffffffu, units.row.begin, from);
+    units.row.n = __shfl_sync(0xffffffffu, units.row.n, from);
+    units.row.L = __shfl_sync(0xffffffffu, units.row.L, from);
+    units.count = __shfl_sync(0xffffffffu, units.count, from);
+    units.step = S::kTiles * a.tile_tokens;
+    int h = min(a.Hk - 1, (int)__fdividef((float)off, (float)head));   // about, then exactly
 #pragma unroll 1
     while (h * head > off) --h;
 #pragma unroll 1
@@ -878,6 +896,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     }
     if (lane == 0) {
       c->start.row = units.row;
+      c->start.count = units.count;
       c->start.b = b;
       c->start.h = h;
       c->start.m = lo;
