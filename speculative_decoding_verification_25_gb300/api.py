@@ -276,8 +276,9 @@ def _flags_ptr(flags, dev):
 
 
 def _stream_handle(stream, dev):
-    """The raw handle of ``stream``, the device's current one if None."""
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    """The raw handle of ``stream``, the device's current one if None (without
+    the Stream object, whose making costs as much as a kernel's launch)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
 
 
 def _on(stream):

@@ -142,6 +142,7 @@ struct AttnControl {   // at the end of the shared memory
   uint64_t s_full[2][2], p_ready[2][2];   // [tile][buffer]
   uint64_t pv_done[2];
   uint32_t tmem;
+  volatile int past;          // units whose P the second tile's issuer has seen
   int abort_word;
   int calm;                   // an abort word that stays 0, for the waits of a CTA that gives up
   int last;
@@ -328,6 +329,20 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
 }
 
 // ----------------------------------------------------------------- products
+// A count and not a barrier: a tile without products may be units ahead, and a
+// wait for a phase sees its parity alone.
+__device__ __forceinline__ bool wait_past(AttnControl* c, int units) {
+  bool ok = c->past >= units;
+#pragma unroll 1
+  for (int i = 0; !ok && i < kNaps && !*(volatile int*)&c->abort_word; ++i) {
+    __nanosleep(64);
+    ok = c->past >= units;
+  }
+  ok = __all_sync(0xffffffffu, ok);
+  if (!ok) *(volatile int*)&c->abort_word = 1;
+  return ok;
+}
+
 // One warp per query tile.  A product's issue lasts as long as the tensor core
 // takes to accept it, so what a warp does between products (waits, commits)
 // would leave the tensor core idle; the other tile's warp fills that.  The
@@ -390,7 +405,11 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.most(), cnt = u.count(t), other = S::kTiles > 1 ? u.count(1 - t) : 0;
     if (n == 0) continue;
-    if (!(ok = mbar_wait(smem_addr(&c->q_full), rounds++ & 1, &c->abort_word))) break;
+    if (!(ok = mbar_wait(smem_addr(&c->q_full), rounds & 1, &c->abort_word))) break;
+    // The turns that the first tile gives belong to one unit: the second tile's
+    // issuer must be past its last wait for P of the unit before.
+    if (S::kTiles > 1 && t == 0 && !(ok = wait_past(c, rounds))) break;
+    ++rounds;
     tc_fence_after();
 #pragma unroll 1
     for (int i = 0; i < min(n, S::kBufs); ++i) {
@@ -400,6 +419,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       release(&c->empty[it % S::kStages], i < cnt);
       ++it;
     }
+    if (ok && cnt <= S::kBufs) release(&c->q_empty, cnt > 0);   // its last scores are issued
 #pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
       const int v_it = it++, k = done + i;
@@ -451,12 +471,10 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       else if (S::kTiles > 1) pass_turn(pass);
       release(&c->empty[v_it % S::kStages], active);
       if (another) release(&c->empty[k_it % S::kStages], next);
+      if (next && i + S::kBufs + 1 == cnt) release(&c->q_empty, true);
     }
     done += cnt;
-    // The last P came after the last scores, so Q is read no more.  Said no
-    // sooner: the next unit's Q tells both issuers that the other is past its
-    // last wait for P, whose turns the next unit may not count towards.
-    if (lane == 0) mbar_arrive(smem_addr(&c->q_empty));
+    if (S::kTiles > 1 && t == 1 && lane == 0) c->past = rounds;
   }
   // everything issued is done before the CTA's memory goes
   release(&c->drain, true);
@@ -811,7 +829,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
       mbar_init(smem_addr(&c->pv_done[t]), 1);
     }
     mbar_init_fence();
-    c->abort_word = c->calm = 0;
+    c->abort_word = c->calm = c->past = 0;
     tma_prefetch_map(&q_map);
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
