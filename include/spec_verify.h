@@ -66,8 +66,9 @@ extern "C" {
 /* status codes returned by the host entry points */
 #define SV_OK 0
 #define SV_ERR_NULL 1       /* a required pointer is NULL */
-#define SV_ERR_SHAPE 2      /* B < 0, K outside [1, SV_MAX_K], V outside [1, spec_verify_max_vocab(dtype)] */
-#define SV_ERR_DTYPE 3      /* dtype is neither SV_F32 nor SV_BF16 */
+#define SV_ERR_SHAPE 2      /* B < 0, K outside [1, SV_MAX_K], V outside [1, spec_verify_max_vocab(dtype)];
+                               other entry points say which sizes they take */
+#define SV_ERR_DTYPE 3      /* dtype is neither SV_F32 nor SV_BF16 (paged operators: SV_BF16, SV_F16) */
 #define SV_ERR_ALIGN 4      /* a pointer is not aligned to its element (workspace: 16 bytes) */
 #define SV_ERR_WORKSPACE 5  /* workspace_bytes < spec_verify_workspace_bytes(B, K, V, dtype) */
 #define SV_ERR_CUDA 6       /* a CUDA runtime call failed (launch, attribute, copy) */
@@ -79,7 +80,8 @@ extern "C" {
 #define SV_DEV_NONFINITE 4u        /* a logit row without a finite maximum or sum */
 #define SV_DEV_BAD_K 8u            /* spec_verify_ragged: k_per_row[b] outside [0, K] */
 #define SV_DEV_PLUG_CLIPPED 16u    /* spec_verify_plug: a row's tokens did not all fit */
-#define SV_DEV_BAD_LENGTH 32u      /* spec_verify_plug: seq_len[b] outside [0, max_len] */
+#define SV_DEV_BAD_LENGTH 32u      /* spec_verify_plug: seq_len[b] outside [0, max_len]; paged
+                                      operators: a length, offset or count out of range */
 #define SV_DEV_BAD_TREE 64u        /* spec_verify_tree: a parent or node token out of range */
 #define SV_DEV_OUT_OF_BOUNDS 256u  /* checked build only (libspec_verify_checked.so, compiled with
                                       -DSV_CHECKED): an index failed its bounds test and the
@@ -359,7 +361,8 @@ int spec_verify_and_plug(const void* target_logits, const void* draft_logits, in
  * request b owns tokens cu_new[b] .. cu_new[b+1]-1 of every packed array.
  * The cache is k_cache, v_cache [n_pages, Hk, page_size, D], dense; slot
  * s = page * page_size + offset names one token's place.  page_size is a
- * power of two in [8, 256]; n_pages * page_size < 2^31 (offsets into the
+ * power of two in [8, 256]; n_pages * page_size < 2^31, and for
+ * spec_paged_attention n_pages * page_size * Hk < 2^31 (offsets into the
  * cache are 64 bits wide).
  *
  * `flags` is one uint32 on the device, or NULL: SV_DEV_* bits are OR-ed into

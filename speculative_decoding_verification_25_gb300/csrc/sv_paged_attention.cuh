@@ -4,30 +4,44 @@
 // sum_j 2^(s_j - r) v_j / sum_j 2^(s_j - r).  Keys are taken a tile at a time;
 // r follows the running maximum only when that has risen by more than
 // kSlack, so a tile seldom has to scale what was summed before it, and the
-// probabilities stay below 2^kSlack.
+// probabilities stay below 2^kSlack.  (Three whole prompts of 4000 to 8192
+// tokens: 774 us; following every rise, 832 us.)
 //
 // Both products run on the tensor core (tcgen05).  A query tile is 128 rows:
 // the G query heads of one key head for 128 / G consecutive tokens, since
 // they share every key and value.  S = Q K^T goes to tensor memory; four
 // warps take it a row per thread, leave P = 2^(S - r), rounded to the
-// operands' type, in the place of S, and O += P V reads P from there.  Rows
-// never meet: no shuffle, and unused rows may hold anything.
+// operands' type (the product takes no other), in the place of S, and
+// O += P V reads P from there.  All sums are float32.  Rows never meet: no
+// shuffle, and unused rows may hold anything.
 //
 // A CTA is one loader warp (TMA into a ring of key and value tiles) and, per
 // query tile, one warp that issues the products and four softmax warps.
 // Two forms:
 //   wide    two query tiles of one unit against tiles of 128 keys: while one
-//           tile's softmax runs, the tensor core works on the other's;
+//           tile's softmax runs, the tensor core works on the other's.  Bound
+//           by the chain of a tile (scores, softmax, products, and a hand-over
+//           between each), about 3300 clocks per 256 x 128 scores of which the
+//           tensor core is busy for 2048: 1.42 PFLOP/s on chunks of 2048
+//           tokens over contexts of 5000 to 7000.
 //   narrow  one query tile against tiles of 64 keys, two S buffers, and two
 //           CTAs per SM: for up to 128 rows per request, where the time is
-//           that of reading the cache.
+//           that of reading the cache: 6.6 to 6.7 TB/s on long contexts.
+// TMEM holds 128 lanes x 512 columns: wide fills it at D = 128 with S (P in
+// its place) and O of both tiles, 4 x 128.  Tiles of 64 keys with two S
+// buffers instead made prompts slower (a product of 64 columns takes 58
+// clocks, one of 128 columns 64).
 //
-// The work is all (request, key head, query unit, key tile) quadruples in
-// that order, cut into equal ranges, one per CTA: every CTA sums the rows'
-// tiles to find its range, so no length is needed on the host.  A unit that
+// The work is the key tiles of all (request, key head, query unit) in that
+// order, cut into equal ranges of keys, one per CTA: every CTA sums the rows'
+// keys to find its range, so no length is needed on the host.  A unit that
 // a range's end cuts leaves unnormalised sums in the workspace; the CTA that
 // takes the unit's last ticket joins them, always in the order of the CTAs,
 // so results do not depend on timing and no CTA waits for another.
+//
+// The kernel's text is kept short (out-of-line or rolled wherever it is not
+// in the inner loop): at 160 KB, with runtime loops unrolled, a prompt of
+// 4096 tokens took 200 us, at about 100 KB 157 us.
 #pragma once
 
 #include <cuda_bf16.h>
