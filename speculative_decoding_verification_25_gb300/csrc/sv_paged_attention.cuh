@@ -15,8 +15,8 @@
 // O += P V reads P from there.  All sums are float32.  Rows never meet: no
 // shuffle, and unused rows may hold anything.
 //
-// A CTA is one loader warp (TMA into a ring of key and value tiles) and, per
-// query tile, one warp that issues the products and four softmax warps.
+// A CTA is one or two loader warps (TMA into a ring of key and value tiles) and,
+// per query tile, one warp that issues the products and four softmax warps.
 // Two forms:
 //   wide    two query tiles of one unit against tiles of 128 keys: while one
 //           tile's softmax runs, the tensor core works on the other's.  Bound
@@ -38,10 +38,6 @@
 // a range's end cuts leaves unnormalised sums in the workspace; the CTA that
 // takes the unit's last ticket joins them, always in the order of the CTAs,
 // so results do not depend on timing and no CTA waits for another.
-//
-// The kernel's text is kept short (out-of-line or rolled wherever it is not
-// in the inner loop): at 160 KB, with runtime loops unrolled, a prompt of
-// 4096 tokens took 200 us, at about 100 KB 157 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -83,6 +79,7 @@ struct AttnShape {
   static constexpr int kQBytes = 128 * kD * 2;
   static constexpr int kStageBytes = kKeys * kD * 2;
   static constexpr int kStages = kD == 128 ? 4 : 8;  // what is left of the shared memory
+  static_assert(kStages % 2 == 0 || !kWide, "keys and values keep to their slots");
   static constexpr int kStagingBytes = 32 * 128;     // of a warp: rows on their way out
   static constexpr int kSoftThreads = 128 * kTiles;
   // wide: whole warpgroups, so that the softmax can take registers from the rest
@@ -261,13 +258,17 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
 }
 
 // ------------------------------------------------------------------- loader
-// One warp.  A key or value tile is kKeys rows of one head, a box of
-// min(page, kKeys) rows per page and 128-byte column block; each lane brings
-// one box.  Rows of pages past the request's length stay as they are.
+// One warp, in the wide form one for queries and keys and one for values (two
+// prompt chunks, pages of 16: 367 and 334 us, pages of 8: 519 and 355 us).  A key or value tile is kKeys rows of
+// one head, a box of min(page, kKeys) rows per page and 128-byte column block;
+// each lane brings one box.  Rows of pages past the request's length stay as
+// they are.  Keys and values alternate in the ring, and its slots are even in
+// number, so a slot is always the same warp's.
 template <typename S>
 __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
                                           uint32_t q_smem, uint32_t ring, const CUtensorMap* q_map,
-                                          const CUtensorMap* k_map, const CUtensorMap* v_map) {
+                                          const CUtensorMap* k_map, const CUtensorMap* v_map,
+                                          bool keys, bool values) {
   const int lane = threadIdx.x & 31;
   const int page = 1 << a.page_shift;
   const int box = min(page, S::kKeys);
@@ -287,8 +288,10 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
     // past the last row of the cache the box fills with zeros
     return ((inside ? id * a.Hk + u.h : a.n_pages * a.Hk) << a.page_shift) + (key & (page - 1));
   };
-  auto bring = [&](const CUtensorMap* map, int y) -> bool {
+  auto bring = [&](const CUtensorMap* map, int y, bool ours) -> bool {
     const int stage = it % S::kStages, lap = it / S::kStages;
+    ++it;
+    if (!ours) return true;
     if (lap > 0 && !mbar_wait(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word))
       return false;
     const uint32_t bar = smem_addr(&c->full[stage]);
@@ -296,7 +299,6 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
     if (lane == 0) mbar_arrive_expect(bar, __popc(who) * box * 128);
     __syncwarp();
     if (y >= 0) tma_load_2d(my_dst + stage * S::kStageBytes, map, my_block * 64, y, bar);
-    ++it;
     return true;
   };
 
@@ -309,26 +311,28 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
     for (int i = 0; i < S::kBufs; ++i) y[i] = box_row(u.j0 + i);
 #pragma unroll
     for (int i = 0; i < S::kBufs; ++i)
-      if (ok && i < n) ok = bring(k_map, y[i]);
-    if (!ok || (rounds > 0 && !(ok = mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1,
-                                               &c->abort_word))))
-      break;
-    ++rounds;
-    const uint32_t bar = smem_addr(&c->q_full);
-    const int q_tile = lane / S::kBlocks;
-    const bool mine = q_tile < S::kTiles && u.count(q_tile) > 0;
-    const unsigned who = __ballot_sync(0xffffffffu, mine);
-    if (lane == 0) mbar_arrive_expect(bar, __popc(who) * a.tile_tokens * a.G * 128);
-    __syncwarp();
-    if (mine)
-      tma_load_3d(q_smem + q_tile * S::kQBytes + my_block * 128 * 128, q_map, my_block * 64,
-                  u.h * a.G, u.units.row.begin + u.first(q_tile), bar);
+      if (ok && i < n) ok = bring(k_map, y[i], keys);
+    if (ok && keys) {
+      if (rounds > 0 &&
+          !(ok = mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1, &c->abort_word)))
+        break;
+      ++rounds;
+      const uint32_t bar = smem_addr(&c->q_full);
+      const int q_tile = lane / S::kBlocks;
+      const bool mine = q_tile < S::kTiles && u.count(q_tile) > 0;
+      const unsigned who = __ballot_sync(0xffffffffu, mine);
+      if (lane == 0) mbar_arrive_expect(bar, __popc(who) * a.tile_tokens * a.G * 128);
+      __syncwarp();
+      if (mine)
+        tma_load_3d(q_smem + q_tile * S::kQBytes + my_block * 128 * 128, q_map, my_block * 64,
+                    u.h * a.G, u.units.row.begin + u.first(q_tile), bar);
+    }
 #pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
       const bool another = i + S::kBufs < n;
       y[S::kBufs] = another ? box_row(u.j0 + i + S::kBufs) : -1;
-      ok = bring(v_map, y[0]);
-      if (ok && another) ok = bring(k_map, y[S::kBufs]);
+      ok = bring(v_map, y[0], values);
+      if (ok && another) ok = bring(k_map, y[S::kBufs], keys);
 #pragma unroll
       for (int x = 0; x < S::kBufs; ++x) y[x] = y[x + 1];
     }
@@ -850,7 +854,6 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   }
   if (warp == kIssuer) tmem_alloc<S::kTmemCols>(smem_addr(&c->tmem));
   wait_for_preceding_grid();
-  allow_dependent_launch();
 
   // -------- weights of all requests, summed: thread i has rows [r0, r1)
   const int per = (a.B + S::kThreads - 1) / S::kThreads;
@@ -875,6 +878,9 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Only now, with this CTA's tensor memory taken: a CTA of the next grid that
+  // held it while it waits for this grid would keep this CTA from starting.
+  allow_dependent_launch();
   long long before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < S::kThreads / 32; ++w) {
@@ -943,9 +949,11 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     // wide: three warpgroups launched with 168 registers a thread; 2 x 208 + 88 = 3 x 168
     if (warp >= kLoader) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-      if (warp == kLoader) attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map);
-      else if (warp < kIssuer + S::kTiles)
+      if (warp >= kIssuer && warp < kIssuer + S::kTiles)
         attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem, warp - kIssuer);
+      else
+        attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map, warp == kLoader,
+                     !kWide || warp != kLoader);
     } else {
       if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
       attn_softmax<E, kD, S>(a, u, c, tmem, staging, quota, w1);

@@ -45,8 +45,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 // Waits until the phase is over; false if the wait was given up, after kNaps
-// polls or once the CTA has given up elsewhere.  Kept short: waits are many,
-// and the instruction cache is small.
+// polls or once the CTA has given up elsewhere.
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_word) {
 #pragma unroll 1
   for (int i = 0; i < kNaps; ++i) {
