@@ -84,6 +84,10 @@ struct AttnShape {
   static constexpr int kSoftThreads = 128 * kTiles;
   // wide: whole warpgroups, so that the softmax can take registers from the rest
   static constexpr int kThreads = kSoftThreads + (kWide ? 128 : 64);
+  // A unit's start and end, in keys.  Whole prompts / 37 ragged requests / 64
+  // x 5 tokens: 727 / 72 / 102 us at 0, 663 / 56 / 97 so, 701 / 63 / 98 at
+  // 768 and 256.
+  static constexpr int kUnitCost = kWide ? 256 : 128;
   static constexpr int kCtasPerSm = kWide ? 1 : 2;
   static constexpr int kTmemCols = kWide ? 512 : 256;
   static constexpr int kRows = 128 * kTiles;
@@ -110,8 +114,9 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, int b, bool* bad 
 }
 // The query units of a request: kTiles tiles of tile_tokens tokens each.  A
 // unit's weight is the number of keys that its last token sees, or one key
-// tile where that is more, so that weights sum in closed form; the last unit's
-// is rounded up to key tiles, so that short contexts are cut between tiles.
+// tile where that is more, and kUnitCost, so that weights sum in closed form;
+// the last unit's keys are rounded up to key tiles, so that short contexts are
+// cut between tiles.
 template <typename S>
 struct AttnUnits {
   AttnRow row;
@@ -123,7 +128,7 @@ struct AttnUnits {
       : row(r), step(S::kTiles * a.tile_tokens), count((r.n + step - 1) / step) {}
   // keys that the request's tokens up to t1 see
   __device__ __forceinline__ int seen(int t1) const { return max(0, row.L - row.n + t1); }
-  __device__ __forceinline__ int weight(int m) const {
+  __device__ __forceinline__ int keys(int m) const {
     if (m < count - 1) return max(S::kKeys, seen((m + 1) * step));
     return max(S::kKeys, (seen(row.n) + S::kKeys - 1) / S::kKeys * S::kKeys);
   }
@@ -135,8 +140,8 @@ struct AttnUnits {
     // units of less than a key tile
     const int few = context < S::kKeys ? min(full, (S::kKeys - 1 - context) / step) : 0;
     const long long i0 = few + 1, i1 = full;
-    return (long long)few * S::kKeys + (i1 - few) * context + (i1 - few) * (i0 + i1) / 2 * step +
-           (units > full ? weight(count - 1) : 0);
+    return (long long)units * S::kUnitCost + (long long)few * S::kKeys + (i1 - few) * context +
+           (i1 - few) * (i0 + i1) / 2 * step + (units > full ? keys(count - 1) : 0);
   }
 };
 
@@ -187,7 +192,7 @@ struct AttnWalk {
 #pragma unroll 1
     while (true) {
       if (!first_of_all) {
-        left -= units.weight(m) - pos;
+        left -= units.keys(m) + S::kUnitCost - pos;
         if (left <= 0) return false;
         pos = 0;
         if (++m == units.count) {
@@ -199,10 +204,10 @@ struct AttnWalk {
         }
       }
       first_of_all = false;
-      const int weight = units.weight(m);
-      tiles = (weight + S::kKeys - 1) / S::kKeys;
+      const int keys = units.keys(m);
+      tiles = (keys + S::kKeys - 1) / S::kKeys;
       j0 = (pos + S::kKeys - 1) / S::kKeys;
-      j1 = left >= weight - pos ? tiles : (pos + (int)left + S::kKeys - 1) / S::kKeys;
+      j1 = left >= keys - pos ? tiles : (pos + (int)left + S::kKeys - 1) / S::kKeys;
       if (j0 < j1) return true;
     }
   }
