@@ -86,7 +86,7 @@ struct AttnShape {
   static constexpr int kThreads = kSoftThreads + (kWide ? 128 : 64);
   // A unit's start and end, in keys.  Wide, whole prompts / 37 ragged requests:
   // 727 / 72 us at 0, 662 / 56 at 256, 701 / 63 at 768.  Narrow, 64 x 5 tokens
-  // / 16 x 1 tokens of long caches: 99.0 / 228.5 us at 32, 98.0 / 227.9 at 64,
+  // / 4 x 1 tokens over long caches: 99.0 / 228.5 us at 32, 98.0 / 227.9 at 64,
   // 98.0 / 228.3 at 128, 98.6 / 228.6 at 192.
   static constexpr int kUnitCost = kWide ? 256 : 64;
   static constexpr int kCtasPerSm = kWide ? 1 : 2;
