@@ -413,7 +413,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     any token stride) over the paged cache [n_pages, Hk, page_size, D]
     (spec_paged_attention).  Request b has tokens cu_new[b]..cu_new[b+1]-1,
     the last of its ``kv_len[b]`` cached ones; a token that sees no key gets
-    zeros.  ``scale`` defaults to D ** -0.5."""
+    zeros.  ``scale`` defaults to D ** -0.5.  A ``workspace`` of the caller's
+    (spec_paged_attention_workspace_bytes) has its first
+    SV_ATTENTION_COUNTER_BYTES zero before its first use, and is used by one
+    call at a time."""
     dt, n_pages, Hk, page_size, D = _check_cache(k_cache, v_cache)
     dev = k_cache.device
     if q.dim() != 3:

@@ -5,7 +5,7 @@
 // r follows the running maximum only when that has risen by more than
 // kSlack, so a tile seldom has to scale what was summed before it, and the
 // probabilities stay below 2^kSlack.  (Three whole prompts of 4000 to 8192
-// tokens: 774 us; following every rise, 832 us.)
+// tokens: 648 us; following every rise, 745 us.)
 //
 // Both products run on the tensor core (tcgen05).  A query tile is 128 rows:
 // the G query heads of one key head for 128 / G consecutive tokens, since
@@ -20,10 +20,11 @@
 // Two forms:
 //   wide    two query tiles of one unit against tiles of 128 keys: while one
 //           tile's softmax runs, the tensor core works on the other's.  Bound
-//           by the chain of a tile (scores, softmax, products, and a hand-over
-//           between each), about 3300 clocks per 256 x 128 scores of which the
-//           tensor core is busy for 2048: 1.42 PFLOP/s on chunks of 2048
-//           tokens over contexts of 5000 to 7000.
+//           by the chain of a tile, about 3100 clocks per 256 x 128 scores, of
+//           which the tensor core is busy for 2048: from P to the next S about
+//           1600 (the products' 1024, their start, the hand-overs), then a
+//           softmax of 1450.  1.49 PFLOP/s on chunks of 2048 tokens over
+//           contexts of 5000 to 7000.
 //   narrow  one query tile against tiles of 64 keys, two S buffers, and two
 //           CTAs per SM: for up to 128 rows per request, where the time is
 //           that of reading the cache: 6.6 to 6.7 TB/s on long contexts.
@@ -85,7 +86,8 @@ struct AttnShape {
   // wide: whole warpgroups, so that the softmax can take registers from the rest
   static constexpr int kThreads = kSoftThreads + (kWide ? 128 : 64);
   // A unit's start and end, in keys.  Wide, whole prompts / 37 ragged requests:
-  // 727 / 72 us at 0, 662 / 56 at 256, 701 / 63 at 768.  Narrow, 64 x 5 tokens
+  // 659 / 57 us at 192, 648 / 55 at 256, 648 / 55.4 at 320 (none of it cost
+  // 727 / 72 where 256 had 663 / 56, and 768 had 701 / 63).  Narrow, 64 x 5 tokens
   // / 4 x 1 tokens over long caches: 99.0 / 228.5 us at 32, 98.0 / 227.9 at 64,
   // 98.0 / 228.3 at 128, 98.6 / 228.6 at 192.
   static constexpr int kUnitCost = kWide ? 256 : 64;
@@ -227,6 +229,28 @@ struct AttnWalk {
     }
     units = AttnUnits<S>(a, attn_row(a, b));
   }
+  // The wide form's softmax needs its registers for the scores: its loop over the
+  // tiles leaves the walk in shared memory (three whole prompts: 665 and, with
+  // the registers' split that then is best, 648 us).
+  __device__ __forceinline__ void park(int4* p) const {
+    if (S::kTiles == 1) return;
+    if ((threadIdx.x & 31) == 0) {
+      p[0] = make_int4(units.row.begin, units.row.n, units.row.L, units.count);
+      p[1] = make_int4(units.step, b, h, m);
+      p[2] = make_int4(pos, j0, j1, tiles);
+      *(long long*)(p + 3) = left;
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void unpark(const int4* p) {
+    if (S::kTiles == 1) return;
+    const int4 x = p[0], y = p[1], z = p[2];
+    left = *(const long long*)(p + 3);
+    units.row.begin = x.x, units.row.n = x.y, units.row.L = x.z, units.count = x.w;
+    units.step = y.x, b = y.y, h = y.z, m = y.w;
+    pos = z.x, j0 = z.y, j1 = z.z, tiles = z.w;
+    __syncwarp();
+  }
   // Query tile t of the unit: its tokens [first, last) within the request,
   // and how many of the unit's key tiles it needs of this CTA.
   __device__ __forceinline__ int first(int t) const { return (m * S::kTiles + t) * a.tile_tokens; }
@@ -265,11 +289,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
 
 // ------------------------------------------------------------------- loader
 // One warp, in the wide form one for queries and keys and one for values (two
-// prompt chunks, pages of 16: 367 and 334 us, pages of 8: 519 and 355 us).  A key or value tile is kKeys rows of
-// one head, a box of min(page, kKeys) rows per page and 128-byte column block;
-// each lane brings one box.  Rows of pages past the request's length stay as
-// they are.  Keys and values alternate in the ring, and its slots are even in
-// number, so a slot is always the same warp's.
+// prompt chunks, pages of 16: one warp 362 us, two 321; pages of 8: 516 and
+// 347).  A key or value tile is kKeys rows of one head, a box of min(page,
+// kKeys) rows per page and 128-byte column block; each lane brings one box.
+// Rows of pages past the request's length stay as they are.  Keys and values
+// alternate in the ring, and its slots are even in number, so a slot is always
+// the same warp's.
 template <typename S>
 __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
                                           uint32_t q_smem, uint32_t ring, const CUtensorMap* q_map,
@@ -658,8 +683,10 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     // the warp's first row sees the fewest of those with a token
     const int fewest = __shfl_sync(0xffffffffu, seen, 0);
     float m = SV_NEG_INF, l = 0.f;
+    int key0 = u.j0 * S::kKeys;   // the tile's first key
+    u.park((int4*)stage);
 #pragma unroll 1
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < n; ++i, key0 += S::kKeys) {
       const int k = done + i, buf = k % S::kBufs;
       if (!(ok = mbar_wait(smem_addr(&c->s_full[t][buf]), (k / S::kBufs) & 1, &c->abort_word)))
         break;
@@ -671,8 +698,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
         for (int x = 0; x < S::kKeys; x += 32) tmem_load32(s_col + x, bits + x);
         tmem_wait_load();
         tmem_pin<S::kKeys>(bits);
-        const int left = seen - (u.j0 + i) * S::kKeys;   // keys of the tile that the row sees
-        if (fewest < (u.j0 + i + 1) * S::kKeys) {
+        const int left = seen - key0;   // keys of the tile that the row sees
+        if (fewest < key0 + S::kKeys) {
 #pragma unroll
           for (int x = 0; x < S::kKeys; ++x)
             if (x >= left) bits[x] = 0xff800000u;
@@ -735,6 +762,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       hand_over(&c->p_ready[t][buf]);
     }
     if (!ok) break;
+    u.unpark((const int4*)stage);
     done += n;
     // one S buffer: one arrival per unit, else one per tile
     if (n > 0)
@@ -952,16 +980,18 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
 
   if (w0 < w1) {
     const AttnWalk<S> u(a, c->start, w1 - w0);
-    // wide: three warpgroups launched with 168 registers a thread; 2 x 208 + 88 = 3 x 168
+    // Wide: three warpgroups launched with 168 registers a thread, and
+    // 2 x 216 + 72 = 3 x 168.  Three whole prompts: 655 us with 208 and 88, 648
+    // so, 816 with 224 and 56, which the issuers cannot do with.
     if (warp >= kLoader) {
-      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp >= kIssuer && warp < kIssuer + S::kTiles)
         attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem, warp - kIssuer);
       else
         attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map, warp == kLoader,
                      !kWide || warp != kLoader);
     } else {
-      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
       attn_softmax<E, kD, S>(a, u, c, tmem, staging, quota, w1);
     }
   }
