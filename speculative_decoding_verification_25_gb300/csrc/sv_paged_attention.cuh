@@ -5,7 +5,7 @@
 // r follows the running maximum only when that has risen by more than
 // kSlack, so a tile seldom has to scale what was summed before it, and the
 // probabilities stay below 2^kSlack.  (Three whole prompts of 4000 to 8192
-// tokens: 648 us; following every rise, 745 us.)
+// tokens: 633 us; following every rise, 728 us.)
 //
 // Both products run on the tensor core (tcgen05).  A query tile is 128 rows:
 // the G query heads of one key head for 128 / G consecutive tokens, since
@@ -20,10 +20,10 @@
 // Two forms:
 //   wide    two query tiles of one unit against tiles of 128 keys: while one
 //           tile's softmax runs, the tensor core works on the other's.  Bound
-//           by the chain of a tile, about 3100 clocks per 256 x 128 scores, of
+//           by the chain of a tile, about 3000 clocks per 256 x 128 scores, of
 //           which the tensor core is busy for 2048: from P to the next S about
 //           1600 (the products' 1024, their start, the hand-overs), then a
-//           softmax of 1450.  1.49 PFLOP/s on chunks of 2048 tokens over
+//           softmax of 1350.  1.52 PFLOP/s on chunks of 2048 tokens over
 //           contexts of 5000 to 7000.
 //   narrow  one query tile against tiles of 64 keys, two S buffers, and two
 //           CTAs per SM: for up to 128 rows per request, where the time is
@@ -230,8 +230,8 @@ struct AttnWalk {
     units = AttnUnits<S>(a, attn_row(a, b));
   }
   // The wide form's softmax needs its registers for the scores: its loop over the
-  // tiles leaves the walk in shared memory (three whole prompts: 665 and, with
-  // the registers' split that then is best, 648 us).
+  // tiles leaves the walk in shared memory (three whole prompts: 633 us; walk in
+  // registers, 659).
   __device__ __forceinline__ void park(int4* p) const {
     if (S::kTiles == 1) return;
     if ((threadIdx.x & 31) == 0) {
@@ -691,6 +691,16 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       if (!(ok = mbar_wait(smem_addr(&c->s_full[t][buf]), (k / S::kBufs) & 1, &c->abort_word)))
         break;
       tc_fence_after();
+      // With two S buffers the scores do not tell that the last O += P V is
+      // done; the wait keeps at most one of them open, as a wait that sees a
+      // phase's parity alone needs.
+      auto give = [&]() -> bool {
+        if (S::kBufs > 1 && i > 0 &&
+            !mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))
+          return false;
+        hand_over(&c->p_ready[t][buf]);
+        return true;
+      };
       if (any) {
         const uint32_t s_col = tmem + lanes + (t * S::kBufs + buf) * S::kKeys;
         uint32_t bits[S::kKeys];
@@ -731,7 +741,6 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
         const float ref = m == SV_NEG_INF ? 0.f : m;
         const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
         const unsigned long long ref2 = f2_pack(-ref, -ref);
-        unsigned long long sums[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < S::kKeys; x += 32) {
           uint32_t p[16];
@@ -743,23 +752,27 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
                       p0, p1);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
-            sums[(y / 2) % 2] = f2_add(sums[(y / 2) % 2], f2_pack(p0, p1));
+            bits[x + y] = __float_as_uint(p0);
+            bits[x + y + 1] = __float_as_uint(p1);
             p[y / 2] = pack2(p0, p1, E());
           }
           tmem_store16(s_col + x / 2, p);
         }
+        tmem_wait_store();
+        if (!(ok = give())) break;
+        // The row's sum, of P before rounding, off the chain (three whole prompts:
+        // 634 us; summed along with the exponentials, 650).
+        unsigned long long sums[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < S::kKeys; x += 2)
+          sums[(x / 2) % 2] = f2_add(sums[(x / 2) % 2], f2_pack(__uint_as_float(bits[x]),
+                                                                __uint_as_float(bits[x + 1])));
         float s0, s1;
         f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
         l += s0 + s1;
-        tmem_wait_store();
-      }
-      // With two S buffers the scores do not tell that the last O += P V is
-      // done; the wait keeps at most one of them open, as a wait that sees a
-      // phase's parity alone needs.
-      if (S::kBufs > 1 && i > 0 &&
-          !(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word)))
+      } else if (!(ok = give())) {
         break;
-      hand_over(&c->p_ready[t][buf]);
+      }
     }
     if (!ok) break;
     u.unpark((const int4*)stage);
@@ -981,8 +994,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   if (w0 < w1) {
     const AttnWalk<S> u(a, c->start, w1 - w0);
     // Wide: three warpgroups launched with 168 registers a thread, and
-    // 2 x 216 + 72 = 3 x 168.  Three whole prompts: 655 us with 208 and 88, 648
-    // so, 816 with 224 and 56, which the issuers cannot do with.
+    // 2 x 216 + 72 = 3 x 168.  Three whole prompts: 638 us with 208 and 88, 633
+    // so, 800 with 224 and 56, which the issuers cannot do with.
     if (warp >= kLoader) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp >= kIssuer && warp < kIssuer + S::kTiles)
