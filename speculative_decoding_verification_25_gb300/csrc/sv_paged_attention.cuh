@@ -534,17 +534,17 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
 // ------------------------------------------------------------------ softmax
 template <int kCount>
 __device__ __forceinline__ float row_max(const uint32_t* bits) {
-  float top[8];
+  float top[4];
 #pragma unroll
-  for (int x = 0; x < 8; ++x) top[x] = __uint_as_float(bits[x]);
+  for (int x = 0; x < 4; ++x) top[x] = __uint_as_float(bits[x]);
 #pragma unroll
-  for (int x = 8; x + 8 < kCount; x += 16)
+  for (int x = 4; x + 4 < kCount; x += 8)
 #pragma unroll
-    for (int y = 0; y < 8; ++y)
-      top[y] = max3(top[y], __uint_as_float(bits[x + y]), __uint_as_float(bits[x + 8 + y]));
+    for (int y = 0; y < 4; ++y)
+      top[y] = max3(top[y], __uint_as_float(bits[x + y]), __uint_as_float(bits[x + 4 + y]));
 #pragma unroll
-  for (int y = 0; y < 8; ++y) top[y] = fmaxf(top[y], __uint_as_float(bits[kCount - 8 + y]));
-  return max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7]));
+  for (int y = 0; y < 4; ++y) top[y] = fmaxf(top[y], __uint_as_float(bits[kCount - 4 + y]));
+  return fmaxf(max3(top[0], top[1], top[2]), top[3]);
 }
 
 // All softmax warps meet (their `phase`-th meeting); false if it was given up.
