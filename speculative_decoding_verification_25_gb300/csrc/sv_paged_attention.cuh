@@ -5,7 +5,7 @@
 // r follows the running maximum only when that has risen by more than
 // kSlack, so a tile seldom has to scale what was summed before it, and the
 // probabilities stay below 2^kSlack.  (Three whole prompts of 4000 to 8192
-// tokens: 633 us; following every rise, 728 us.)
+// tokens: 629 us; following every rise, 722 us.)
 //
 // Both products run on the tensor core (tcgen05).  A query tile is 128 rows:
 // the G query heads of one key head for 128 / G consecutive tokens, since
@@ -21,10 +21,10 @@
 //   wide    two query tiles of one unit against tiles of 128 keys: while one
 //           tile's softmax runs, the tensor core works on the other's.  Bound
 //           by the chain of a tile, about 3000 clocks per 256 x 128 scores, of
-//           which the tensor core is busy for 2048: from P to the next S about
-//           1600 (the products' 1024, their start, the hand-overs), then a
-//           softmax of 1350.  1.52 PFLOP/s on chunks of 2048 tokens over
-//           contexts of 5000 to 7000.
+//           which the tensor core is busy for 2048: a softmax of 1200, then
+//           from P to the next S 1600 (the products' 1024, their start, the
+//           hand-overs) and what the other tile's turn adds.  1.53 PFLOP/s on
+//           chunks of 2048 tokens over contexts of 5000 to 7000.
 //   narrow  one query tile against tiles of 64 keys, two S buffers, and two
 //           CTAs per SM: for up to 128 rows per request, where the time is
 //           that of reading the cache: 6.6 to 6.7 TB/s on long contexts.
@@ -86,8 +86,8 @@ struct AttnShape {
   // wide: whole warpgroups, so that the softmax can take registers from the rest
   static constexpr int kThreads = kSoftThreads + (kWide ? 128 : 64);
   // A unit's start and end, in keys.  Wide, whole prompts / 37 ragged requests:
-  // 659 / 57 us at 192, 648 / 55 at 256, 648 / 55.4 at 320 (none of it cost
-  // 727 / 72 where 256 had 663 / 56, and 768 had 701 / 63).  Narrow, 64 x 5 tokens
+  // 687 / 68 us at 0, 637 / 57 at 192, 629 / 54.3 at 256, 631 / 55 at 320.
+  // Narrow, 64 x 5 tokens
   // / 4 x 1 tokens over long caches: 99.0 / 228.5 us at 32, 98.0 / 227.9 at 64,
   // 98.0 / 228.3 at 128, 98.6 / 228.6 at 192.
   static constexpr int kUnitCost = kWide ? 256 : 64;
@@ -230,8 +230,8 @@ struct AttnWalk {
     units = AttnUnits<S>(a, attn_row(a, b));
   }
   // The wide form's softmax needs its registers for the scores: its loop over the
-  // tiles leaves the walk in shared memory (three whole prompts: 633 us; walk in
-  // registers, 659).
+  // tiles leaves the walk in shared memory (three whole prompts: 629 us; walk in
+  // registers, 652).
   __device__ __forceinline__ void park(int4* p) const {
     if (S::kTiles == 1) return;
     if ((threadIdx.x & 31) == 0) {
@@ -289,8 +289,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
 
 // ------------------------------------------------------------------- loader
 // One warp, in the wide form one for queries and keys and one for values (two
-// prompt chunks, pages of 16: one warp 362 us, two 321; pages of 8: 516 and
-// 347).  A key or value tile is kKeys rows of one head, a box of min(page,
+// prompt chunks, pages of 16: one warp 352 us, two 316; pages of 8: 509 and
+// 344).  A key or value tile is kKeys rows of one head, a box of min(page,
 // kKeys) rows per page and 128-byte column block; each lane brings one box.
 // Rows of pages past the request's length stay as they are.  Keys and values
 // alternate in the ring, and its slots are even in number, so a slot is always
@@ -761,7 +761,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
         tmem_wait_store();
         if (!(ok = give())) break;
         // The row's sum, of P before rounding, off the chain (three whole prompts:
-        // 634 us; summed along with the exponentials, 650).
+        // 629 us; summed along with the exponentials, 642).
         unsigned long long sums[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < S::kKeys; x += 2)
@@ -994,8 +994,8 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   if (w0 < w1) {
     const AttnWalk<S> u(a, c->start, w1 - w0);
     // Wide: three warpgroups launched with 168 registers a thread, and
-    // 2 x 216 + 72 = 3 x 168.  Three whole prompts: 638 us with 208 and 88, 633
-    // so, 800 with 224 and 56, which the issuers cannot do with.
+    // 2 x 216 + 72 = 3 x 168.  Three whole prompts: 633 us with 208 and 88, 629
+    // so, 798 with 224 and 56, which the issuers cannot do with.
     if (warp >= kLoader) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       if (warp >= kIssuer && warp < kIssuer + S::kTiles)
