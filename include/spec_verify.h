@@ -44,9 +44,10 @@
  *     flag is OR-ed into the workspace (see spec_verify_device_errors);
  *   - the first call on a device fills the per-device cache (SM count,
  *     occupancy, kernel attributes).  After one such call, spec_verify,
- *     spec_verify_ragged, spec_verify_plug and spec_verify_and_plug make no
- *     call that CUDA stream capture forbids, so they may be captured into a CUDA graph and
- *     replayed (buffers and shapes fixed at capture).
+ *     spec_verify_ragged, spec_verify_plug, spec_verify_and_plug and the
+ *     spec_paged_* calls make no call that CUDA stream capture forbids, so
+ *     they may be captured into a CUDA graph and replayed (buffers and shapes
+ *     fixed at capture).
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H
@@ -472,7 +473,10 @@ int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, in
  *                call's use alone.  Its first SV_ATTENTION_COUNTER_BYTES
  *                must be zero before its first call (one cudaMemsetAsync);
  *                every call leaves them zero again, except one that set
- *                SV_DEV_TIMEOUT.
+ *                SV_DEV_TIMEOUT.  A captured memset has not run before its
+ *                graph does: give every capture scratch of its own, zeroed
+ *                within it, or scratch that was zeroed outside.  Graphs that
+ *                share scratch run one after the other.
  *
  * One launch.  Returns SV_OK, SV_ERR_DTYPE, SV_ERR_SHAPE, SV_ERR_NULL,
  * SV_ERR_ALIGN, SV_ERR_WORKSPACE or SV_ERR_CUDA.  T == 0 is a no-op; with
@@ -487,6 +491,15 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
                          const int32_t* kv_len, int B, int T, int Hq, int Hk, int D, int page_size,
                          int max_pages, int n_pages, float scale, void* out, float* lse,
                          void* workspace, size_t workspace_bytes, uint32_t* flags, void* stream);
+
+/*
+ * *id = a number for the capture that `stream` is in, unique in the process;
+ * 0 while it is not being captured.  Scratch that has to be zero before its
+ * first use belongs to one capture (or to calls outside any): zeroing it
+ * during a capture only records that it be zeroed.  Returns SV_OK, SV_ERR_NULL
+ * (id is NULL) or SV_ERR_CUDA.
+ */
+int spec_stream_capture_id(void* stream, uint64_t* id);
 
 /* Static, NUL-terminated description of a status code. */
 const char* spec_verify_status_string(int status);

@@ -26,7 +26,8 @@ from . import _native as _N
 _DTYPES = {torch.bfloat16: N.SV_BF16, torch.float32: N.SV_F32}
 _CACHE_DTYPES = {torch.bfloat16: N.SV_BF16, torch.float16: N.SV_F16}
 _workspaces: dict = {}
-_attention_workspaces: dict = {}
+_attention_workspaces: dict = {}   # (device, stream, D): workspace of calls outside captures
+_captured_workspaces: dict = {}    # (device, stream, D): (capture, workspace of that capture)
 
 
 class VerifyResult(NamedTuple):
@@ -384,22 +385,45 @@ class AttentionResult(NamedTuple):
     lse: Optional[torch.Tensor] = None     # [T, Hq] float32: log of the softmax's sum
 
 
+def _capture_id(stream, handle):
+    """0 outside captures, else a number for the capture that the stream is in."""
+    if stream is None and not torch.cuda.is_current_stream_capturing():
+        return 0
+    return N.spec_stream_capture_id(handle)
+
+
 def attention_workspace(D: int, device: torch.device,
                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """The cached workspace of ``paged_attention`` on a (device, stream), its
-    counters zeroed once; calls on different streams must not share one."""
+    counters zeroed once; calls on different streams must not share one.
+
+    A stream that is being captured has another one for each capture, whose
+    counters the graph zeroes whenever it runs: graphs captured on one stream
+    may be replayed in any order, on any streams, beside calls outside them.
+    Of a stream's captures the last one's is kept here; those before it live
+    in their graphs' memory pools, so graphs that share a pool must not be
+    replayed at the same time."""
     need = N.spec_paged_attention_workspace_bytes(D)
     if need == 0:
         raise ValueError(f"invalid head dimension {D}")
     index = device.index if device.index is not None else torch.cuda.current_device()
     st = stream if stream is not None else torch.cuda.current_stream(index)
     key = (index, st.cuda_stream, D)
-    ws = _attention_workspaces.get(key)
+    capture = _capture_id(st, st.cuda_stream)
+    if capture:
+        owner, ws = _captured_workspaces.get(key, (0, None))
+        if owner != capture:
+            ws = None
+    else:
+        ws = _attention_workspaces.get(key)
     if ws is None:
         with torch.cuda.stream(st):   # allocated and zeroed on the stream that uses it
             ws = torch.empty(need, dtype=torch.uint8, device=device)
             ws[:N.SV_ATTENTION_COUNTER_BYTES].zero_()
-        _attention_workspaces[key] = ws
+        if capture:
+            _captured_workspaces[key] = (capture, ws)
+        else:
+            _attention_workspaces[key] = ws
     return ws
 
 
@@ -439,7 +463,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             _check(out.lse, "out.lse", dtype=torch.float32, shape=(T, Hq), device=dev)
     handle = _stream_handle(stream, dev)
     if workspace is None:
-        workspace = _attention_workspaces.get((dev.index, handle, D))
+        if not _capture_id(stream, handle):
+            workspace = _attention_workspaces.get((dev.index, handle, D))
         if workspace is None:
             workspace = attention_workspace(D, dev, stream)
     status = N.spec_paged_attention_raw(

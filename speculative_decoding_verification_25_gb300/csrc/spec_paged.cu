@@ -296,4 +296,14 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
                            (cudaStream_t)stream, (size_t)v.smem_bytes));
 }
 
+int spec_stream_capture_id(void* stream, uint64_t* id) {
+  if (!id) return SV_ERR_NULL;
+  cudaStreamCaptureStatus state = cudaStreamCaptureStatusNone;
+  unsigned long long capture = 0;
+  const cudaError_t e = cudaStreamGetCaptureInfo((cudaStream_t)stream, &state, &capture);
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  *id = e == cudaSuccess && state == cudaStreamCaptureStatusActive ? capture : 0;
+  return done(e);
+}
+
 }  // extern "C"
