@@ -47,6 +47,7 @@
 #include <type_traits>
 
 #include "sv_paged.cuh"
+#include "sv_ranges.h"
 #include "sv_tensor.cuh"
 
 namespace sv {
@@ -790,8 +791,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     const int cta = blockIdx.x;
     // from the start of this range to the unit's, in keys; the unit's first CTA
     const long long ahead = w1 - u.left - u.pos - cta * quota;
-    const int c_first =
-        u.pos == 0 ? cta : cta - (quota >= u.pos ? 1 : (u.pos + (int)quota - 1) / (int)quota);
+    const int c_first = cta - ranges_back(u.pos, quota);
     const bool begins_late = ahead + (cta - c_first) * quota != 0;   // after its range's start
     const size_t slots = (size_t)gridDim.x * 2;
     const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
@@ -837,9 +837,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     if (whole) continue;
     // the CTA that has the unit's last tile
     const long long end = ahead + (long long)(u.tiles - 1) * S::kKeys;
-    const int c_last =
-        u.j1 == u.tiles ? cta
-        : cta + (int)(end >> 32 == 0 ? (unsigned)end / (unsigned)quota : end / quota);
+    const int c_last = u.j1 == u.tiles ? cta : cta + ranges_ahead(end, quota);
     // what all warps wrote is released by one thread's ticket, and what other
     // CTAs wrote is acquired by it
     if (!(ok = soft_meet(c, meetings++))) break;
@@ -934,10 +932,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     if (w < warp) before += c->sums[w];
     total += c->sums[w];
   }
-  const unsigned ctas = gridDim.x;
-  const long long quota = max((long long)S::kKeys, total >> 32 == 0
-                                                       ? (long long)(((unsigned)total + ctas - 1) / ctas)
-                                                       : (total + ctas - 1) / ctas);
+  const long long quota = range_quota(total, gridDim.x, S::kKeys);
   const long long w0 = (long long)blockIdx.x * quota, w1 = min(total, w0 + quota);
   long long begin = before + inc - mine;
   // One thread's rows hold the start of the range; its warp finds the place.
