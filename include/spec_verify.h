@@ -364,7 +364,7 @@ int spec_verify_and_plug(const void* target_logits, const void* draft_logits, in
  * s = page * page_size + offset names one token's place.  page_size is a
  * power of two in [8, 256]; n_pages * page_size < 2^31, and for
  * spec_paged_attention n_pages * page_size * Hk < 2^31 (offsets into the
- * cache are 64 bits wide).
+ * cache are 64 bits wide) and max_pages * page_size <= 2^31 - 512.
  *
  * `flags` is one uint32 on the device, or NULL: SV_DEV_* bits are OR-ed into
  * it and never cleared.  Arrays that a call writes must not overlap those

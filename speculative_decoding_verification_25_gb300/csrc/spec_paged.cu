@@ -87,6 +87,10 @@ int page_shift_of(int page_size) {
 }
 
 constexpr long long k2_31 = 1ll << 31;
+// Most keys of a request: the attention's walk looks up to two key tiles (of
+// 128 at most) past the last key, and a unit's cost past its keys, in 32 bits.
+constexpr long long kMostKeys = k2_31 - 512;
+static_assert(sv::AttnShape<128, true>::kUnitCost + 2 * sv::AttnShape<128, true>::kKeys <= 512, "fits");
 
 int done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
@@ -231,7 +235,8 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   const int shift = page_shift_of(page_size);
   if (shift < 0 || B < 0 || T < 0 || Hk < 1 || Hq < Hk || Hq % Hk || Hq / Hk > 128 || Hq > 4096 ||
       (D != 64 && D != 128) || max_pages < 1 || n_pages < 1 ||
-      (long long)max_pages * page_size >= k2_31 || (long long)n_pages * page_size * Hk >= k2_31 ||
+      (long long)max_pages * page_size > kMostKeys ||
+      (long long)n_pages * page_size * Hk >= k2_31 ||
       q_stride < (int64_t)Hq * D || !(scale > 0.f && scale <= 3.4e38f))
     return SV_ERR_SHAPE;
   if (T == 0) return SV_OK;

@@ -14,5 +14,23 @@ def N():
     return _native
 
 
+FAKE = 0x10000   # never dereferenced: every call below fails validation first
+ATTEND = dict(q=FAKE, qs=1024, kc=FAKE, vc=FAKE, dtype=1, table=FAKE, cu=FAKE, kv=FAKE, B=2, T=4, Hq=8, Hk=2, D=128, page=16,
+              max_pages=9, n_pages=50, scale=0.1, out=FAKE, lse=None, ws=FAKE, wsb=0, flags=None, stream=None)
+
+
+def _attend(N, **kw):
+    return N.spec_paged_attention_raw(*{**ATTEND, **kw}.values())
+
+
+@pytest.mark.parametrize("page", [8, 16, 64, 256])
+def test_attention_refuses_tables_whose_keys_pass_31_bits_in_a_tile(N, page):
+    """The kernel's key numbers run two tiles and a unit's cost past the table's last key."""
+    most = (2 ** 31 - 512) // page
+    assert _attend(N, page=page, max_pages=most) == N.SV_ERR_WORKSPACE       # the sizes pass
+    assert _attend(N, page=page, max_pages=most + 1) == N.SV_ERR_SHAPE
+    assert _attend(N, page=page, max_pages=2 ** 31 // page - 1) == N.SV_ERR_SHAPE
+
+
 def test_capture_id_needs_a_place_for_it(N):
     assert N.load().spec_stream_capture_id(None, ctypes.POINTER(ctypes.c_uint64)()) == N.SV_ERR_NULL
