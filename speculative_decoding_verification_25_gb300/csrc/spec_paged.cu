@@ -92,6 +92,12 @@ constexpr long long k2_31 = 1ll << 31;
 constexpr long long kMostKeys = k2_31 - 512;
 static_assert(sv::AttnShape<128, true>::kUnitCost + 2 * sv::AttnShape<128, true>::kKeys <= 512, "fits");
 
+#ifdef SV_CHECKED
+int g_naps = sv::kNaps;   // tests shorten it
+#else
+constexpr int g_naps = sv::kNaps;
+#endif
+
 int done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
 // A map of 16-bit elements for boxes of 64 columns (128 bytes, swizzled) by
@@ -285,6 +291,7 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   a.tickets = (int*)workspace;
   a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
   a.flags = flags;
+  a.naps = g_naps;
   CUtensorMap q_map, k_map, v_map;
   const cuuint64_t q_dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
   const cuuint64_t q_pitches[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
@@ -300,6 +307,12 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args,
                            (cudaStream_t)stream, (size_t)v.smem_bytes));
 }
+
+#ifdef SV_CHECKED
+// Tests of the checked build: after how many polls a wait inside a kernel is
+// given up (0: at once); a negative number restores the limit.
+void spec_checked_wait_polls(int polls) { g_naps = polls < 0 ? sv::kNaps : polls; }
+#endif
 
 int spec_stream_capture_id(void* stream, uint64_t* id) {
   if (!id) return SV_ERR_NULL;

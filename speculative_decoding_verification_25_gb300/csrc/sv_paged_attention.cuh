@@ -70,6 +70,7 @@ struct AttnArgs {
   int* tickets;                 // one per CTA, zero between calls
   float* partial;               // [CTA][2][rows][D], then [CTA][2][rows][2]
   unsigned* flags;
+  int naps;                     // polls after which a wait is given up
 };
 
 template <int kD, bool kWide>
@@ -322,15 +323,16 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
   };
   auto bring = [&](const CUtensorMap* map, int y, bool ours) -> bool {
     const int stage = it % S::kStages, lap = it / S::kStages;
+    if (ours) {
+      if (lap > 0 && !mbar_wait(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, a.naps))
+        return false;
+      const uint32_t bar = smem_addr(&c->full[stage]);
+      const unsigned who = __ballot_sync(0xffffffffu, y >= 0);
+      if (lane == 0) mbar_arrive_expect(bar, __popc(who) * box * 128);
+      __syncwarp();
+      if (y >= 0) tma_load_2d(my_dst + stage * S::kStageBytes, map, my_block * 64, y, bar);
+    }
     ++it;
-    if (!ours) return true;
-    if (lap > 0 && !mbar_wait(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word))
-      return false;
-    const uint32_t bar = smem_addr(&c->full[stage]);
-    const unsigned who = __ballot_sync(0xffffffffu, y >= 0);
-    if (lane == 0) mbar_arrive_expect(bar, __popc(who) * box * 128);
-    __syncwarp();
-    if (y >= 0) tma_load_2d(my_dst + stage * S::kStageBytes, map, my_block * 64, y, bar);
     return true;
   };
 
@@ -346,7 +348,7 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
       if (ok && i < n) ok = bring(k_map, y[i], keys);
     if (ok && keys) {
       if (rounds > 0 &&
-          !(ok = mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1, &c->abort_word)))
+          !(ok = mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1, &c->abort_word, a.naps)))
         break;
       ++rounds;
       const uint32_t bar = smem_addr(&c->q_full);
@@ -370,21 +372,25 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
     }
   }
   if (bad) set_flag(a.flags, kDevBadPage);
-  if (!ok) {   // given up: the copies in flight still land in this CTA's memory
+  // Copies in flight land in this CTA's memory, which has to outlive them even
+  // where the warps that would have read them have given up.  Of the ring's last
+  // lap the warp waits for its own (two warps: keys the even slots, values the odd).
 #pragma unroll 1
-    for (int i = max(0, it - S::kStages); i < it; ++i)
-      (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->calm);
-    if (rounds > 0) (void)mbar_poll(smem_addr(&c->q_full), (rounds - 1) & 1, &c->calm);
-  }
+  for (int i = max(0, it - S::kStages); i < it; ++i)
+    if (i % 2 == 0 ? keys : values)
+      (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->calm, kNaps);
+  if (rounds > 0) (void)mbar_poll(smem_addr(&c->q_full), (rounds - 1) & 1, &c->calm, kNaps);
+  __syncwarp();
 }
 
 // ----------------------------------------------------------------- products
 // A count and not a barrier: a tile without products may be units ahead, and a
-// wait for a phase sees its parity alone.
-__device__ __forceinline__ bool wait_past(AttnControl* c, int units) {
+// wait for a phase sees its parity alone.  A turn sleeps about a sixteenth of
+// what a poll of a barrier does.
+__device__ __forceinline__ bool wait_past(AttnControl* c, int units, int naps) {
   bool ok = c->past >= units;
 #pragma unroll 1
-  for (int i = 0; !ok && i < kNaps && !*(volatile int*)&c->abort_word; ++i) {
+  for (int i = 0; !ok && i < 16 * naps && !*(volatile int*)&c->abort_word; ++i) {
     __nanosleep(64);
     ok = c->past >= units;
   }
@@ -421,7 +427,8 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
 
   auto s_col = [&](int k) { return s_base + (k % S::kBufs) * S::kKeys; };
   auto wait_stage = [&](int i) {
-    return mbar_wait(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->abort_word);
+    return mbar_wait(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->abort_word,
+                     a.naps);
   };
   // Descriptors step by addresses / 16, and never out of their field.
   const uint64_t q_desc = tile_desc(q_smem + t * S::kQBytes, 16, 1024);
@@ -455,10 +462,10 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.most(), cnt = u.count(t), other = S::kTiles > 1 ? u.count(1 - t) : 0;
     if (n == 0) continue;
-    if (!(ok = mbar_wait(smem_addr(&c->q_full), rounds & 1, &c->abort_word))) break;
+    if (!(ok = mbar_wait(smem_addr(&c->q_full), rounds & 1, &c->abort_word, a.naps))) break;
     // The turns that the first tile gives belong to one unit: the second tile's
     // issuer must be past its last wait for P of the unit before.
-    if (S::kTiles > 1 && t == 0 && !(ok = wait_past(c, rounds))) break;
+    if (S::kTiles > 1 && t == 0 && !(ok = wait_past(c, rounds, a.naps))) break;
     ++rounds;
     tc_fence_after();
 #pragma unroll 1
@@ -499,7 +506,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
         if (S::kTiles > 1 && !(t == 0 ? i > 0 && i - 1 < other : i < other) && lane == 0)
           mbar_arrive(smem_addr(&c->p_ready[t][0]));
         if (!(ok = mbar_wait(smem_addr(&c->p_ready[t][k % S::kBufs]), (k / S::kBufs) & 1,
-                             &c->abort_word)))
+                             &c->abort_word, a.naps)))
           break;
         tc_fence_after();
       }
@@ -528,7 +535,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   }
   // everything issued is done before the CTA's memory goes
   release(&c->drain, true);
-  (void)mbar_poll(smem_addr(&c->drain), 0, &c->calm);
+  (void)mbar_poll(smem_addr(&c->drain), 0, &c->calm, kNaps);
   __syncwarp();
 }
 
@@ -549,10 +556,10 @@ __device__ __forceinline__ float row_max(const uint32_t* bits) {
 }
 
 // All softmax warps meet (their `phase`-th meeting); false if it was given up.
-__device__ __forceinline__ bool soft_meet(AttnControl* c, int phase) {
+__device__ __forceinline__ bool soft_meet(AttnControl* c, int phase, int naps) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&c->met));
-  return mbar_wait(smem_addr(&c->met), phase & 1, &c->abort_word);
+  return mbar_wait(smem_addr(&c->met), phase & 1, &c->abort_word, naps);
 }
 
 __device__ __forceinline__ int take_ticket(int* ticket) {
@@ -689,7 +696,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
 #pragma unroll 1
     for (int i = 0; i < n; ++i, key0 += S::kKeys) {
       const int k = done + i, buf = k % S::kBufs;
-      if (!(ok = mbar_wait(smem_addr(&c->s_full[t][buf]), (k / S::kBufs) & 1, &c->abort_word)))
+      if (!(ok = mbar_wait(smem_addr(&c->s_full[t][buf]), (k / S::kBufs) & 1, &c->abort_word,
+                           a.naps)))
         break;
       tc_fence_after();
       // With two S buffers the scores do not tell that the last O += P V is
@@ -697,7 +705,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       // phase's parity alone needs.
       auto give = [&]() -> bool {
         if (S::kBufs > 1 && i > 0 &&
-            !mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))
+            !mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word, a.naps))
           return false;
         hand_over(&c->p_ready[t][buf]);
         return true;
@@ -724,7 +732,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           l *= f;
           if (i > 0) {   // what was summed before, once the products are done
             if (S::kBufs > 1) {
-              if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word))) break;
+              if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word, a.naps)))
+                break;
               tc_fence_after();
             }
 #pragma unroll 1
@@ -781,7 +790,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     // one S buffer: one arrival per unit, else one per tile
     if (n > 0)
       ok = mbar_wait(smem_addr(&c->pv_done[t]), (S::kBufs > 1 ? done - 1 : rounds++) & 1,
-                     &c->abort_word);
+                     &c->abort_word, a.naps);
     if (!ok) break;
     tc_fence_after();
     // A unit that is all this CTA's is written out; a part of one goes to the
@@ -840,13 +849,13 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     const int c_last = u.j1 == u.tiles ? cta : cta + ranges_ahead(end, quota);
     // what all warps wrote is released by one thread's ticket, and what other
     // CTAs wrote is acquired by it
-    if (!(ok = soft_meet(c, meetings++))) break;
+    if (!(ok = soft_meet(c, meetings++, a.naps))) break;
     if (threadIdx.x == 0) {
       const bool last = take_ticket(&a.tickets[c_first]) == c_last - c_first;
       if (last) a.tickets[c_first] = 0;
       c->last = last;
     }
-    if (!(ok = soft_meet(c, meetings++))) break;
+    if (!(ok = soft_meet(c, meetings++, a.naps))) break;
     if (c->last) {
       const int parts = c_last - c_first + 1;
       if (u.rows() * (kD / 4) <= S::kSoftThreads)

@@ -2,8 +2,8 @@
 // (tcgen05) as inline PTX, for kernels whose operands lie in 128-byte
 // swizzled shared memory tiles.
 //
-// Every wait is bounded: after kNaps polls it gives up and raises the CTA's
-// abort word, which the other waits see.
+// Every wait is bounded: after a limit of polls (kNaps, less only in tests) it
+// gives up and raises the CTA's abort word, which the other waits see.
 #pragma once
 
 #include <cuda.h>
@@ -44,19 +44,21 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Waits until the phase is over; false if the wait was given up, after kNaps
+// Waits until the phase is over; false if the wait was given up, after `naps`
 // polls or once the CTA has given up elsewhere.
-__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_word) {
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, volatile int* abort_word,
+                                          int naps) {
 #pragma unroll 1
-  for (int i = 0; i < kNaps; ++i) {
+  for (int i = 0; i < naps; ++i) {
     if (mbar_try(bar, parity)) return true;
     if (*abort_word) break;
   }
   return false;
 }
 // All lanes of a warp wait; false (for all of them) if the wait was given up.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_word) {
-  const bool ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_word));
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_word,
+                                          int naps) {
+  const bool ok = __all_sync(0xffffffffu, mbar_poll(bar, parity, abort_word, naps));
   if (!ok) *abort_word = 1;
   return ok;
 }
