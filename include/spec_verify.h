@@ -472,17 +472,23 @@ int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, in
  *                spec_paged_attention_workspace_bytes(D) bytes, for this
  *                call's use alone.  Its first SV_ATTENTION_COUNTER_BYTES
  *                must be zero before its first call (one cudaMemsetAsync);
- *                every call leaves them zero again, except one that set
- *                SV_DEV_TIMEOUT.  A captured memset has not run before its
+ *                every call leaves them zero again, except one that gave up
+ *                (SV_DEV_TIMEOUT).  A captured memset has not run before its
  *                graph does: give every capture scratch of its own, zeroed
  *                within it, or scratch that was zeroed outside.  Graphs that
  *                share scratch run one after the other.
+ *
+ * Every wait inside the kernel is bounded, at about a second.  A call in
+ * which one runs out sets SV_DEV_TIMEOUT in `flags` and in the workspace, and
+ * rows of it may be unwritten.  From then on, calls with that workspace set the
+ * flag too and give NaN in all of out and lse, until
+ * spec_paged_attention_device_errors (or a memset of the counters) clears it.
  *
  * One launch.  Returns SV_OK, SV_ERR_DTYPE, SV_ERR_SHAPE, SV_ERR_NULL,
  * SV_ERR_ALIGN, SV_ERR_WORKSPACE or SV_ERR_CUDA.  T == 0 is a no-op; with
  * B == 0 the arrays of B entries may be NULL.
  */
-#define SV_ATTENTION_COUNTER_BYTES 4096
+#define SV_ATTENTION_COUNTER_BYTES 4096   /* a ticket per CTA; the last word: SV_DEV_TIMEOUT */
 
 size_t spec_paged_attention_workspace_bytes(int D);
 
@@ -491,6 +497,15 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
                          const int32_t* kv_len, int B, int T, int Hq, int Hk, int D, int page_size,
                          int max_pages, int n_pages, float scale, void* out, float* lse,
                          void* workspace, size_t workspace_bytes, uint32_t* flags, void* stream);
+
+/*
+ * Whether calls with this workspace have given up since it was last cleared:
+ * *flags (a HOST pointer) is SV_DEV_TIMEOUT or 0.  If they have, the counters
+ * are cleared for the next call.  SYNCHRONISES `stream`, on which the calls
+ * were; not for streams that are being captured.  Returns SV_OK, SV_ERR_NULL,
+ * SV_ERR_ALIGN or SV_ERR_CUDA.
+ */
+int spec_paged_attention_device_errors(void* workspace, void* stream, uint32_t* flags);
 
 /*
  * *id = a number for the capture that `stream` is in, unique in the process;

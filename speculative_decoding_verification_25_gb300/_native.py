@@ -73,6 +73,7 @@ _SIG = {
     "spec_paged_attention_workspace_bytes": (ctypes.c_size_t, [_I]),
     "spec_paged_attention": (_I, [_P, _L, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                                   ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "spec_paged_attention_device_errors": (_I, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
     "spec_stream_capture_id": (_I, [_P, ctypes.POINTER(ctypes.c_uint64)]),
 }
 
@@ -234,6 +235,15 @@ def spec_paged_attention_raw(q_ptr, q_stride, k_cache_ptr, v_cache_ptr, dtype, b
         q_ptr, q_stride, k_cache_ptr, v_cache_ptr, dtype, block_table_ptr, cu_new_ptr, kv_len_ptr,
         B, T, Hq, Hk, D, page_size, max_pages, n_pages, scale, out_ptr, lse_ptr, workspace_ptr,
         workspace_bytes, flags_ptr, stream_handle)
+
+
+def spec_paged_attention_device_errors(workspace_ptr, stream_handle) -> int:
+    """SV_DEV_TIMEOUT if calls with the workspace have given up, which clears it, else 0."""
+    flags = ctypes.c_uint32(0)
+    st = load().spec_paged_attention_device_errors(workspace_ptr, stream_handle, ctypes.byref(flags))
+    if st != SV_OK:
+        raise SpecVerifyError(st, "spec_paged_attention_device_errors")
+    return flags.value
 
 
 def spec_stream_capture_id(stream_handle) -> int:

@@ -427,6 +427,16 @@ def attention_workspace(D: int, device: torch.device,
     return ws
 
 
+def attention_errors(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> int:
+    """SV_DEV_TIMEOUT if a ``paged_attention`` call with ``workspace`` has given
+    up since this was last asked, else 0 (synchronises the stream).  Such a
+    call leaves rows unwritten, and those after it give NaN until this clears
+    the workspace.  The workspace of calls without one is
+    ``attention_workspace(D, device, stream)``."""
+    st = stream if stream is not None else torch.cuda.current_stream(workspace.device)
+    return N.spec_paged_attention_device_errors(workspace.data_ptr(), st.cuda_stream)
+
+
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     block_table: torch.Tensor, cu_new: torch.Tensor, kv_len: torch.Tensor, *,
                     scale: Optional[float] = None, want_lse: bool = False,
@@ -440,7 +450,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     zeros.  ``scale`` defaults to D ** -0.5.  A ``workspace`` of the caller's
     (spec_paged_attention_workspace_bytes) has its first
     SV_ATTENTION_COUNTER_BYTES zero before its first use, and is used by one
-    call at a time."""
+    call at a time.  ``flags`` (one int32) collects SV_DEV_* bits;
+    SV_DEV_TIMEOUT stays in the workspace as well (``attention_errors``)."""
     dt, n_pages, Hk, page_size, D = _check_cache(k_cache, v_cache)
     dev = k_cache.device
     if q.dim() != 3:

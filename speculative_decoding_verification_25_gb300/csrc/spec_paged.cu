@@ -86,6 +86,9 @@ int page_shift_of(int page_size) {
   return -1;
 }
 
+static_assert(sv::kAttnMaxCtas * sizeof(int) <= SV_ATTENTION_COUNTER_BYTES - sizeof(uint32_t),
+              "the status word lies behind the tickets");
+
 constexpr long long k2_31 = 1ll << 31;
 // Most keys of a request: the attention's walk looks up to two key tiles (of
 // 128 at most) past the last key, and a unit's cost past its keys, in 32 bits.
@@ -289,6 +292,7 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   a.out = (char*)out;
   a.lse = lse;
   a.tickets = (int*)workspace;
+  a.status = (unsigned*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES) - 1;
   a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
   a.flags = flags;
   a.naps = g_naps;
@@ -306,6 +310,17 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   void* args[] = {&a, &q_map, &k_map, &v_map};
   return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args,
                            (cudaStream_t)stream, (size_t)v.smem_bytes));
+}
+
+int spec_paged_attention_device_errors(void* workspace, void* stream, uint32_t* flags) {
+  if (!workspace || !flags) return SV_ERR_NULL;
+  if (!aligned_to(workspace, 16)) return SV_ERR_ALIGN;
+  cudaStream_t st = (cudaStream_t)stream;
+  const char* status = (const char*)workspace + SV_ATTENTION_COUNTER_BYTES - sizeof(uint32_t);
+  cudaError_t e = cudaMemcpyAsync(flags, status, sizeof(uint32_t), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e == cudaSuccess && *flags) e = cudaMemsetAsync(workspace, 0, SV_ATTENTION_COUNTER_BYTES, st);
+  return done(e);
 }
 
 #ifdef SV_CHECKED

@@ -68,6 +68,7 @@ struct AttnArgs {
   char* out;
   float* lse;                   // or nullptr
   int* tickets;                 // one per CTA, zero between calls
+  unsigned* status;             // in the workspace: not 0 once a call has given up
   float* partial;               // [CTA][2][rows][D], then [CTA][2][rows][2]
   unsigned* flags;
   int naps;                     // polls after which a wait is given up
@@ -167,6 +168,7 @@ struct AttnControl {   // at the end of the shared memory
   int abort_word;
   int calm;                   // an abort word that stays 0, for the waits of a CTA that gives up
   int last;
+  unsigned status;            // what an earlier call left in the workspace
   AttnStart start;
   long long sums[12];
 };
@@ -908,6 +910,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
   }
   if (warp == kIssuer) tmem_alloc<S::kTmemCols>(smem_addr(&c->tmem));
   wait_for_preceding_grid();
+  if (threadIdx.x == 0) c->status = __ldcg(a.status);
 
   // -------- weights of all requests, summed: thread i has rows [r0, r1)
   const int per = (a.B + S::kThreads - 1) / S::kThreads;
@@ -942,7 +945,9 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     total += c->sums[w];
   }
   const long long quota = range_quota(total, gridDim.x, S::kKeys);
-  const long long w0 = (long long)blockIdx.x * quota, w1 = min(total, w0 + quota);
+  // After a call that gave up, tickets may be anything: no work, and NaN below.
+  const bool spoilt = c->status != 0;
+  const long long w0 = (long long)blockIdx.x * quota, w1 = spoilt ? w0 : min(total, w0 + quota);
   long long begin = before + inc - mine;
   // One thread's rows hold the start of the range; its warp finds the place.
   const unsigned holds = __ballot_sync(0xffffffffu, w0 < w1 && begin <= w0 && w0 < begin + mine);
@@ -1012,25 +1017,29 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
       attn_softmax<E, kD, S>(a, u, c, tmem, staging, quota, w1);
     }
   }
-  // tokens past the last request's
-  const int used = min(max(a.cu_new[a.B], 0), a.T);
+  // tokens past the last request's, or all of them
+  const int used = spoilt ? 0 : min(max(a.cu_new[a.B], 0), a.T);
   const long long spare = (long long)(a.T - used) * a.Hq;
   if (spare > 0) {
     const long long first = (long long)used * a.Hq;
+    const uint32_t fill = spoilt ? 0x7fff7fffu : 0u;   // two NaN of either type
 #pragma unroll 1
     for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < spare * (kD / 8);
          x += (long long)gridDim.x * blockDim.x)
-      ((uint4*)a.out)[first * (kD / 8) + x] = make_uint4(0, 0, 0, 0);
+      ((uint4*)a.out)[first * (kD / 8) + x] = make_uint4(fill, fill, fill, fill);
     if (a.lse)
 #pragma unroll 1
       for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < spare;
            x += (long long)gridDim.x * blockDim.x)
-        a.lse[first + x] = SV_NEG_INF;
+        a.lse[first + x] = spoilt ? __int_as_float(0x7fffffff) : SV_NEG_INF;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0 && c->abort_word) set_flag(a.flags, kDevTimeout);
+  if (threadIdx.x == 0 && (c->abort_word || spoilt)) {
+    set_flag(a.flags, kDevTimeout);
+    set_flag(a.status, kDevTimeout);
+  }
   if (warp == kIssuer) tmem_free<S::kTmemCols>(tmem);
 }
 

@@ -75,3 +75,28 @@ def test_some_waits_run_out(polls, name, limit):
     polls(-1)
     flags.zero_()
     assert _same(c.run(workspace=_workspace(c.D), flags=flags), want) and flags.item() == 0
+
+
+@pytest.mark.parametrize("name", ["verify", "prompt", "split", "split_wide"])
+def test_a_call_that_gave_up_is_not_forgotten(polls, name):
+    """Calls on the same workspace give NaN and the flag until it is cleared,
+    whoever asks: flags are optional, the workspace remembers."""
+    import torch
+    from speculative_decoding_verification_25_gb300 import _native as N, api
+    rows, *shape = CASES[name]
+    c = PagedCase(rows, *shape, seed=9, extra_tokens=2)
+    want = c.run()
+    ws = api.attention_workspace(c.D, torch.device("cuda:0"))
+    assert api.attention_errors(ws) == 0
+    polls(0)
+    c.run()
+    polls(-1)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    for _ in range(2):
+        r = c.run(flags=flags)
+        assert bool(r.out.isnan().all()) and bool(r.lse.isnan().all()) and flags.item() == N.SV_DEV_TIMEOUT
+    assert api.attention_errors(ws) == N.SV_DEV_TIMEOUT
+    assert api.attention_errors(ws) == 0 and int(ws[:N.SV_ATTENTION_COUNTER_BYTES].sum()) == 0
+    flags.zero_()
+    assert _same(c.run(flags=flags), want) and flags.item() == 0
+    assert api.attention_errors(ws) == 0

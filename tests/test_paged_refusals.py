@@ -34,3 +34,11 @@ def test_attention_refuses_tables_whose_keys_pass_31_bits_in_a_tile(N, page):
 
 def test_capture_id_needs_a_place_for_it(N):
     assert N.load().spec_stream_capture_id(None, ctypes.POINTER(ctypes.c_uint64)()) == N.SV_ERR_NULL
+
+
+def test_attention_errors_need_a_workspace_and_a_place(N):
+    flags = ctypes.c_uint32(0)
+    call = N.load().spec_paged_attention_device_errors
+    assert call(None, None, ctypes.byref(flags)) == N.SV_ERR_NULL
+    assert call(FAKE, None, ctypes.POINTER(ctypes.c_uint32)()) == N.SV_ERR_NULL
+    assert call(FAKE + 8, None, ctypes.byref(flags)) == N.SV_ERR_ALIGN
