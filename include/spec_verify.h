@@ -30,6 +30,8 @@
  *     are dense, row-major, C-contiguous, owned by the caller;
  *   - the library allocates no memory and keeps no state beyond a per-device
  *     cache of the SM count and kernel attributes;
+ *   - the arrays' device is the calling thread's current one (the launch
+ *     geometry is that device's, and NULL streams are its own);
  *   - work is enqueued on `stream` (a cudaStream_t; NULL = legacy default
  *     stream) and runs asynchronously: spec_verify never synchronises the
  *     host; inputs must stay unchanged until the stream has run the call;

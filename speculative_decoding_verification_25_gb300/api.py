@@ -52,6 +52,22 @@ def _check(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _device(dev: torch.device):
+    """Makes ``dev`` the current device, on which the library launches."""
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _stream(stream: Optional[torch.cuda.Stream], dev: torch.device) -> torch.cuda.Stream:
+    """``stream``, the device's current one if None."""
+    if stream is None:
+        return torch.cuda.current_stream(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    return stream
+
+
 def workspace_for(B: int, K: int, V: int, dtype: int, device: torch.device,
                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """A cached device workspace large enough for this shape, one per
@@ -95,7 +111,7 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torch.T
     _check(draft_tokens, "draft_tokens", dtype=torch.int32, shape=(B, K), device=dev)
     _check(uniforms, "uniforms", dtype=torch.float32, shape=(B, K + 1), device=dev)
     _check(temperature, "temperature", dtype=torch.float32, shape=(B,), device=dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    st = _stream(stream, dev)
     if out is None:
         with torch.cuda.stream(st):   # outputs belong to the stream that writes them
             out = VerifyResult(
@@ -109,16 +125,18 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torch.T
     lq = out.logq.data_ptr() if out.logq is not None else None
     ws_bytes = workspace.numel() * workspace.element_size()
     if k_per_row is None:
-        status = N.spec_verify_raw(
-            target.data_ptr(), draft.data_ptr(), dt, draft_tokens.data_ptr(), uniforms.data_ptr(),
-            temperature.data_ptr(), B, K, V, out.accepted_len.data_ptr(),
-            out.out_tokens.data_ptr(), lp, lq, workspace.data_ptr(), ws_bytes, st.cuda_stream)
+        with _device(dev):
+            status = N.spec_verify_raw(
+                target.data_ptr(), draft.data_ptr(), dt, draft_tokens.data_ptr(), uniforms.data_ptr(),
+                temperature.data_ptr(), B, K, V, out.accepted_len.data_ptr(),
+                out.out_tokens.data_ptr(), lp, lq, workspace.data_ptr(), ws_bytes, st.cuda_stream)
     else:
         _check(k_per_row, "k_per_row", dtype=torch.int32, shape=(B,), device=dev)
-        status = N.spec_verify_ragged_raw(
-            target.data_ptr(), draft.data_ptr(), dt, draft_tokens.data_ptr(), uniforms.data_ptr(),
-            temperature.data_ptr(), k_per_row.data_ptr(), B, K, V, out.accepted_len.data_ptr(),
-            out.out_tokens.data_ptr(), lp, lq, workspace.data_ptr(), ws_bytes, st.cuda_stream)
+        with _device(dev):
+            status = N.spec_verify_ragged_raw(
+                target.data_ptr(), draft.data_ptr(), dt, draft_tokens.data_ptr(), uniforms.data_ptr(),
+                temperature.data_ptr(), k_per_row.data_ptr(), B, K, V, out.accepted_len.data_ptr(),
+                out.out_tokens.data_ptr(), lp, lq, workspace.data_ptr(), ws_bytes, st.cuda_stream)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status)
     return out
@@ -127,7 +145,8 @@ def spec_verify(target: torch.Tensor, draft: torch.Tensor, draft_tokens: torch.T
 def device_errors(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> int:
     """SV_DEV_* flags of the last call on ``workspace`` (synchronises the stream)."""
     st = stream if stream is not None else torch.cuda.current_stream(workspace.device)
-    return N.spec_verify_device_errors(workspace.data_ptr(), st.cuda_stream)
+    with _device(workspace.device):
+        return N.spec_verify_device_errors(workspace.data_ptr(), st.cuda_stream)
 
 
 def plug(result: VerifyResult, tokens: torch.Tensor, seq_len: torch.Tensor, *,
@@ -147,12 +166,13 @@ def plug(result: VerifyResult, tokens: torch.Tensor, seq_len: torch.Tensor, *,
         _check(last_token, "last_token", dtype=torch.int32, shape=(B,), device=dev)
     if flags is not None:
         _check(flags, "flags", dtype=torch.int32, shape=(1,), device=dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
-    status = N.spec_verify_plug_raw(
-        result.accepted_len.data_ptr(), result.out_tokens.data_ptr(), B, K1 - 1,
-        tokens.data_ptr(), seq_len.data_ptr(), tokens.shape[1],
-        last_token.data_ptr() if last_token is not None else None,
-        flags.data_ptr() if flags is not None else None, st.cuda_stream)
+    st = _stream(stream, dev)
+    with _device(dev):
+        status = N.spec_verify_plug_raw(
+            result.accepted_len.data_ptr(), result.out_tokens.data_ptr(), B, K1 - 1,
+            tokens.data_ptr(), seq_len.data_ptr(), tokens.shape[1],
+            last_token.data_ptr() if last_token is not None else None,
+            flags.data_ptr() if flags is not None else None, st.cuda_stream)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_verify_plug")
 
@@ -188,7 +208,7 @@ def spec_verify_and_plug(target: torch.Tensor, draft: torch.Tensor, draft_tokens
         _check(last_token, "last_token", dtype=torch.int32, shape=(B,), device=dev)
     if k_per_row is not None:
         _check(k_per_row, "k_per_row", dtype=torch.int32, shape=(B,), device=dev)
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    st = _stream(stream, dev)
     if out is None:
         with torch.cuda.stream(st):   # outputs belong to the stream that writes them
             out = VerifyResult(
@@ -198,15 +218,16 @@ def spec_verify_and_plug(target: torch.Tensor, draft: torch.Tensor, draft_tokens
                 torch.empty(B, K, dtype=torch.float32, device=dev) if want_logprobs else None)
     if workspace is None:
         workspace = workspace_for(B, K, V, dt, dev, st)
-    status = N.spec_verify_and_plug_raw(
-        target.data_ptr(), draft.data_ptr(), dt, draft_tokens.data_ptr(), uniforms.data_ptr(),
-        temperature.data_ptr(), k_per_row.data_ptr() if k_per_row is not None else None, B, K, V,
-        out.accepted_len.data_ptr(), out.out_tokens.data_ptr(),
-        out.logp.data_ptr() if out.logp is not None else None,
-        out.logq.data_ptr() if out.logq is not None else None,
-        tokens.data_ptr(), seq_len.data_ptr(), tokens.shape[1],
-        last_token.data_ptr() if last_token is not None else None,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.cuda_stream)
+    with _device(dev):
+        status = N.spec_verify_and_plug_raw(
+            target.data_ptr(), draft.data_ptr(), dt, draft_tokens.data_ptr(), uniforms.data_ptr(),
+            temperature.data_ptr(), k_per_row.data_ptr() if k_per_row is not None else None, B, K, V,
+            out.accepted_len.data_ptr(), out.out_tokens.data_ptr(),
+            out.logp.data_ptr() if out.logp is not None else None,
+            out.logq.data_ptr() if out.logq is not None else None,
+            tokens.data_ptr(), seq_len.data_ptr(), tokens.shape[1],
+            last_token.data_ptr() if last_token is not None else None,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.cuda_stream)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_verify_and_plug")
     return out
@@ -238,18 +259,19 @@ def verify_tree(target: torch.Tensor, node_tokens: torch.Tensor, parents: torch.
     need = _N.spec_verify_tree_workspace_bytes(B, N, V, dt)
     if need == 0:
         raise ValueError(f"invalid tree shape B={B} N={N} V={V}")
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    st = _stream(stream, dev)
     with torch.cuda.stream(st):   # blocks the allocator may reuse only after st's work
         if workspace is None:
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
         res = TreeResult(torch.empty(B, dtype=torch.int32, device=dev),
                          torch.empty(B, N + 1, dtype=torch.int32, device=dev),
                          torch.empty(B, N, dtype=torch.int32, device=dev) if want_nodes else None)
-    status = _N.spec_verify_tree_raw(
-        target.data_ptr(), dt, node_tokens.data_ptr(), parents.data_ptr(), B, N, V,
-        res.accepted_len.data_ptr(), res.out_tokens.data_ptr(),
-        res.accepted_nodes.data_ptr() if res.accepted_nodes is not None else None,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.cuda_stream)
+    with _device(dev):
+        status = _N.spec_verify_tree_raw(
+            target.data_ptr(), dt, node_tokens.data_ptr(), parents.data_ptr(), B, N, V,
+            res.accepted_len.data_ptr(), res.out_tokens.data_ptr(),
+            res.accepted_nodes.data_ptr() if res.accepted_nodes is not None else None,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), st.cuda_stream)
     if status != _N.SV_OK:
         raise _N.SpecVerifyError(status, "spec_verify_tree")
     return res
@@ -279,7 +301,9 @@ def _flags_ptr(flags, dev):
 def _stream_handle(stream, dev):
     """The raw handle of ``stream``, the device's current one if None (without
     the Stream object, whose making costs as much as a kernel's launch)."""
-    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return _stream(stream, dev).cuda_stream
 
 
 def _on(stream):
@@ -318,8 +342,9 @@ def paged_plan(seq_len: torch.Tensor, num_new: torch.Tensor, page_count: torch.T
     else:
         outs = [_ints(t, "out." + name, (n,), dev)
                 for t, name, n in zip(out, PagedPlan._fields, sizes)]
-    status = N.spec_paged_plan_raw(*ins, B, page_size, max_pages, n_pages, max_tokens, *outs,
-                                   _flags_ptr(flags, dev), _stream_handle(stream, dev))
+    with _device(dev):
+        status = N.spec_paged_plan_raw(*ins, B, page_size, max_pages, n_pages, max_tokens, *outs,
+                                       _flags_ptr(flags, dev), _stream_handle(stream, dev))
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_plan")
     return out
@@ -372,10 +397,11 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, slot_map: torch.Tenso
     slots = _ints(slot_map, "slot_map", (T,), dev)
     k_stride = _check_packed(k_new, "k_new", k_cache.dtype, (T, Hk, D), dev)
     v_stride = _check_packed(v_new, "v_new", k_cache.dtype, (T, Hk, D), dev)
-    status = N.spec_paged_append_raw(
-        k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, slots, dt, T, Hk, D, page_size,
-        n_pages, k_cache.data_ptr(), v_cache.data_ptr(), _flags_ptr(flags, dev),
-        _stream_handle(stream, dev))
+    with _device(dev):
+        status = N.spec_paged_append_raw(
+            k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, slots, dt, T, Hk, D, page_size,
+            n_pages, k_cache.data_ptr(), v_cache.data_ptr(), _flags_ptr(flags, dev),
+            _stream_handle(stream, dev))
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_append")
 
@@ -409,7 +435,8 @@ def attention_workspace(D: int, device: torch.device,
     index = device.index if device.index is not None else torch.cuda.current_device()
     st = stream if stream is not None else torch.cuda.current_stream(index)
     key = (index, st.cuda_stream, D)
-    capture = _capture_id(st, st.cuda_stream)
+    with _device(st.device):
+        capture = _capture_id(st, st.cuda_stream)
     if capture:
         owner, ws = _captured_workspaces.get(key, (0, None))
         if owner != capture:
@@ -434,7 +461,8 @@ def attention_errors(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream
     the workspace.  The workspace of calls without one is
     ``attention_workspace(D, device, stream)``."""
     st = stream if stream is not None else torch.cuda.current_stream(workspace.device)
-    return N.spec_paged_attention_device_errors(workspace.data_ptr(), st.cuda_stream)
+    with _device(workspace.device):
+        return N.spec_paged_attention_device_errors(workspace.data_ptr(), st.cuda_stream)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -472,18 +500,19 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _check(out.out, "out.out", dtype=q.dtype, shape=(T, Hq, D), device=dev)
         if out.lse is not None:
             _check(out.lse, "out.lse", dtype=torch.float32, shape=(T, Hq), device=dev)
-    handle = _stream_handle(stream, dev)
-    if workspace is None:
-        if not _capture_id(stream, handle):
-            workspace = _attention_workspaces.get((dev.index, handle, D))
+    with _device(dev):
+        handle = _stream_handle(stream, dev)
         if workspace is None:
-            workspace = attention_workspace(D, dev, stream)
-    status = N.spec_paged_attention_raw(
-        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, *tables, B, T, Hq, Hk,
-        D, page_size, max_pages, n_pages, D ** -0.5 if scale is None else scale,
-        out.out.data_ptr(), out.lse.data_ptr() if out.lse is not None else None,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _flags_ptr(flags, dev),
-        handle)
+            if not _capture_id(stream, handle):
+                workspace = _attention_workspaces.get((dev.index, handle, D))
+            if workspace is None:
+                workspace = attention_workspace(D, dev, stream)
+        status = N.spec_paged_attention_raw(
+            q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, *tables, B, T, Hq, Hk,
+            D, page_size, max_pages, n_pages, D ** -0.5 if scale is None else scale,
+            out.out.data_ptr(), out.lse.data_ptr() if out.lse is not None else None,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _flags_ptr(flags, dev),
+            handle)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_attention")
     return out
