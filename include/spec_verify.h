@@ -454,9 +454,11 @@ int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, in
  * A token that sees no key (L - n + i < 0, or L == 0) gets out = 0 and lse =
  * -inf, and so do the tokens from cu_new[B] to T.  Sums and softmax
  * statistics are float32; the probabilities are rounded to `dtype` once,
- * before their product with v.  Scores must be finite (no NaN or infinity
- * in q or in the keys and values that a request has); what a page holds past
- * kv_len is never looked at.  Results do not depend on timing.
+ * before their product with v.  A token and head that sees a NaN or a +inf
+ * score has NaN in out and in lse; a score of -inf counts for nothing.  A
+ * request's keys may be NaN or infinite where a token does not see them, its
+ * values may not (0 * NaN).  What a page holds past kv_len is never looked
+ * at.  Results do not depend on timing.
  *
  *   q            [T, Hq, D] of `dtype` (SV_BF16 or SV_F16); heads dense, tokens
  *                q_stride elements apart (a multiple of 8, at least Hq * D).

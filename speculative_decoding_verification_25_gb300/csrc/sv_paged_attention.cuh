@@ -564,6 +564,13 @@ __device__ __forceinline__ bool soft_meet(AttnControl* c, int phase, int naps) {
   return mbar_wait(smem_addr(&c->met), phase & 1, &c->abort_word, naps);
 }
 
+// What a row's sum l and reference m give.  A row that sees no key has l == 0;
+// one that sees a NaN or +inf score has a NaN, which stays.
+__device__ __forceinline__ float row_inverse(float l) { return l == 0.f ? 0.f : 1.f / l; }
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l == 0.f ? SV_NEG_INF : (m + log2f(l)) * kLn2;
+}
+
 __device__ __forceinline__ int take_ticket(int* ticket) {
   int before;
   asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
@@ -652,12 +659,12 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
     const int g = at % 128;
     const long long to =
         (long long)(u.units.row.begin + u.first(at / 128) + g / a.G) * a.Hq + u.h * a.G + g % a.G;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = row_inverse(l);
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
       *(uint2*)(a.out + (to * kD + (v * kSpan + col) * 4) * 2) =
           make_uint2(pack2(o[v].x * inv, o[v].y * inv, E()), pack2(o[v].z * inv, o[v].w * inv, E()));
-    if (a.lse && col == 0) a.lse[to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
+    if (a.lse && col == 0) a.lse[to] = row_lse(m, l);
   }
 }
 
@@ -807,7 +814,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     const size_t slots = (size_t)gridDim.x * 2;
     const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
     if (any) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = row_inverse(l);
       // rows of `out` from the unit's first token and head, or rows of the slot
       const long long unit = (long long)(u.units.row.begin + u.first(0)) * a.Hq + u.h * a.G;
       const int to = !mine ? -1 : whole ? (token - u.first(0)) * a.Hq + r_head : t * 128 + r;
@@ -841,7 +848,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       if (mine) {
         if (!whole)
           ((float2*)(a.partial + slots * S::kRows * kD))[slot * S::kRows + to] = make_float2(m, l);
-        else if (a.lse) a.lse[unit + to] = l > 0.f ? (m + log2f(l)) * kLn2 : SV_NEG_INF;
+        else if (a.lse) a.lse[unit + to] = row_lse(m, l);
       }
     }
     tc_fence_before();
