@@ -52,10 +52,13 @@ def _check(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must be contiguous")
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _device(dev: torch.device):
     """Makes ``dev`` the current device, on which the library launches."""
     if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
+        return _HERE
     return torch.cuda.device(dev)
 
 
@@ -308,7 +311,7 @@ def _stream_handle(stream, dev):
 
 def _on(stream):
     """Makes what is allocated inside belong to ``stream`` (None: the current one)."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def paged_plan(seq_len: torch.Tensor, num_new: torch.Tensor, page_count: torch.Tensor,
