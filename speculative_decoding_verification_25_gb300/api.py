@@ -301,6 +301,13 @@ def _flags_ptr(flags, dev):
     return None if flags is None else _ints(flags, "flags", (1,), dev)
 
 
+def _scratch(t, name, dev):
+    """(address, bytes) of a contiguous tensor on ``dev``, of any type."""
+    if not (isinstance(t, torch.Tensor) and t.device == dev and t.is_cuda and t.is_contiguous()):
+        _check(t, name, device=dev)   # says what is wrong
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _stream_handle(stream, dev):
     """The raw handle of ``stream``, the device's current one if None (without
     the Stream object, whose making costs as much as a kernel's launch)."""
@@ -463,9 +470,12 @@ def attention_errors(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream
     call leaves rows unwritten, and those after it give NaN until this clears
     the workspace.  The workspace of calls without one is
     ``attention_workspace(D, device, stream)``."""
-    st = stream if stream is not None else torch.cuda.current_stream(workspace.device)
+    address, size = _scratch(workspace, "workspace", workspace.device)
+    if size < N.SV_ATTENTION_COUNTER_BYTES:
+        raise ValueError("workspace is smaller than its counters")
+    st = _stream(stream, workspace.device)
     with _device(workspace.device):
-        return N.spec_paged_attention_device_errors(workspace.data_ptr(), st.cuda_stream)
+        return N.spec_paged_attention_device_errors(address, st.cuda_stream)
 
 
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -514,8 +524,7 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, *tables, B, T, Hq, Hk,
             D, page_size, max_pages, n_pages, D ** -0.5 if scale is None else scale,
             out.out.data_ptr(), out.lse.data_ptr() if out.lse is not None else None,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), _flags_ptr(flags, dev),
-            handle)
+            *_scratch(workspace, "workspace", dev), _flags_ptr(flags, dev), handle)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_attention")
     return out

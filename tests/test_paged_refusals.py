@@ -3,6 +3,7 @@ host, before anything reaches a GPU."""
 import ctypes
 
 import pytest
+import torch
 
 
 @pytest.fixture(scope="module")
@@ -42,3 +43,42 @@ def test_attention_errors_need_a_workspace_and_a_place(N):
     assert call(None, None, ctypes.byref(flags)) == N.SV_ERR_NULL
     assert call(FAKE, None, ctypes.POINTER(ctypes.c_uint32)()) == N.SV_ERR_NULL
     assert call(FAKE + 8, None, ctypes.byref(flags)) == N.SV_ERR_ALIGN
+
+
+class FakeCuda(torch.Tensor):
+    """A host tensor that says it lies on a CUDA device."""
+    index = 0
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", self.index))
+
+
+def test_scratch_is_dense_and_on_the_device(N):
+    from speculative_decoding_verification_25_gb300 import api
+    dev = torch.device("cuda", 0)
+    good = torch.zeros(8, 4).as_subclass(FakeCuda)
+    assert api._scratch(good, "workspace", dev) == (good.data_ptr(), 128)
+    for bad in (torch.zeros(8, 4), torch.zeros(8, 4).as_subclass(FakeCuda)[:, :2], None, 1 << 16):
+        with pytest.raises((TypeError, ValueError), match="workspace must be"):
+            api._scratch(bad, "workspace", dev)
+    good.index = 1
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        api._scratch(good, "workspace", dev)
+    with pytest.raises(ValueError, match="workspace"):
+        api.attention_errors(torch.zeros(8192, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="smaller than its counters"):
+        api.attention_errors(torch.zeros(64, dtype=torch.uint8).as_subclass(FakeCuda))
+
+
+@pytest.mark.gpu
+def test_attention_refuses_workspaces_of_the_host_and_strided_ones(N):
+    from paged_util import PagedCase
+    c = PagedCase([(40, 3)], 4, 2, 64, 16, "bf16")
+    need = N.spec_paged_attention_workspace_bytes(64)
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        c.run(workspace=torch.zeros(need, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        c.run(workspace=torch.zeros(need, 2, dtype=torch.uint8, device="cuda:0")[:, 0])
+    with pytest.raises(TypeError, match="workspace"):
+        c.run(workspace=12345)
+    with pytest.raises(N.SpecVerifyError):
+        c.run(workspace=torch.zeros(need - 16, dtype=torch.uint8, device="cuda:0"))
