@@ -469,7 +469,7 @@ int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, in
  *                decrease or leave [0, T] is skipped, a length outside [0,
  *                max_pages * page_size] is clamped; SV_DEV_BAD_LENGTH.
  *   D            64 or 128; Hq a multiple of Hk, Hq / Hk <= 128.
- *   scale        > 0, finite.
+ *   scale        > 0; scale * log2(e) finite.
  *   out          [T, Hq, D] of `dtype`, dense.
  *   lse          [T, Hq] float32, dense, or NULL.
  *   workspace    device scratch, 16-byte aligned, of at least

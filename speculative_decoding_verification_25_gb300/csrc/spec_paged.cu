@@ -246,7 +246,7 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
       (D != 64 && D != 128) || max_pages < 1 || n_pages < 1 ||
       (long long)max_pages * page_size > kMostKeys ||
       (long long)n_pages * page_size * Hk >= k2_31 ||
-      q_stride < (int64_t)Hq * D || !(scale > 0.f && scale <= 3.4e38f))
+      q_stride < (int64_t)Hq * D || !(scale > 0.f && scale * sv::kLog2e <= 3.4e38f))
     return SV_ERR_SHAPE;
   if (T == 0) return SV_OK;
   if (!q || !k_cache || !v_cache || (B > 0 && (!block_table || !kv_len)) || !cu_new || !out ||

@@ -33,6 +33,14 @@ def test_attention_refuses_tables_whose_keys_pass_31_bits_in_a_tile(N, page):
     assert _attend(N, page=page, max_pages=2 ** 31 // page - 1) == N.SV_ERR_SHAPE
 
 
+def test_attention_refuses_scales_that_overflow(N):
+    """The kernel's scale is scale * log2(e), which has to be finite as well."""
+    for scale in (1e-38, 1.0, 2e38, 2.3e38):
+        assert _attend(N, scale=scale) == N.SV_ERR_WORKSPACE, scale   # the scale passes
+    for scale in (2.4e38, 3e38, 3.4e38):
+        assert _attend(N, scale=scale) == N.SV_ERR_SHAPE, scale
+
+
 def test_capture_id_needs_a_place_for_it(N):
     assert N.load().spec_stream_capture_id(None, ctypes.POINTER(ctypes.c_uint64)()) == N.SV_ERR_NULL
 
