@@ -108,8 +108,8 @@ def _open(path: str) -> ctypes.CDLL:
 
 
 def load_checked() -> ctypes.CDLL:
-    """The checked build (every kernel index tested against its buffer; a
-    failure sets SV_DEV_OUT_OF_BOUNDS), with the same C entry points."""
+    """The checked build (the global indexes of the verify and paged kernels
+    tested against their buffers; a failure sets SV_DEV_OUT_OF_BOUNDS), with the same C entry points."""
     global _lib_checked
     if _lib_checked is None:
         if not os.path.exists(LIB_CHECKED_PATH):

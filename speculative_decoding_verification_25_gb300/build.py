@@ -1,11 +1,11 @@
 """Build libspec_verify.so in-tree with nvcc for sm_103a.
 
 Two translation units (the verify step, the paged cache operators), one
--gencode, no cmake (about a minute of nvcc).  The checked variant, libspec_verify_checked.so, is the same source compiled
-with -DSV_CHECKED: every global index the verify kernel forms is tested
-against its buffer before the access (a failure sets SV_DEV_OUT_OF_BOUNDS
-instead of faulting); the tests run it on small and odd shapes.  All
-compile in parallel.
+-gencode, no cmake (about a minute of nvcc).  The checked variant,
+libspec_verify_checked.so, is the same source compiled with -DSV_CHECKED: every
+global index that a verify or paged kernel forms is tested against its buffer
+before the access (a failure sets SV_DEV_OUT_OF_BOUNDS instead of faulting);
+the tests run it on small and odd shapes.  All compile in parallel.
 ``python -m speculative_decoding_verification_25_gb300.build``.
 """
 from __future__ import annotations

@@ -232,7 +232,7 @@ int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, in
 size_t spec_paged_attention_workspace_bytes(int D) {
   if (D != 64 && D != 128) return 0;
   return SV_ATTENTION_COUNTER_BYTES +
-         (size_t)sv::kAttnMaxCtas * 2 * sv::kAttnRowsPerSlot * (D + 2) * sizeof(float);
+         (size_t)sv::kAttnRows * (D + 2) * sizeof(float);
 }
 
 int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,

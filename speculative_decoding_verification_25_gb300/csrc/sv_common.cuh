@@ -14,8 +14,8 @@ namespace sv {
 #define SV_NEG_INF (-__int_as_float(0x7f800000))
 constexpr float kFltMin = 1.17549435e-38f;
 
-// The checked build (compiled with -DSV_CHECKED): every global index the
-// verify kernel forms is tested against its buffer's extent before the
+// The checked build (compiled with -DSV_CHECKED): every global index that a
+// verify or paged kernel forms is tested against its buffer's extent before the
 // access; a failed test skips the access and sets kDevOutOfBounds in the
 // device flags instead of faulting.  The plain build compiles the tests
 // away.

@@ -22,4 +22,12 @@ __device__ __forceinline__ void set_flag(unsigned* flags, unsigned bits) {
   if (flags) atomicOr(flags, bits);
 }
 
+// The checked build's test before an access of element i of n; the plain build
+// takes every index for good.
+__device__ __forceinline__ bool in_array(unsigned* flags, long long i, long long n) {
+  if (!kChecked || (i >= 0 && i < n)) return true;
+  set_flag(flags, kDevOutOfBounds);
+  return false;
+}
+
 }  // namespace sv

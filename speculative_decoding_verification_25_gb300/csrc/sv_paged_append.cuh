@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kAppendThreads) sv_paged_append_kernel(AppendA
             const long long page = slot >> a.page_shift;
             const int off = slot & ((1 << a.page_shift) - 1);
             to[u] = ((((page * a.Hk + h) << a.page_shift) + off) << a.head_shift) + d;
+            if (!in_array(a.flags, to[u], a.n_slots * a.pieces)) to[u] = -1;
             ldg_stream16(a.k_new + t * a.k_pitch + (long long)c * 16, k[u]);
             ldg_stream16(a.v_new + t * a.v_pitch + (long long)c * 16, v[u]);
           } else {

@@ -57,6 +57,8 @@ constexpr float kLn2 = 0.693147181f;
 constexpr float kSlack = 8.f;        // in log2: probabilities up to 256, exact in both types' range
 constexpr int kAttnMaxCtas = 320;    // resident CTAs that the workspace has room for (narrow)
 constexpr int kAttnRowsPerSlot = 128;
+// rows of partial sums in the workspace, for both forms
+constexpr long long kAttnRows = 2ll * kAttnMaxCtas * kAttnRowsPerSlot;
 
 struct AttnArgs {
   const int32_t* block_table;   // [B, max_pages]
@@ -107,6 +109,7 @@ struct AttnRow {
   int begin, n, L;
 };
 __device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, int b, bool* bad = nullptr) {
+  if (!in_array(a.flags, b, a.B)) return {0, 0, 0};
   const int begin = a.cu_new[b], end = a.cu_new[b + 1];
   const int most = a.max_pages << a.page_shift;
   const int len = a.kv_len[b];
@@ -317,7 +320,9 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
   auto box_row = [&](int j) -> int {
     const int key = j * S::kKeys + my_page * box;
     if (my_page >= boxes || key >= u.units.row.L) return -1;
-    const int id = a.block_table[(long long)u.b * a.max_pages + (key >> a.page_shift)];
+    const int pg = key >> a.page_shift;
+    if (!in_array(a.flags, u.b, a.B) || !in_array(a.flags, pg, a.max_pages)) return -1;
+    const int id = a.block_table[(long long)u.b * a.max_pages + pg];
     const bool inside = id >= 0 && id < a.n_pages;
     bad |= !inside;
     // past the last row of the cache the box fills with zeros
@@ -581,14 +586,15 @@ __device__ __forceinline__ int take_ticket(int* ticket) {
 // four whole segments per instruction: they pass through shared memory, their
 // 16-byte pieces placed so that neither side meets bank conflicts.  The
 // lane's segment is `to` pitches from `base`, none if negative; the warp's
-// first `rows` have one.
+// first `rows` have one.  The array is the `pieces` 16-byte pieces from `array`.
 __device__ __forceinline__ void stage_piece(char* stage, int piece, uint32_t x, uint32_t y,
                                             uint32_t z, uint32_t w) {
   const int lane = threadIdx.x & 31;
   *(uint4*)(stage + lane * 128 + (piece ^ (lane & 7)) * 16) = make_uint4(x, y, z, w);
 }
-__device__ __forceinline__ void store_staged(const char* stage, char* base, int to, int pitch,
-                                             int rows) {
+__device__ __forceinline__ void store_staged(unsigned* flags, const char* stage, char* base, int to,
+                                             int pitch, int rows, const void* array,
+                                             long long pieces) {
   const int lane = threadIdx.x & 31, piece = lane % 8;
   __syncwarp();
 #pragma unroll 1
@@ -602,8 +608,10 @@ __device__ __forceinline__ void store_staged(const char* stage, char* base, int 
       at[i] = __shfl_sync(0xffffffffu, to, row);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (at[i] >= 0) *(uint4*)(base + (long long)at[i] * pitch + piece * 16) = v[i];
+    for (int i = 0; i < 4; ++i) {
+      char* p = base + (long long)at[i] * pitch + piece * 16;
+      if (at[i] >= 0 && in_array(flags, (p - (const char*)array) / 16, pieces)) *(uint4*)p = v[i];
+    }
   }
   __syncwarp();
 }
@@ -619,6 +627,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
   const size_t slots = (size_t)gridDim.x * 2;
   const float4* sums = (const float4*)a.partial;
   const float2* stats = (const float2*)(a.partial + slots * S::kRows * kD);
+  if (!in_array(a.flags, slots * S::kRows - 1, kAttnRows)) return;
   const int rows0 = (u.last(0) - u.first(0)) * a.G;   // a second tile only where the first is full
   const int items = u.rows() * kSpan, col = threadIdx.x % kSpan;
 #pragma unroll 1
@@ -634,7 +643,8 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
 #pragma unroll
       for (int q = 0; q < kAhead; ++q) {
         const int p = min(p0 + q, parts - 1);
-        const size_t row = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows + at;
+        size_t row = ((size_t)(c_first + p) * 2 + (p == 0 && begins_late ? 1 : 0)) * S::kRows + at;
+        if (!in_array(a.flags, row, slots * S::kRows)) row = 0;
         ml[q] = __ldcg(&stats[row]);
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) f[q][v] = __ldcg(&sums[row * (kD / 4) + v * kSpan + col]);
@@ -660,6 +670,7 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
     const long long to =
         (long long)(u.units.row.begin + u.first(at / 128) + g / a.G) * a.Hq + u.h * a.G + g % a.G;
     const float inv = row_inverse(l);
+    if (!in_array(a.flags, to, (long long)a.T * a.Hq)) continue;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
       *(uint2*)(a.out + (to * kD + (v * kSpan + col) * 4) * 2) =
@@ -819,6 +830,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
       const long long unit = (long long)(u.units.row.begin + u.first(0)) * a.Hq + u.h * a.G;
       const int to = !mine ? -1 : whole ? (token - u.first(0)) * a.Hq + r_head : t * 128 + r;
       char* base = whole ? a.out + unit * kD * 2 : (char*)(a.partial + slot * S::kRows * kD);
+      const long long out_rows = (long long)a.T * a.Hq;
+      const long long part_rows = min((long long)slots * S::kRows, kAttnRows);
 #pragma unroll 1
       for (int x = 0; x < kD; x += 32) {
         uint32_t bits[32] = {};
@@ -842,13 +855,16 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           for (int y = 0; y < 8; ++y)
             stage_piece(stage, y, bits[4 * y], bits[4 * y + 1], bits[4 * y + 2], bits[4 * y + 3]);
         }
-        store_staged(stage, base, to, whole ? kD * 2 : kD * 4, rows);
+        store_staged(a.flags, stage, base, to, whole ? kD * 2 : kD * 4, rows,
+                     whole ? (const void*)a.out : a.partial,
+                     whole ? out_rows * (kD / 8) : part_rows * (kD / 4));
         base += 128;
       }
       if (mine) {
-        if (!whole)
-          ((float2*)(a.partial + slots * S::kRows * kD))[slot * S::kRows + to] = make_float2(m, l);
-        else if (a.lse) a.lse[unit + to] = row_lse(m, l);
+        const long long row = whole ? unit + to : (long long)slot * S::kRows + to;
+        const bool good = in_array(a.flags, row, whole ? out_rows : part_rows);
+        if (good && !whole) ((float2*)(a.partial + slots * S::kRows * kD))[row] = make_float2(m, l);
+        if (good && whole && a.lse) a.lse[row] = row_lse(m, l);
       }
     }
     tc_fence_before();
@@ -860,7 +876,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     // CTAs wrote is acquired by it
     if (!(ok = soft_meet(c, meetings++, a.naps))) break;
     if (threadIdx.x == 0) {
-      const bool last = take_ticket(&a.tickets[c_first]) == c_last - c_first;
+      const bool last = in_array(a.flags, c_first, gridDim.x) &&
+                        take_ticket(&a.tickets[c_first]) == c_last - c_first;
       if (last) a.tickets[c_first] = 0;
       c->last = last;
     }

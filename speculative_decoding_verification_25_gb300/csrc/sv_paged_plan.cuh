@@ -185,24 +185,32 @@ __global__ void __launch_bounds__(kPlanThreads) sv_paged_plan_kernel(PlanArgs a)
   for (int r = r0; r < r1; ++r) s_need[r] = min(s_need[r], N);
   __syncthreads();
 
+  // entry pg of row r's block table, and whether the checked build admits it
+  auto entry = [&](int r, int pg) { return (long long)r * a.max_pages + pg; };
+  auto has_entry = [&](int r, int pg) {
+    return in_array(a.flags, r, a.B) && in_array(a.flags, pg, a.max_pages);
+  };
   // k-th page taken, k < F + R: those given back in order, then the stack from its top
   auto taken = [&](int k) -> int {
-    if (k >= R) return a.free_pages[F - 1 - (k - R)];
+    if (k >= R) {
+      const int at = F - 1 - (k - R);
+      return in_array(a.flags, at, a.n_pages) ? a.free_pages[at] : -1;
+    }
     const int r = row_of(s_back, a.B, k);
     const int first = r > 0 ? s_back[r - 1] : 0;
-    const int want = s_have[r] - (s_back[r] - first);
-    return a.block_table[(long long)r * a.max_pages + want + (k - first)];
+    const int pg = s_have[r] - (s_back[r] - first) + (k - first);
+    return has_entry(r, pg) ? a.block_table[entry(r, pg)] : -1;
   };
 
   // -------- the CTAs of the cluster share out what is left
   const unsigned first = cta * threads + tid, step = n_ctas * threads;   // sums stay below 2^31
   for (unsigned k = first; k < (unsigned)N; k += step) {   // the tables' new entries
     const int r = row_of(s_need, a.B, k);
-    a.block_table[(long long)r * a.max_pages + s_have[r] + (k - (r > 0 ? s_need[r - 1] : 0))] =
-        taken(k);
+    const int pg = s_have[r] + (k - (r > 0 ? s_need[r - 1] : 0));
+    if (has_entry(r, pg)) a.block_table[entry(r, pg)] = taken(k);
   }
   for (unsigned j = first; (long long)j < R - N; j += step) {   // given back and not taken
-    if (F + j < (unsigned)a.n_pages) a.free_pages[F + j] = taken(R - 1 - j);
+    if (F + j < (unsigned)a.n_pages) a.free_pages[F + j] = taken(R - 1 - j);   // bounded here
     else bad |= kDevLength;
   }
   const int tokens = a.B > 0 ? s_cu[a.B - 1] : 0;
@@ -219,14 +227,17 @@ __global__ void __launch_bounds__(kPlanThreads) sv_paged_plan_kernel(PlanArgs a)
         const int have = s_have[r];
         if (have >= 0) {
           const int pg = pos >> a.page_shift;
-          const int id = pg < have ? a.block_table[(long long)r * a.max_pages + pg]
-                                   : taken((r > 0 ? s_need[r - 1] : 0) + pg - have);
+          const int id = pg >= have         ? taken((r > 0 ? s_need[r - 1] : 0) + pg - have)
+                         : has_entry(r, pg) ? a.block_table[entry(r, pg)]
+                                            : -1;
           if (id >= 0 && id < a.n_pages) slot = (id << a.page_shift) | (pos & (page - 1));
           else bad |= kDevBadPage;
         }
       }
-      a.slot_map[t] = slot;
-      a.positions[t] = pos;
+      if (in_array(a.flags, t, a.max_tokens)) {
+        a.slot_map[t] = slot;
+        a.positions[t] = pos;
+      }
     }
   }
   if (bad) set_flag(a.flags, bad);
