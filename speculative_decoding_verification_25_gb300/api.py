@@ -520,11 +520,14 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                 workspace = _attention_workspaces.get((dev.index, handle, D))
             if workspace is None:
                 workspace = attention_workspace(D, dev, stream)
+            scratch = workspace.data_ptr(), workspace.numel()
+        else:
+            scratch = _scratch(workspace, "workspace", dev)
         status = N.spec_paged_attention_raw(
             q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, *tables, B, T, Hq, Hk,
             D, page_size, max_pages, n_pages, D ** -0.5 if scale is None else scale,
             out.out.data_ptr(), out.lse.data_ptr() if out.lse is not None else None,
-            *_scratch(workspace, "workspace", dev), _flags_ptr(flags, dev), handle)
+            *scratch, _flags_ptr(flags, dev), handle)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_attention")
     return out
