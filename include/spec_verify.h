@@ -453,8 +453,9 @@ int spec_paged_append(const void* k_new, int64_t k_stride, const void* v_new, in
  *
  * A token that sees no key (L - n + i < 0, or L == 0) gets out = 0 and lse =
  * -inf, and so do the tokens from cu_new[B] to T.  Sums and softmax
- * statistics are float32; the probabilities are rounded to `dtype` once,
- * before their product with v.  A token and head that sees a NaN or a +inf
+ * statistics are float32; the probabilities, of about 1 where a row's scores
+ * are highest, are rounded to `dtype` once, before their product with v
+ * (float16 has steps of 2^-24).  A token and head that sees a NaN or a +inf
  * score has NaN in out and in lse; a score of -inf counts for nothing.  A
  * request's keys may be NaN or infinite where a token does not see them, its
  * values may not (0 * NaN).  What a page holds past kv_len is never looked

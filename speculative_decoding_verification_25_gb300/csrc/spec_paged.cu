@@ -265,7 +265,7 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   // on one key head) and streams the cache with two CTAs per SM; the wide
   // form holds 256 and keeps the tensor core busier.  The host knows the
   // mean of the rows alone; both forms take requests of any length.
-  // Measured, narrow and wide: 20 rows per request (64 requests) 98 and 114 us,
+  // Measured (in a graph), narrow and wide: 20 rows per request (64 requests) 98 and 114 us,
   // 72 rows (256 long contexts) 964 and 1008; 64 requests of 96 rows 111 and
   // 121, 128 rows 116 and 122, 160 rows 200 and 134, 256 rows 208 and 146; 580
   // rows (37 ragged requests, D = 64) 70 and 54, 8192 rows 449 and 308.

@@ -7,12 +7,21 @@
 // probabilities stay below 2^kSlack.  (Three whole prompts of 4000 to 8192
 // tokens: 629 us; following every rise, 722 us.)
 //
+// Times here are of calls replayed from a graph in short bursts, the SM clock
+// at 2070 MHz.  Under a load of seconds the card's power cap takes the clock to
+// 1950 MHz, and prompts take 6% longer, replayed or called (670 and 671 us).
+//
 // Both products run on the tensor core (tcgen05).  A query tile is 128 rows:
 // the G query heads of one key head for 128 / G consecutive tokens, since
 // they share every key and value.  S = Q K^T goes to tensor memory; four
 // warps take it a row per thread, leave P = 2^(S - r), rounded to the
 // operands' type (the product takes no other), in the place of S, and
-// O += P V reads P from there.  All sums are float32.  Rows never meet: no
+// O += P V reads P from there.  All sums are float32, that of P is of P before
+// its rounding.  The rounding of P adds as much to a result's error as that of
+// the result itself: normal keys and values differ from 64 bits by 0.0023
+// relative in bfloat16, 0.0017 without it, and by 0.00028 and 0.00021 in
+// float16 (a sum of the rounded P gives the same).  float16 has steps of 2^-24:
+// probabilities below that of the reference's are lost.  Rows never meet: no
 // shuffle, and unused rows may hold anything.
 //
 // A CTA is one or two loader warps (TMA into a ring of key and value tiles) and,
@@ -23,8 +32,9 @@
 //           by the chain of a tile, about 3000 clocks per 256 x 128 scores, of
 //           which the tensor core is busy for 2048: a softmax of 1200, then
 //           from P to the next S 1600 (the products' 1024, their start, the
-//           hand-overs) and what the other tile's turn adds.  1.53 PFLOP/s on
-//           chunks of 2048 tokens over contexts of 5000 to 7000.
+//           hand-overs) and what the other tile's turn adds.  1.52 PFLOP/s on
+//           chunks of 2048 tokens over contexts of 5000 to 7000 (1.43 under
+//           the power cap).
 //   narrow  one query tile against tiles of 64 keys, two S buffers, and two
 //           CTAs per SM: for up to 128 rows per request, where the time is
 //           that of reading the cache: 6.6 to 6.7 TB/s on long contexts.

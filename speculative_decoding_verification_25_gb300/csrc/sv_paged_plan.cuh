@@ -11,7 +11,7 @@
 // else it is as large as the tokens ask for.
 //
 // Bound by latency: the chain load lengths -> two block sums -> bisect ->
-// load page -> store: 3.4 us for one row, 6.1 us for 64 rows of five tokens,
+// load page -> store: 3.2 us for one row, 5.9 us for 64 rows of five tokens,
 // 10 us for 1024 rows and half a million tokens, whose 4 MB over 118 CTAs add
 // what one CTA per cluster of eight took 60 us for.
 #pragma once
