@@ -513,6 +513,102 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
 int spec_paged_attention_device_errors(void* workspace, void* stream, uint32_t* flags);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Appends with the position rotation, and a cache of 4 bits.
+ *
+ * spec_paged_append_rotary is spec_paged_append with the rotation of queries
+ * and keys on the way.  With position p = positions[t], the rotated columns of
+ * a head (its first rotary_dim = 2 r) turn in pairs:
+ *
+ *   x' = x cos - y sin,   y' = x sin + y cos,
+ *
+ * pair i having cos = cos_sin[p, i] and sin = cos_sin[p, r + i], and as (x, y)
+ * columns i and r + i, or, if `interleaved` is not 0, 2 i and 2 i + 1.  The
+ * arithmetic is float32, each result rounded once; other columns are copied.
+ * Rotated keys and plain values go to slot_map[t] of the cache (a negative slot
+ * skips the token), rotated queries to q_out.
+ *
+ *   q            [T, Hq, D] of `dtype` (SV_BF16 or SV_F16), or NULL with Hq == 0.
+ *   k_new, v_new [T, Hk, D] of `dtype`.  All three: heads dense, tokens
+ *                `stride` elements apart (multiples of 8, at least a token's).
+ *   positions    [T] int32.  A negative one marks padding: zeros in q_out,
+ *                nothing in the cache.  One of max_positions or more, or a
+ *                negative one whose slot is not, does the same and sets
+ *                SV_DEV_BAD_LENGTH.
+ *   cos_sin      [max_positions, rotary_dim] float32, 16-byte aligned.
+ *   rotary_dim   a multiple of 32, at most D (64 or 128).
+ *   q_out        [T, Hq, D], tokens q_out_stride elements apart; it may be q
+ *                itself, with its stride.
+ *   slot_map, k_cache, v_cache, flags: as for spec_paged_append.
+ *
+ * One launch.  Returns SV_OK, SV_ERR_DTYPE, SV_ERR_SHAPE, SV_ERR_NULL,
+ * SV_ERR_ALIGN or SV_ERR_CUDA.  T == 0 is a no-op.
+ */
+int spec_paged_append_rotary(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                             const void* v_new, int64_t v_stride, const int32_t* positions,
+                             const float* cos_sin, int max_positions, int rotary_dim, int interleaved,
+                             const int32_t* slot_map, int dtype, int T, int Hq, int Hk, int D,
+                             int page_size, int n_pages, void* q_out, int64_t q_out_stride,
+                             void* k_cache, void* v_cache, uint32_t* flags, void* stream);
+
+/*
+ * The 4-bit cache: k_codes, v_codes [n_pages, Hk, page_size, D / 2] bytes, the
+ * even column's code in a byte's low half, and k_scales, v_scales [n_pages, Hk,
+ * page_size, D / 16] bytes, a scale for each group of 16 columns.  A code is an
+ * e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6; 8 more for the negative ones), a
+ * scale an e4m3 one (no infinity, NaN is 0x7f), and a value is
+ *
+ *   code * scale * gain,
+ *
+ * with one gain for all keys and one for all values (1e-30 to 1e30), the same
+ * in every call on a cache: 1, or what keeps largest magnitudes over 6 gain
+ * between 2^-6 and 448, where scales have their full precision.
+ *
+ * spec_paged_append_fp4 is spec_paged_append_rotary into such a cache.  Of a
+ * group with largest magnitude a (rotated, of exact arithmetic)
+ *   scale = a / (6 gain), rounded to e4m3 (448 at most),
+ *   code  = x / (scale gain), rounded to e2m1 (6 at most), 0 where scale is 0,
+ * both to the nearest number and of two to the even one, as exact arithmetic
+ * rounds them.  A group with a NaN or an infinity gets the scale 0x7f and is
+ * all NaN.  positions and cos_sin may be NULL, both of them, with Hq == 0: keys
+ * are not rotated.
+ */
+int spec_paged_append_fp4(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                          const void* v_new, int64_t v_stride, const int32_t* positions,
+                          const float* cos_sin, int max_positions, int rotary_dim, int interleaved,
+                          const int32_t* slot_map, int dtype, int T, int Hq, int Hk, int D,
+                          int page_size, int n_pages, float k_gain, float v_gain, void* q_out,
+                          int64_t q_out_stride, void* k_codes, void* k_scales, void* v_codes,
+                          void* v_scales, uint32_t* flags, void* stream);
+
+/*
+ * k_out[t], v_out[t] = the values held at slot_map[t], [T, Hk, D] of `dtype`,
+ * dense; zeros for a negative slot, and for one past the cache, which sets
+ * SV_DEV_BAD_PAGE.  Values are formed in float32 and rounded to `dtype`
+ * (with gains that are powers of two they are exact within its range).  A
+ * slot may come more than once.  One launch; the codes of spec_paged_append.
+ */
+int spec_paged_read_fp4(const void* k_codes, const void* k_scales, const void* v_codes,
+                        const void* v_scales, const int32_t* slot_map, int dtype, int T, int Hk, int D,
+                        int page_size, int n_pages, float k_gain, float v_gain, void* k_out,
+                        void* v_out, uint32_t* flags, void* stream);
+
+/*
+ * spec_paged_attention over a 4-bit cache: the same tokens, masks, results and
+ * arguments, its workspace (spec_paged_attention_workspace_bytes, which calls
+ * of both kinds may share, one after the other) and its waits, with the cache in
+ * four arrays, 16-byte aligned, and its gains.  scale * log2(e) * k_gain is a
+ * normal float32 number.
+ */
+int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_codes, const void* k_scales,
+                             const void* v_codes, const void* v_scales, int dtype,
+                             const int32_t* block_table, const int32_t* cu_new,
+                             const int32_t* kv_len, int B, int T, int Hq, int Hk, int D,
+                             int page_size, int max_pages, int n_pages, float scale, float k_gain,
+                             float v_gain, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, uint32_t* flags, void* stream);
+
+/*
  * *id = a number for the capture that `stream` is in, unique in the process;
  * 0 while it is not being captured.  Scratch that has to be zero before its
  * first use belongs to one capture (or to calls outside any): zeroing it

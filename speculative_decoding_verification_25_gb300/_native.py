@@ -50,6 +50,7 @@ SV_ATTENTION_COUNTER_BYTES = 4096
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
+_F = ctypes.c_float
 _SIG = {
     "spec_verify_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
     "spec_verify_max_vocab": (_I, [_I]),
@@ -74,6 +75,13 @@ _SIG = {
     "spec_paged_attention": (_I, [_P, _L, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
                                   ctypes.c_float, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "spec_paged_attention_device_errors": (_I, [_P, _P, ctypes.POINTER(ctypes.c_uint32)]),
+    "spec_paged_append_rotary": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _I, _P, _I, _I, _I, _I, _I, _I,
+                                      _I, _P, _L, _P, _P, _P, _P]),
+    "spec_paged_append_fp4": (_I, [_P, _L, _P, _L, _P, _L, _P, _P, _I, _I, _I, _P, _I, _I, _I, _I, _I, _I,
+                                   _I, _F, _F, _P, _L, _P, _P, _P, _P, _P, _P]),
+    "spec_paged_read_fp4": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _F, _P, _P, _P, _P]),
+    "spec_paged_attention_fp4": (_I, [_P, _L, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I,
+                                      _F, _F, _F, _P, _P, _P, ctypes.c_size_t, _P, _P]),
     "spec_stream_capture_id": (_I, [_P, ctypes.POINTER(ctypes.c_uint64)]),
 }
 
@@ -244,6 +252,50 @@ def spec_paged_attention_device_errors(workspace_ptr, stream_handle) -> int:
     if st != SV_OK:
         raise SpecVerifyError(st, "spec_paged_attention_device_errors")
     return flags.value
+
+
+def spec_paged_append_rotary_raw(q_ptr, q_stride, k_new_ptr, k_stride, v_new_ptr, v_stride, positions_ptr,
+                                 cos_sin_ptr, max_positions, rotary_dim, interleaved, slot_map_ptr, dtype,
+                                 T, Hq, Hk, D, page_size, n_pages, q_out_ptr, q_out_stride, k_cache_ptr,
+                                 v_cache_ptr, flags_ptr, stream_handle) -> int:
+    """Rotated queries, and rotated keys and values to their slots of the paged cache."""
+    return load().spec_paged_append_rotary(
+        q_ptr, q_stride, k_new_ptr, k_stride, v_new_ptr, v_stride, positions_ptr, cos_sin_ptr, max_positions,
+        rotary_dim, interleaved, slot_map_ptr, dtype, T, Hq, Hk, D, page_size, n_pages, q_out_ptr,
+        q_out_stride, k_cache_ptr, v_cache_ptr, flags_ptr, stream_handle)
+
+
+def spec_paged_append_fp4_raw(q_ptr, q_stride, k_new_ptr, k_stride, v_new_ptr, v_stride, positions_ptr,
+                              cos_sin_ptr, max_positions, rotary_dim, interleaved, slot_map_ptr, dtype, T,
+                              Hq, Hk, D, page_size, n_pages, k_gain, v_gain, q_out_ptr, q_out_stride,
+                              k_codes_ptr, k_scales_ptr, v_codes_ptr, v_scales_ptr, flags_ptr,
+                              stream_handle) -> int:
+    """The same to a 4-bit cache; without positions and cos_sin nothing is rotated."""
+    return load().spec_paged_append_fp4(
+        q_ptr, q_stride, k_new_ptr, k_stride, v_new_ptr, v_stride, positions_ptr, cos_sin_ptr, max_positions,
+        rotary_dim, interleaved, slot_map_ptr, dtype, T, Hq, Hk, D, page_size, n_pages, k_gain, v_gain,
+        q_out_ptr, q_out_stride, k_codes_ptr, k_scales_ptr, v_codes_ptr, v_scales_ptr, flags_ptr,
+        stream_handle)
+
+
+def spec_paged_read_fp4_raw(k_codes_ptr, k_scales_ptr, v_codes_ptr, v_scales_ptr, slot_map_ptr, dtype, T, Hk,
+                            D, page_size, n_pages, k_gain, v_gain, k_out_ptr, v_out_ptr, flags_ptr,
+                            stream_handle) -> int:
+    """The values that a 4-bit cache holds at given slots."""
+    return load().spec_paged_read_fp4(
+        k_codes_ptr, k_scales_ptr, v_codes_ptr, v_scales_ptr, slot_map_ptr, dtype, T, Hk, D, page_size,
+        n_pages, k_gain, v_gain, k_out_ptr, v_out_ptr, flags_ptr, stream_handle)
+
+
+def spec_paged_attention_fp4_raw(q_ptr, q_stride, k_codes_ptr, k_scales_ptr, v_codes_ptr, v_scales_ptr, dtype,
+                                 block_table_ptr, cu_new_ptr, kv_len_ptr, B, T, Hq, Hk, D, page_size,
+                                 max_pages, n_pages, scale, k_gain, v_gain, out_ptr, lse_ptr, workspace_ptr,
+                                 workspace_bytes, flags_ptr, stream_handle) -> int:
+    """Attention of the new tokens over the 4-bit paged cache."""
+    return load().spec_paged_attention_fp4(
+        q_ptr, q_stride, k_codes_ptr, k_scales_ptr, v_codes_ptr, v_scales_ptr, dtype, block_table_ptr,
+        cu_new_ptr, kv_len_ptr, B, T, Hq, Hk, D, page_size, max_pages, n_pages, scale, k_gain, v_gain,
+        out_ptr, lse_ptr, workspace_ptr, workspace_bytes, flags_ptr, stream_handle)
 
 
 def spec_stream_capture_id(stream_handle) -> int:

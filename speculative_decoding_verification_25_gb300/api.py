@@ -11,7 +11,9 @@ torch.bfloat16 or torch.float32; ``draft_tokens`` [B, K] int32;
 ``paged_plan``, ``paged_append`` and ``paged_attention`` are the target
 model's pass over a paged key/value cache, with the request lengths on the
 device: a step plans its pages and slots, and every layer appends the new
-tokens' keys and values and attends.
+tokens' keys and values and attends.  ``paged_append_rotary`` appends with
+the position rotation on the way; ``PagedCacheFp4`` is a cache of 4 bits, with
+``paged_append_fp4``, ``paged_read_fp4`` and ``paged_attention_fp4``.
 """
 from __future__ import annotations
 
@@ -478,6 +480,30 @@ def attention_errors(workspace: torch.Tensor, stream: Optional[torch.cuda.Stream
         return N.spec_paged_attention_device_errors(address, st.cuda_stream)
 
 
+def _attention_scratch(workspace, D, dev, stream, handle):
+    """(address, bytes) of the caller's workspace, or of the cached one."""
+    if workspace is not None:
+        return _scratch(workspace, "workspace", dev)
+    if not _capture_id(stream, handle):
+        workspace = _attention_workspaces.get((dev.index, handle, D))
+    if workspace is None:
+        workspace = attention_workspace(D, dev, stream)
+    return workspace.data_ptr(), workspace.numel()
+
+
+def _attention_outputs(out, q, want_lse, stream):
+    T, Hq, D = q.shape
+    if out is None:
+        with _on(stream):   # outputs belong to the stream that writes them
+            return AttentionResult(
+                torch.empty(T, Hq, D, dtype=q.dtype, device=q.device),
+                torch.empty(T, Hq, dtype=torch.float32, device=q.device) if want_lse else None)
+    _check(out.out, "out.out", dtype=q.dtype, shape=(T, Hq, D), device=q.device)
+    if out.lse is not None:
+        _check(out.lse, "out.lse", dtype=torch.float32, shape=(T, Hq), device=q.device)
+    return out
+
+
 def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                     block_table: torch.Tensor, cu_new: torch.Tensor, kv_len: torch.Tensor, *,
                     scale: Optional[float] = None, want_lse: bool = False,
@@ -504,25 +530,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     B, max_pages = block_table.shape
     tables = (_ints(block_table, "block_table", (B, max_pages), dev),
               _ints(cu_new, "cu_new", (B + 1,), dev), _ints(kv_len, "kv_len", (B,), dev))
-    if out is None:
-        with _on(stream):   # outputs belong to the stream that writes them
-            out = AttentionResult(
-                torch.empty(T, Hq, D, dtype=q.dtype, device=dev),
-                torch.empty(T, Hq, dtype=torch.float32, device=dev) if want_lse else None)
-    else:
-        _check(out.out, "out.out", dtype=q.dtype, shape=(T, Hq, D), device=dev)
-        if out.lse is not None:
-            _check(out.lse, "out.lse", dtype=torch.float32, shape=(T, Hq), device=dev)
+    out = _attention_outputs(out, q, want_lse, stream)
     with _device(dev):
         handle = _stream_handle(stream, dev)
-        if workspace is None:
-            if not _capture_id(stream, handle):
-                workspace = _attention_workspaces.get((dev.index, handle, D))
-            if workspace is None:
-                workspace = attention_workspace(D, dev, stream)
-            scratch = workspace.data_ptr(), workspace.numel()
-        else:
-            scratch = _scratch(workspace, "workspace", dev)
+        scratch = _attention_scratch(workspace, D, dev, stream, handle)
         status = N.spec_paged_attention_raw(
             q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), dt, *tables, B, T, Hq, Hk,
             D, page_size, max_pages, n_pages, D ** -0.5 if scale is None else scale,
@@ -530,4 +541,204 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
             *scratch, _flags_ptr(flags, dev), handle)
     if status != N.SV_OK:
         raise N.SpecVerifyError(status, "spec_paged_attention")
+    return out
+
+
+# ------------------------------------------- rotation on the way, caches of 4 bits
+
+def rotary_table(max_positions: int, rotary_dim: int, *, base: float = 10000.0,
+                 inv_freq: Optional[torch.Tensor] = None, device=None) -> torch.Tensor:
+    """Cosines and sines [max_positions, rotary_dim] float32 of the angles
+    position * inv_freq, formed in float64.  ``inv_freq`` [rotary_dim / 2]
+    defaults to base ** (-2 i / rotary_dim)."""
+    if max_positions < 1 or rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("max_positions must be positive, rotary_dim positive and even")
+    if inv_freq is None:
+        inv_freq = base ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64) / rotary_dim)
+    elif inv_freq.shape != (rotary_dim // 2,):
+        raise ValueError(f"inv_freq must have shape {(rotary_dim // 2,)}, got {tuple(inv_freq.shape)}")
+    rates = inv_freq.to(device=device, dtype=torch.float64)
+    angle = torch.arange(max_positions, dtype=torch.float64, device=rates.device)[:, None] * rates
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+class PagedCacheFp4(NamedTuple):
+    """A paged cache of 4-bit keys and values: two e2m1 codes a byte (the even
+    column's in the low half) and an e4m3 scale for each group of 16 columns."""
+    k: torch.Tensor         # [n_pages, Hk, page_size, D / 2] uint8
+    k_scale: torch.Tensor   # [n_pages, Hk, page_size, D / 16] float8_e4m3fn
+    v: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def paged_cache_fp4(n_pages: int, Hk: int, page_size: int, D: int, device=None) -> PagedCacheFp4:
+    """An empty cache (all zeros)."""
+    if D not in (64, 128):
+        raise ValueError(f"invalid head dimension {D}")
+    shape = (n_pages, Hk, page_size)
+    make = lambda n: torch.zeros(*shape, n, dtype=torch.uint8, device=device)
+    return PagedCacheFp4(make(D // 2), make(D // 16).view(torch.float8_e4m3fn),
+                         make(D // 2), make(D // 16).view(torch.float8_e4m3fn))
+
+
+def _check_cache_fp4(cache):
+    """The four addresses, and (n_pages, Hk, page_size, D), of a 4-bit cache."""
+    k, k_scale, v, v_scale = cache
+    if k.dim() != 4:
+        raise ValueError("cache.k must be [n_pages, Hk, page_size, D / 2]")
+    dev, (n_pages, Hk, page_size, half) = k.device, k.shape
+    scales = (n_pages, Hk, page_size, half // 8)
+    for t, name, dtype, shape in ((k, "k", torch.uint8, k.shape), (k_scale, "k_scale", torch.float8_e4m3fn, scales),
+                                  (v, "v", torch.uint8, k.shape), (v_scale, "v_scale", torch.float8_e4m3fn, scales)):
+        if not (t.is_cuda and t.is_contiguous() and t.dtype is dtype and t.shape == shape and t.device == dev):
+            _check(t, "cache." + name, dtype=dtype, shape=shape, device=dev)
+    return (k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr()), (n_pages, Hk, page_size, 2 * half)
+
+
+def _append_inputs(q, k_new, v_new, positions, cos_sin, slot_map, q_out, dtype, Hk, D, dev, stream):
+    """What both rotated appends take, as their C arguments up to T and Hq, and q_out."""
+    if slot_map.dim() != 1:
+        raise ValueError("slot_map must be [T]")
+    T = slot_map.shape[0]
+    if (positions is None) != (cos_sin is None):
+        raise ValueError("positions and cos_sin come together")
+    if cos_sin is None:
+        if q is not None:
+            raise ValueError("q needs positions and cos_sin")
+        table = (None, None, 0, 0)
+    else:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_positions, rotary_dim]")
+        _check(cos_sin, "cos_sin", dtype=torch.float32, device=dev)
+        table = (_ints(positions, "positions", (T,), dev), cos_sin.data_ptr(), *cos_sin.shape)
+    k_stride = _check_packed(k_new, "k_new", dtype, (T, Hk, D), dev)
+    v_stride = _check_packed(v_new, "v_new", dtype, (T, Hk, D), dev)
+    queries, results = (None, 0), (None, 0)
+    Hq = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
+        Hq = q.shape[1]
+        queries = (q, _check_packed(q, "q", dtype, (T, Hq, D), dev))
+        if q_out is None:
+            with _on(stream):   # outputs belong to the stream that writes them
+                q_out = torch.empty(T, Hq, D, dtype=dtype, device=dev)
+        results = (q_out, _check_packed(q_out, "q_out", dtype, (T, Hq, D), dev))
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    address = lambda t: None if t is None else t.data_ptr()
+    ins = (address(queries[0]), queries[1], k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, *table)
+    return ins, _ints(slot_map, "slot_map", (T,), dev), T, Hq, (address(results[0]), results[1]), q_out
+
+
+def paged_append_rotary(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                        positions: torch.Tensor, cos_sin: torch.Tensor, slot_map: torch.Tensor,
+                        k_cache: torch.Tensor, v_cache: torch.Tensor, *, interleaved: bool = False,
+                        q_out: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """``paged_append`` with the position rotation on the way
+    (spec_paged_append_rotary); returns the rotated queries.
+
+    ``q`` [T, Hq, D] (or None) and ``k_new`` are rotated by ``positions`` [T]
+    int32 (a plan's; negative ones are padding, whose queries become zeros)
+    with the table ``cos_sin`` [max_positions, rotary_dim] (``rotary_table``):
+    pairs are columns i and i + rotary_dim / 2, or neighbours if
+    ``interleaved``.  ``q_out`` may be ``q`` itself."""
+    dt, n_pages, Hk, page_size, D = _check_cache(k_cache, v_cache)
+    dev = k_cache.device
+    if positions is None or cos_sin is None:
+        raise ValueError("positions and cos_sin are needed")
+    ins, slots, T, Hq, result, q_out = _append_inputs(q, k_new, v_new, positions, cos_sin, slot_map, q_out,
+                                                      k_cache.dtype, Hk, D, dev, stream)
+    with _device(dev):
+        status = N.spec_paged_append_rotary_raw(
+            *ins, int(interleaved), slots, dt, T, Hq, Hk, D, page_size, n_pages, *result, k_cache.data_ptr(),
+            v_cache.data_ptr(), _flags_ptr(flags, dev), _stream_handle(stream, dev))
+    if status != N.SV_OK:
+        raise N.SpecVerifyError(status, "spec_paged_append_rotary")
+    return q_out
+
+
+def paged_append_fp4(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
+                     positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor], slot_map: torch.Tensor,
+                     cache: PagedCacheFp4, *, k_gain: float = 1.0, v_gain: float = 1.0,
+                     interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                     flags: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """``paged_append_rotary`` into a 4-bit cache (spec_paged_append_fp4).  With
+    ``positions`` and ``cos_sin`` None (and ``q`` too) nothing is rotated.  The
+    gains are the cache's, the same in every call."""
+    addresses, (n_pages, Hk, page_size, D) = _check_cache_fp4(cache)
+    dev = cache.k.device
+    dt = _CACHE_DTYPES.get(k_new.dtype)
+    if dt is None:
+        raise TypeError(f"k_new dtype {k_new.dtype} is not bfloat16 or float16")
+    ins, slots, T, Hq, result, q_out = _append_inputs(q, k_new, v_new, positions, cos_sin, slot_map, q_out,
+                                                      k_new.dtype, Hk, D, dev, stream)
+    with _device(dev):
+        status = N.spec_paged_append_fp4_raw(
+            *ins, int(interleaved), slots, dt, T, Hq, Hk, D, page_size, n_pages, k_gain, v_gain, *result,
+            *addresses, _flags_ptr(flags, dev), _stream_handle(stream, dev))
+    if status != N.SV_OK:
+        raise N.SpecVerifyError(status, "spec_paged_append_fp4")
+    return q_out
+
+
+def paged_read_fp4(cache: PagedCacheFp4, slot_map: torch.Tensor, dtype: torch.dtype = torch.bfloat16, *,
+                   k_gain: float = 1.0, v_gain: float = 1.0, flags: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None) -> tuple:
+    """Keys and values [T, Hk, D] that a 4-bit cache holds at the slots
+    ``slot_map`` [T], zeros for negative ones (spec_paged_read_fp4)."""
+    addresses, (n_pages, Hk, page_size, D) = _check_cache_fp4(cache)
+    dev = cache.k.device
+    dt = _CACHE_DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError(f"dtype {dtype} is not bfloat16 or float16")
+    if slot_map.dim() != 1:
+        raise ValueError("slot_map must be [T]")
+    T = slot_map.shape[0]
+    slots = _ints(slot_map, "slot_map", (T,), dev)
+    with _on(stream):   # outputs belong to the stream that writes them
+        k, v = (torch.empty(T, Hk, D, dtype=dtype, device=dev) for _ in range(2))
+    with _device(dev):
+        status = N.spec_paged_read_fp4_raw(
+            *addresses, slots, dt, T, Hk, D, page_size, n_pages, k_gain, v_gain, k.data_ptr(), v.data_ptr(),
+            _flags_ptr(flags, dev), _stream_handle(stream, dev))
+    if status != N.SV_OK:
+        raise N.SpecVerifyError(status, "spec_paged_read_fp4")
+    return k, v
+
+
+def paged_attention_fp4(q: torch.Tensor, cache: PagedCacheFp4, block_table: torch.Tensor,
+                        cu_new: torch.Tensor, kv_len: torch.Tensor, *, scale: Optional[float] = None,
+                        k_gain: float = 1.0, v_gain: float = 1.0, want_lse: bool = False,
+                        out: Optional[AttentionResult] = None, flags: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream: Optional[torch.cuda.Stream] = None) -> AttentionResult:
+    """``paged_attention`` over a 4-bit cache (spec_paged_attention_fp4), with
+    the same workspaces; ``q`` is bfloat16 or float16."""
+    addresses, (n_pages, Hk, page_size, D) = _check_cache_fp4(cache)
+    dev = cache.k.device
+    dt = _CACHE_DTYPES.get(q.dtype)
+    if dt is None:
+        raise TypeError(f"q dtype {q.dtype} is not bfloat16 or float16")
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
+    T, Hq, _ = q.shape
+    q_stride = _check_packed(q, "q", q.dtype, (T, Hq, D), dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, max_pages = block_table.shape
+    tables = (_ints(block_table, "block_table", (B, max_pages), dev),
+              _ints(cu_new, "cu_new", (B + 1,), dev), _ints(kv_len, "kv_len", (B,), dev))
+    out = _attention_outputs(out, q, want_lse, stream)
+    with _device(dev):
+        handle = _stream_handle(stream, dev)
+        scratch = _attention_scratch(workspace, D, dev, stream, handle)
+        status = N.spec_paged_attention_fp4_raw(
+            q.data_ptr(), q_stride, *addresses, dt, *tables, B, T, Hq, Hk, D, page_size, max_pages, n_pages,
+            D ** -0.5 if scale is None else scale, k_gain, v_gain, out.out.data_ptr(),
+            out.lse.data_ptr() if out.lse is not None else None, *scratch, _flags_ptr(flags, dev), handle)
+    if status != N.SV_OK:
+        raise N.SpecVerifyError(status, "spec_paged_attention_fp4")
     return out

@@ -1,7 +1,8 @@
 """Build libspec_verify.so in-tree with nvcc for sm_103a.
 
-Two translation units (the verify step, the paged cache operators), one
--gencode, no cmake (about a minute of nvcc).  The checked variant,
+Four translation units (the verify step, the paged cache operators, the appends with
+a rotation, the attention over a 4-bit cache), one -gencode, no cmake (about a
+minute of nvcc).  The checked variant,
 libspec_verify_checked.so, is the same source compiled with -DSV_CHECKED: every
 global index that a verify or paged kernel forms is tested against its buffer
 before the access (a failure sets SV_DEV_OUT_OF_BOUNDS instead of faulting);
@@ -19,7 +20,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libspec_verify.so")
 LIB_CHECKED = os.path.join(PKG, "libspec_verify_checked.so")
-SRCS = [os.path.join(PKG, "csrc", f) for f in ("spec_verify.cu", "spec_paged.cu")]
+SRCS = [os.path.join(PKG, "csrc", f) for f in ("spec_verify.cu", "spec_paged.cu", "spec_rotary.cu", "spec_fp4.cu")]
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -8,20 +8,22 @@
 #include <mutex>
 
 #include "spec_verify.h"
-#include "sv_host.h"
 #include "sv_paged_append.cuh"
 #include "sv_paged_attention.cuh"
+#include "sv_paged_host.h"
 #include "sv_paged_plan.cuh"
 
 namespace {
 
 using sv::aligned_to;
+using sv::done;
+using sv::EncodeTiled;
+using sv::k2_31;
+using sv::kMaxDevices;
 using sv::launch_early;
+using sv::page_shift_of;
 
-constexpr int kMaxDevices = 64;
 constexpr int kMaxCluster = 8;   // portable cluster size
-
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
 
 struct PagedDevice {
   std::once_flag once;
@@ -67,29 +69,14 @@ PagedDevice* paged_device() {
       const AttentionVariant v = attention_variant(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, i & 4);
       d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
     }
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-    if (d.error == cudaSuccess)
-      d.error = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                 cudaEnableDefault, &found);
-    if (d.error == cudaSuccess && found != cudaDriverEntryPointSuccess)
-      d.error = cudaErrorSymbolNotFound;
-    d.encode = (EncodeTiled)fn;
+    if (d.error == cudaSuccess) d.error = sv::find_encoder(&d.encode);
   });
   return d.error == cudaSuccess ? &d : nullptr;
-}
-
-// log2 of a page size, -1 if it is none
-int page_shift_of(int page_size) {
-  for (int s = 3; s <= 8; ++s)
-    if (page_size == 1 << s) return s;
-  return -1;
 }
 
 static_assert(sv::kAttnMaxCtas * sizeof(int) <= SV_ATTENTION_COUNTER_BYTES - sizeof(uint32_t),
               "the status word lies behind the tickets");
 
-constexpr long long k2_31 = 1ll << 31;
 // Most keys of a request: the attention's walk looks up to two key tiles (of
 // 128 at most) past the last key, and a unit's cost past its keys, in 32 bits.
 constexpr long long kMostKeys = k2_31 - 512;
@@ -100,8 +87,6 @@ int g_naps = sv::kNaps;   // tests shorten it
 #else
 constexpr int g_naps = sv::kNaps;
 #endif
-
-int done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
 // A map of 16-bit elements for boxes of 64 columns (128 bytes, swizzled) by
 // box1 (by box2): dims and boxes innermost first, pitches in bytes.
