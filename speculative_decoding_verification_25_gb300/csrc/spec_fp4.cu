@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "spec_verify.h"
 #include "sv_fp4_attention.cuh"
 #include "sv_paged_host.h"
@@ -16,8 +18,66 @@ using sv::k2_31;
 using sv::launch_early;
 using sv::page_shift_of;
 
-constexpr float kLog2e = 1.44269504f;
-constexpr long long kMostKeys = k2_31 - 512;
+using sv::EncodeTiled;
+using sv::kMaxDevices;
+using sv::kMostKeys;
+
+struct Fp4Device {
+  std::once_flag once;
+  int sm_count = 0;
+  EncodeTiled encode = nullptr;
+  cudaError_t error = cudaSuccess;
+};
+Fp4Device g_fp4[kMaxDevices];
+
+struct Variant {
+  const void* fn;
+  int threads, smem_bytes, rows;
+};
+template <typename E, int kD, int kRows>
+Variant variant() {
+  using S = sv::Fp4Shape<kD, kRows>;
+  return {(const void*)sv::sv_fp4_attention_kernel<E, kD, kRows>, S::kThreads, S::kSmemBytes, kRows};
+}
+template <typename E>
+Variant variant_of(int D, bool many) {
+  if (D == 128) return many ? variant<E, 128, 128>() : variant<E, 128, 32>();
+  return many ? variant<E, 64, 128>() : variant<E, 64, 32>();
+}
+Variant variant_of(int dtype, int D, bool many) {
+  return dtype == SV_BF16 ? variant_of<__nv_bfloat16>(D, many) : variant_of<__half>(D, many);
+}
+
+// SM count, shared memory limits and the tensor map encoder; once per device.
+Fp4Device* fp4_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  Fp4Device& d = g_fp4[dev];
+  std::call_once(d.once, [&d, dev]() {
+    d.error = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev);
+    for (int i = 0; i < 8 && d.error == cudaSuccess; ++i) {
+      const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, i & 4);
+      d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
+    }
+    if (d.error == cudaSuccess) d.error = sv::find_encoder(&d.encode);
+  });
+  return d.error == cudaSuccess ? &d : nullptr;
+}
+
+// A map of the codes' rows, one for a token and key head, in boxes of `box` rows.
+bool encode_codes(const Fp4Device& d, CUtensorMap* map, const void* base, int D, long long rows, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows};
+  const cuuint64_t pitches[1] = {(cuuint64_t)D / 2};
+  const cuuint32_t boxes[2] = {(cuuint32_t)D / 2, (cuuint32_t)box}, ones[2] = {1, 1};
+  return d.encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, pitches, boxes, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+#ifdef SV_CHECKED
+int g_naps = sv::kNaps;   // tests shorten it
+#else
+constexpr int g_naps = sv::kNaps;
+#endif
 
 }  // namespace
 
@@ -37,8 +97,8 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
       (long long)max_pages * page_size > kMostKeys ||
       (long long)n_pages * page_size * Hk >= k2_31 || q_stride < (int64_t)Hq * D ||
       !(k_gain >= 1e-30f && k_gain <= 1e30f) || !(v_gain >= 1e-30f && v_gain <= 1e30f) ||
-      !(scale > 0.f && (double)scale * kLog2e * k_gain <= 3.4e38 &&
-        (double)scale * kLog2e * k_gain >= 1.2e-38))
+      !(scale > 0.f && (double)scale * sv::kLog2e * k_gain <= 3.4e38 &&
+        (double)scale * sv::kLog2e * k_gain >= 1.2e-38))
     return SV_ERR_SHAPE;
   if (T == 0) return SV_OK;
   if (!q || !k_codes || !k_scales || !v_codes || !v_scales || (B > 0 && (!block_table || !kv_len)) ||
@@ -50,13 +110,15 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
       !aligned_to(cu_new, 4) || !aligned_to(kv_len, 4) || !aligned_to(lse, 4) || !aligned_to(flags, 4))
     return SV_ERR_ALIGN;
   if (workspace_bytes < spec_paged_attention_workspace_bytes(D)) return SV_ERR_WORKSPACE;
+  Fp4Device* dev = fp4_device();
+  if (!dev) return SV_ERR_CUDA;
+  const int G = Hq / Hk;
+  // The host knows the mean of a request's rows (the G heads of its tokens on one key head) alone.
+  const bool many = G > 32 || (long long)T * G > 32ll * (B > 0 ? B : 1);
+  const Variant v = variant_of(dtype, D, many);
+  const int ctas = dev->sm_count < sv::kAttnMaxCtas ? dev->sm_count : sv::kAttnMaxCtas;
+
   sv::Fp4Args a;
-  a.q = (const char*)q;
-  a.q_pitch = (long long)q_stride * 2;
-  a.k_codes = (const char*)k_codes;
-  a.k_scales = (const uint8_t*)k_scales;
-  a.v_codes = (const char*)v_codes;
-  a.v_scales = (const uint8_t*)v_scales;
   a.block_table = block_table;
   a.cu_new = cu_new;
   a.kv_len = kv_len;
@@ -64,23 +126,36 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   a.T = T;
   a.Hq = Hq;
   a.Hk = Hk;
-  a.G = Hq / Hk;
+  a.G = G;
   a.page_shift = shift;
   a.max_pages = max_pages;
   a.n_pages = n_pages;
-  a.scale_log2 = scale * kLog2e * k_gain;
-  a.v_gain = v_gain;
+  a.tile_tokens = v.rows / G;
+  a.scale_log2 = (float)((double)scale * sv::kLog2e * k_gain);
   a.out = (char*)out;
   a.lse = lse;
+  a.tickets = (int*)workspace;
+  a.status = (unsigned*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES) - 1;
+  a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
   a.flags = flags;
-  const void* fn = dtype == SV_BF16
-                       ? (D == 128 ? (const void*)sv::sv_fp4_attention_kernel<__nv_bfloat16, 128>
-                                   : (const void*)sv::sv_fp4_attention_kernel<__nv_bfloat16, 64>)
-                       : (D == 128 ? (const void*)sv::sv_fp4_attention_kernel<__half, 128>
-                                   : (const void*)sv::sv_fp4_attention_kernel<__half, 64>);
-  void* args[] = {&a};
-  return done(launch_early(fn, dim3((unsigned)T, (unsigned)((Hq + sv::kFp4Warps - 1) / sv::kFp4Warps)),
-                           dim3(32 * sv::kFp4Warps), args, (cudaStream_t)stream));
+  a.naps = g_naps;
+  a.q = (const char*)q;
+  a.q_pitch = (long long)q_stride * 2;
+  a.k_scales = (const uint8_t*)k_scales;
+  a.v_scales = (const uint8_t*)v_scales;
+  a.v_gain = v_gain;
+  const long long rows = (long long)n_pages * Hk * page_size;
+  const int box = page_size < 128 ? page_size : 128;
+  CUtensorMap k_map, v_map;
+  if (!encode_codes(*dev, &k_map, k_codes, D, rows, box) || !encode_codes(*dev, &v_map, v_codes, D, rows, box))
+    return SV_ERR_CUDA;
+  void* args[] = {&a, &k_map, &v_map};
+  return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args,
+                           (cudaStream_t)stream, (size_t)v.smem_bytes));
 }
+
+#ifdef SV_CHECKED
+void spec_checked_wait_polls_fp4(int polls) { g_naps = polls < 0 ? sv::kNaps : polls; }
+#endif
 
 }  // extern "C"

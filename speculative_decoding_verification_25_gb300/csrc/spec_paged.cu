@@ -20,6 +20,7 @@ using sv::done;
 using sv::EncodeTiled;
 using sv::k2_31;
 using sv::kMaxDevices;
+using sv::kMostKeys;
 using sv::launch_early;
 using sv::page_shift_of;
 
@@ -77,9 +78,6 @@ PagedDevice* paged_device() {
 static_assert(sv::kAttnMaxCtas * sizeof(int) <= SV_ATTENTION_COUNTER_BYTES - sizeof(uint32_t),
               "the status word lies behind the tickets");
 
-// Most keys of a request: the attention's walk looks up to two key tiles (of
-// 128 at most) past the last key, and a unit's cost past its keys, in 32 bits.
-constexpr long long kMostKeys = k2_31 - 512;
 static_assert(sv::AttnShape<128, true>::kUnitCost + 2 * sv::AttnShape<128, true>::kKeys <= 512, "fits");
 
 #ifdef SV_CHECKED

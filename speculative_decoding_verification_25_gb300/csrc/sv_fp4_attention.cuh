@@ -1,120 +1,791 @@
-// Attention over a paged cache of 4-bit keys and values: one warp per new token
-// and query head, a key per lane for the scores and kD / 32 columns per lane for
-// the values, with the running maximum and sum of a softmax in float32.
+// Attention of each request's new tokens over its paged keys and values of 4 bits.
+//
+// The mathematics is that of sv_paged_attention.cuh; both products run on the
+// tensor core, transposed: with the cache's part as the first operand,
+//   S^T = K Q^T      128 keys x the unit's query rows,
+//   O^T += V^T P^T   kD columns x query rows.
+// A tile of the first operand has 128 rows whatever it holds, so the cache fills
+// it and the few query rows of a token or a draft are the short side (16
+// to kRows columns).  The first operand comes from tensor memory, where the CTA's
+// warps write what they unpack: shared memory carries the cache as it is packed,
+// 0.56 bytes a value, and would be the bound of 16-bit tiles (5 bytes a value).
+//
+// Operands are float16 whatever the queries' type.  A code times a scale is exact
+// there.  bfloat16 queries are too, scaled by a power of two that a unit's rows
+// share, except that steps are 2^-40 of the unit's largest magnitude or less.
+// Probabilities (at most 2^kSlack) are rounded to 11 bits.  The caller's gains
+// go into the scores' factor and into the results'.
+//
+// A thread of the softmax has a key and the scores of all rows.  A row's
+// reference is common to the tile: it changes only when some score exceeds
+// it by more than kSlack, which one vote of the warps tells; then the maxima are
+// taken across the threads, and what was summed is scaled.  Row sums stay
+// with the threads until the unit ends.
+//
+// Work is cut into ranges and joined as in sv_paged_attention.cuh.
 #pragma once
 
 #include "sv_fp4.cuh"
-#include "sv_paged.cuh"
-#include "sv_rotary.cuh"
+#include "sv_paged_attention.cuh"
 
 namespace sv {
 
-struct Fp4Args {
+struct Fp4Args : AttnArgs {
   const char* q;
-  long long q_pitch;
-  const char* k_codes;
+  long long q_pitch;   // bytes between tokens
   const uint8_t* k_scales;
-  const char* v_codes;
   const uint8_t* v_scales;
-  const int32_t* block_table;
-  const int32_t* cu_new;
-  const int32_t* kv_len;
-  int B, T, Hq, Hk, G, page_shift, max_pages, n_pages;
-  float scale_log2, v_gain;
-  char* out;
-  float* lse;
-  unsigned* flags;
+  float v_gain;
 };
-constexpr int kFp4Warps = 4;
 
-template <typename E, int kD>
-__global__ void __launch_bounds__(32 * kFp4Warps) sv_fp4_attention_kernel(const __grid_constant__ Fp4Args a) {
-  wait_for_preceding_grid();
-  allow_dependent_launch();
-  __shared__ float q_row[kFp4Warps][kD];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const int token = blockIdx.x, h = blockIdx.y * kFp4Warps + warp;
-  if (h >= a.Hq) return;
-  // the request that has the token, of those whose offsets are sound
-  int b = -1, begin = 0, n = 0;
-  bool bad = false;
-  for (int i = lane; i < a.B; i += 32) {
-    const int lo = a.cu_new[i], hi = a.cu_new[i + 1], len = a.kv_len[i];
-    const bool sound = lo >= 0 && hi >= lo && hi <= a.T;
-    bad |= !sound || len < 0 || len > (a.max_pages << a.page_shift);
-    if (sound && token >= lo && token < hi) b = i, begin = lo, n = hi - lo;
+template <int kD, int kRowsMost>
+struct Fp4Shape {
+  static constexpr int kTiles = 1;
+  static constexpr int kKeys = 128;
+  static constexpr int kRows = kRowsMost;                  // query rows of a unit, at most
+  static constexpr int kGroups = kRows > 64 ? 2 : 1;       // groups of four softmax warps
+  static constexpr int kCols = kRows / kGroups;            // rows of such a group
+  static constexpr int kUnitCost = 64;
+  static constexpr int kSoftThreads = 128 * kGroups;
+  static constexpr int kThreads = kSoftThreads + 2 * 128 + 128;
+  static constexpr int kBlocks = kD / 64;
+  static constexpr int kQBytes = kRows * kD * 2;           // two of them
+  static constexpr int kPBytes = 128 * 128 * ((kRows + 63) / 64);   // two of them
+  static constexpr int kCodeBytes = 128 * kD / 2, kScaleBytes = 128 * kD / 16;
+  static constexpr int kStageBytes = kCodeBytes + kScaleBytes;
+  static constexpr int kBufs = kRows > 64 ? 1 : 2;         // of keys and of values in tensor memory
+  static constexpr int kValueScales = 128 * (kD / 16) * 2; // float16, two of them
+  static constexpr int kControlBytes = 1024;
+  static constexpr int kStatBytes = kGroups * 64 * 4 * (4 + 3);   // of four warps, and three of a row
+  static constexpr int kFixedBytes = 2 * (kQBytes + kPBytes + kValueScales) + kControlBytes + kStatBytes;
+  static constexpr int kMostStages = (227 * 1024 - 1024 - kFixedBytes) / kStageBytes;
+  static constexpr int kStages = kMostStages / 2 * 2 < 16 ? kMostStages / 2 * 2 : 16;
+  static constexpr int kSmemBytes = kFixedBytes + kStages * kStageBytes;
+  // columns of tensor memory
+  static constexpr int kS = 0, kO = 2 * kRows, kK = 3 * kRows, kV = kK + kBufs * 64, kTmemCols = 512;
+  static_assert(kV + kBufs * 64 <= kTmemCols, "fits");
+  static_assert(kStages >= 4, "fits");
+};
+
+struct Fp4Control {
+  uint64_t full[16], empty[16];
+  uint64_t q_full[2], q_free[2], k_ready[2], k_free[2], v_ready[2], v_free[2];
+  uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];
+  uint64_t drain, met;
+  uint32_t tmem;
+  int abort_word, calm, last;
+  unsigned status;
+  int q_exponent[2];
+  AttnStart start;
+  long long sums[20];
+};
+static_assert(sizeof(Fp4Control) <= 1024, "fits kControlBytes");
+
+// Four warps meet (barrier `id`); whether any, or all, of them say so.
+__device__ __forceinline__ bool vote_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool vote_all(int id, bool x) { return !vote_any(id, !x); }
+
+// Largest of the warp's values, NaN aside.
+__device__ __forceinline__ float redux_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ------------------------------------------------------------------- loader
+// Key and value tiles as they are packed, alternating in the ring: lanes 0 to 15
+// bring a page's codes each, lanes 16 to 31 its scales, which lie in a row (a
+// tiled copy wants 128 bytes).  Rows of pages past the request's length stay as
+// they are; a page outside the cache has scales of zero.
+template <int kD, typename S>
+__device__ __forceinline__ void fp4_load(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, char* ring,
+                                         const CUtensorMap* k_map, const CUtensorMap* v_map) {
+  const int lane = threadIdx.x & 31;
+  const int page = 1 << a.page_shift, box = min(page, S::kKeys), boxes = S::kKeys / box;
+  const int mine = lane % 16, none = (a.n_pages * a.Hk) << a.page_shift;   // one past the cache's rows
+  int it = 0;
+  bool ok = true, bad = false;
+
+  // First row, in the cache, of the lane's box of key tile j; -1 if it has none.
+  auto box_row = [&](int j) -> int {
+    const int key = j * S::kKeys + mine * box;
+    if (mine >= boxes || key >= u.units.row.L) return -1;
+    const int pg = key >> a.page_shift;
+    if (!in_array(a.flags, u.b, a.B) || !in_array(a.flags, pg, a.max_pages)) return -1;
+    const int id = a.block_table[(long long)u.b * a.max_pages + pg];
+    if (id >= 0 && id < a.n_pages) return ((id * a.Hk + u.h) << a.page_shift) + (key & (page - 1));
+    bad = true;
+    return none;
+  };
+  auto bring = [&](const CUtensorMap* codes, const uint8_t* scales, int y) -> bool {
+    const int stage = it % S::kStages, lap = it / S::kStages;
+    if (lap > 0 &&
+        !mbar_wait(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, naps_of(a)))
+      return false;
+    const uint32_t bar = smem_addr(&c->full[stage]);
+    char* to = ring + stage * S::kStageBytes;
+    char* scale_to = to + S::kCodeBytes + mine * box * (kD / 16);
+    const unsigned code_lanes = __ballot_sync(0xffffffffu, y >= 0 && lane < 16);
+    const unsigned scale_lanes = __ballot_sync(0xffffffffu, y >= 0 && y < none && lane >= 16);
+    if (y == none && lane >= 16) {
+      for (int x = 0; x < box * (kD / 16); x += 4) *(uint32_t*)(scale_to + x) = 0;
+      fence_async_shared();   // before the copy of the slot's next lap
+    }
+    __syncwarp();
+    if (lane == 0)
+      mbar_arrive_expect(bar, __popc(code_lanes) * box * (kD / 2) + __popc(scale_lanes) * box * (kD / 16));
+    __syncwarp();
+    if (y >= 0 && lane < 16) tma_load_2d(smem_addr(to + mine * box * (kD / 2)), codes, 0, y, bar);
+    if (y >= 0 && y < none && lane >= 16)
+      bulk_load(smem_addr(scale_to), scales + (long long)y * (kD / 16), box * (kD / 16), bar);
+    ++it;
+    return true;
+  };
+
+#pragma unroll 1
+  for (bool first = true; ok && u.next(first); first = false) {
+    const int n = u.count(0);
+    if (n == 0) continue;
+    int y = box_row(u.j0);
+#pragma unroll 1
+    for (int i = 0; ok && i < n; ++i) {
+      const int next = i + 1 < n ? box_row(u.j0 + i + 1) : -1;
+      ok = bring(k_map, a.k_scales, y);
+      if (ok) ok = bring(v_map, a.v_scales, y);
+      y = next;
+    }
   }
-  if (bad && token == 0 && h == 0) set_flag(a.flags, kDevLength);
-  const unsigned who = __ballot_sync(0xffffffffu, b >= 0);
-  int seen = 0;
-  if (who) {
-    const int from = __ffs(who) - 1;
-    b = __shfl_sync(0xffffffffu, b, from);
-    begin = __shfl_sync(0xffffffffu, begin, from);
-    n = __shfl_sync(0xffffffffu, n, from);
-    const int L = min(max(a.kv_len[b], 0), a.max_pages << a.page_shift);
-    seen = max(0, L - n + (token - begin) + 1);
-  }
-  const char* q = a.q + token * a.q_pitch + (long long)h * kD * 2;
-  for (int i = lane; i < kD / 2; i += 32) Element<E>::unpack(((const uint32_t*)q)[i], &q_row[warp][2 * i]);
+  if (bad) set_flag(a.flags, kDevBadPage);
+  // copies in flight land in this CTA's memory, which has to outlive them
+#pragma unroll 1
+  for (int i = max(0, it - S::kStages); i < it; ++i)
+    (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->calm, kNaps);
   __syncwarp();
-  const int hk = h / a.G;
-  float m = SV_NEG_INF, l = 0.f, o[kD / 32] = {};
-  for (int key0 = 0; key0 < seen; key0 += 32) {
-    const int key = key0 + lane;
-    long long row = -1;
-    float s = SV_NEG_INF;
-    if (key < seen) {
-      const int id = a.block_table[(long long)b * a.max_pages + (key >> a.page_shift)];
-      if (id >= 0 && id < a.n_pages)
-        row = (((long long)id * a.Hk + hk) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
-      else set_flag(a.flags, kDevBadPage);
-      s = 0.f;
-      for (int g = 0; g < kD / kFp4Group && row >= 0; ++g) {
-        const uint2 w = *(const uint2*)(a.k_codes + row * (kD / 2) + g * 8);
-        const float unit = fp4_scale(a.k_scales[row * (kD / kFp4Group) + g]);
-        uint32_t r[8];
-        fp4_unpack(w.x, r);
-        fp4_unpack(w.y, r + 4);
-        float part = 0.f;
-        for (int x = 0; x < 8; ++x) {
-          const float2 f = __half22float2(*(const __half2*)&r[x]);
-          part += q_row[warp][g * 16 + 2 * x] * f.x + q_row[warp][g * 16 + 2 * x + 1] * f.y;
+}
+
+// ------------------------------------------------------------------ queries
+// One warp brings a unit's rows to shared memory as float16, columns past them
+// zero, a unit ahead of their use.
+template <typename E, int kD, typename S>
+__device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, char* q_ptr) {
+  constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
+  constexpr int kLanes = kD / 8, kPass = 32 / kLanes, kAhead = 4;   // rows per pass, passes in flight
+  const int lane = threadIdx.x & 31, part = lane % kLanes;
+  int rounds = 0;
+#pragma unroll 1
+  for (bool first = true; u.next(first); first = false) {
+    if (u.count(0) == 0) continue;
+    const int buf = rounds % 2, rows = u.rows(), cols = (rows + 15) / 16 * 16;
+    if (rounds >= 2 && !mbar_wait(smem_addr(&c->q_free[buf]), (rounds / 2 - 1) & 1, &c->abort_word, naps_of(a)))
+      break;
+    char* to = q_ptr + buf * S::kQBytes + (part / 8) * (S::kRows * 128);
+    auto load = [&](int row, uint32_t (&w)[4]) {
+      w[0] = w[1] = w[2] = w[3] = 0;
+      if (row >= rows) return;
+      const int t = u.units.row.begin + u.first(0) + row / a.G, h = u.h * a.G + row % a.G;
+      if (in_array(a.flags, t, a.T)) ldg_stream16(a.q + t * a.q_pitch + h * (kD * 2) + part * 16, w);
+    };
+    auto store = [&](int row, const uint32_t (&w)[4]) {
+      if (row < cols)
+        *(uint4*)(to + row * 128 + ((part % 8) ^ (row % 8)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    int exponent = 0;
+    float top = 0.f;
+    // Magnitudes between 2^-2 and 2^15 need no scaling: tried first.
+#pragma unroll 1
+    for (int again = 0; again < 2; ++again) {
+      // 2^-exponent in two factors, each of which is a normal number
+      const float f0 = ldexpf(1.f, -exponent / 2), f1 = ldexpf(1.f, -exponent - -exponent / 2);
+#pragma unroll 1
+      for (int r0 = lane / kLanes; r0 < cols; r0 += kPass * kAhead) {
+        uint32_t w[kAhead][4];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(r0 + i * kPass, w[i]);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (kBf16) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float lo = __uint_as_float(w[i][x] << 16), hi = __uint_as_float(w[i][x] & 0xffff0000u);
+              if (fabsf(lo) < 3.4e38f) top = fmaxf(top, fabsf(lo));   // neither infinities nor NaN
+              if (fabsf(hi) < 3.4e38f) top = fmaxf(top, fabsf(hi));
+              w[i][x] = pack2(lo * f0 * f1, hi * f0 * f1, __half());
+            }
+          }
+          store(r0 + i * kPass, w[i]);
         }
-        s += part * unit;
       }
-      s *= a.scale_log2;
+      if (!kBf16 || again) break;
+      top = redux_max(top);
+      if (top == 0.f || (top >= 0.25f && top < 32768.f)) break;
+      exponent = (int)(__float_as_uint(top) >> 23) - 127 - 14;   // subnormal: as if 2^-127
     }
-    float top = s;
-    for (int x = 16; x > 0; x /= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    top = fmaxf(top, m);
-    const float ref = top == SV_NEG_INF ? 0.f : top, f = m == SV_NEG_INF ? 0.f : exp2f(m - ref);
-    const float p = key < seen ? exp2f(s - ref) : 0.f;
-    m = top;
-    l = l * f + p;
-    for (int x = 0; x < kD / 32; ++x) o[x] *= f;
-    for (int j = 0; j < min(32, seen - key0); ++j) {
-      const long long r = __shfl_sync(0xffffffffu, row, j);
-      const float pj = __shfl_sync(0xffffffffu, p, j);
-      if (r < 0) continue;
-      const float unit = fp4_scale(a.v_scales[r * (kD / kFp4Group) + lane / (512 / kD)]);
-      const uint32_t w = kD == 128 ? *(const uint16_t*)(a.v_codes + r * (kD / 2) + lane * 2)
-                                   : *(const uint8_t*)(a.v_codes + r * (kD / 2) + lane);
-      uint32_t v[4];
-      fp4_unpack(w, v);
-      for (int x = 0; x < kD / 64; ++x) {
-        const float2 e = __half22float2(*(const __half2*)&v[x]);
-        o[2 * x] += pj * (e.x * unit);
-        o[2 * x + 1] += pj * (e.y * unit);
+    fence_async_shared();
+    if (lane == 0) c->q_exponent[buf] = exponent;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&c->q_full[buf]));
+    ++rounds;
+  }
+}
+
+// --------------------------------------------------------------- unpacking
+// The key of lane x of a tile's 128: chosen so that the 16 of a block come in the
+// order in which the values' columns do (see fp4_values), and that eight lanes in
+// a row meet no bank conflict, neither in the packed keys nor in P.
+__device__ __forceinline__ int fp4_key(int x) {
+  const int a = x % 8 / 2, j = 2 * ((a >= 2) != (x % 16 >= 8)) + x % 2;
+  return x / 16 * 16 + 4 * a + j;
+}
+// Where P^T has the key: the order of the values' columns within a block.
+__device__ __forceinline__ int fp4_place(int key) {
+  return key / 16 * 16 + key % 4 / 2 * 8 + key % 16 / 4 * 2 + key % 2;
+}
+// Byte of 16-byte piece `piece` of a row of packed codes, as its TMA load swizzles it.
+template <int kD>
+__device__ __forceinline__ uint32_t fp4_piece(int row, int piece) {
+  return kD == 128 ? row * 64 + ((piece ^ (row / 2 % 4)) * 16) : row * 32 + ((piece ^ (row / 4 % 2)) * 16);
+}
+
+// Four warps: a thread unpacks a key to its lane of tensor memory, two columns
+// of the head a column.
+template <int kD, typename S>
+__device__ __forceinline__ void fp4_keys(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, const char* ring,
+                                         uint32_t tmem) {
+  const int lane = threadIdx.x & 31, x = threadIdx.x % 128, key = fp4_key(x);
+  const uint32_t to = tmem + ((uint32_t)(x / 32 * 32) << 16) + S::kK;
+  int g = 0;
+#pragma unroll 1
+  for (bool first = true; u.next(first); first = false) {
+    const int n = u.count(0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, ++g) {
+      const int stage = 2 * g % S::kStages, lap = 2 * g / S::kStages, buf = g % S::kBufs;
+      if (!mbar_wait(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a))) return;
+      const char* tile = ring + stage * S::kStageBytes;
+      uint4 w[kD / 32];
+      uint32_t scales[kD / 64];
+#pragma unroll
+      for (int p = 0; p < kD / 32; ++p) w[p] = *(const uint4*)(tile + fp4_piece<kD>(key, p));
+#pragma unroll
+      for (int p = 0; p < kD / 64; ++p)
+        scales[p] = *(const uint32_t*)(tile + S::kCodeBytes + key * (kD / 16) + p * 4);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&c->empty[stage]));
+      if (g >= S::kBufs &&
+          !mbar_wait(smem_addr(&c->k_free[buf]), (g / S::kBufs - 1) & 1, &c->abort_word, naps_of(a)))
+        return;
+      tc_fence_after();
+#pragma unroll
+      for (int p = 0; p < kD / 32; ++p) {
+        const uint32_t pair = fp4_scales(scales[p / 2] >> (p % 2 * 16));
+        const uint32_t s0 = __byte_perm(pair, 0, 0x1010), s1 = __byte_perm(pair, 0, 0x3232);
+        uint32_t r[16];
+        fp4_unpack(w[p].x, r);
+        fp4_unpack(w[p].y, r + 4);
+        fp4_unpack(w[p].z, r + 8);
+        fp4_unpack(w[p].w, r + 12);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) r[y] = mul_f16x2(r[y], y < 8 ? s0 : s1);
+        tmem_store16(to + buf * 64 + p * 16, r);
+      }
+      tmem_wait_store();
+      hand_over(&c->k_ready[buf]);
+    }
+  }
+}
+
+// Four warps: 32 columns of the head each, transposed.  ldmatrix gives lane l, of
+// 16 keys and 16 bytes of codes, the bytes l / 4 and l / 4 + 8 of keys 4 (l % 4)
+// to 4 (l % 4) + 3; even columns go to lanes 0 to 15 of tensor memory, odd ones
+// to lanes 16 to 31, two keys a column.  Scales become float16 in shared memory
+// first, by key: those past the request's length 0, whatever they were, so that
+// the values there are 0 too.
+template <int kD, typename S>
+__device__ __forceinline__ void fp4_values(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, const char* ring,
+                                           uint32_t tmem, char* scale_ptr) {
+  constexpr int kScales = kD / 16;
+  const int lane = threadIdx.x & 31, x = threadIdx.x % 128, warp = x / 32;
+  const bool active = warp < kD / 32;
+  const uint32_t to = tmem + ((uint32_t)(warp * 32) << 16) + S::kV;
+  int g = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (bool first = true; u.next(first); first = false) {
+    const int n = u.count(0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, ++g) {
+      const int stage = (2 * g + 1) % S::kStages, lap = (2 * g + 1) / S::kStages, buf = g % S::kBufs;
+      ok = ok && mbar_wait(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a));
+      const char* tile = ring + stage * S::kStageBytes;
+      __half* scales = (__half*)(scale_ptr + g % 2 * S::kValueScales);   // [kScales][128]
+      if (ok) {
+        const bool inside = (u.j0 + i) * S::kKeys + x < u.units.row.L;
+#pragma unroll
+        for (int p = 0; p < kScales / 4; ++p) {
+          const uint32_t w = *(const uint32_t*)(tile + S::kCodeBytes + x * kScales + p * 4);
+          const uint32_t s[2] = {inside ? fp4_scales(w) : 0, inside ? fp4_scales(w >> 16) : 0};
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            scales[(p * 4 + 2 * y) * 128 + x] = __low2half(*(const __half2*)&s[y]);
+            scales[(p * 4 + 2 * y + 1) * 128 + x] = __high2half(*(const __half2*)&s[y]);
+          }
+        }
+      }
+      // all four warps leave together, here
+      if (!vote_all(4, ok)) return;
+      ok = g < S::kBufs ||
+           mbar_wait(smem_addr(&c->v_free[buf]), (g / S::kBufs - 1) & 1, &c->abort_word, naps_of(a));
+      tc_fence_after();
+      if (ok && active) {
+#pragma unroll
+        for (int block = 0; block < 8; block += 2) {
+          const uint32_t from = smem_addr(tile) + fp4_piece<kD>(block * 16 + lane, warp);
+          uint32_t m[4];   // bytes l / 4 and l / 4 + 8 of two blocks of 16 keys
+          asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3])
+                       : "r"(from)
+                       : "memory");
+          uint32_t even[8], odd[8];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {   // half y % 2 of the bytes, block y / 2
+            const uint2 s = *(const uint2*)(scales + (warp * 2 + y % 2) * 128 + (block + y / 2) * 16 + lane % 4 * 4);
+            uint32_t r[4];
+            fp4_unpack(m[y], r);
+            const int at = y / 2 * 4 + y % 2;
+            even[at] = mul_f16x2(__byte_perm(r[0], r[1], 0x5410), s.x);
+            even[at + 2] = mul_f16x2(__byte_perm(r[2], r[3], 0x5410), s.y);
+            odd[at] = mul_f16x2(__byte_perm(r[0], r[1], 0x7632), s.x);
+            odd[at + 2] = mul_f16x2(__byte_perm(r[2], r[3], 0x7632), s.y);
+          }
+          tmem_store_16x16(to + buf * 64 + block * 8, even);
+          tmem_store_16x16(to + (16u << 16) + buf * 64 + block * 8, odd);
+        }
+        tmem_wait_store();
+      }
+      if (ok) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&c->empty[stage]));
+        hand_over(&c->v_ready[buf]);
       }
     }
   }
-  for (int x = 16; x > 0; x /= 2) l += __shfl_xor_sync(0xffffffffu, l, x);
-  const float inv = l == 0.f ? 0.f : a.v_gain / l;
-  const long long to = (long long)token * a.Hq + h;
-  for (int x = 0; x < kD / 64; ++x)
-    *(uint32_t*)(a.out + (to * kD + lane * (kD / 32) + 2 * x) * 2) = Element<E>::pack(o[2 * x] * inv, o[2 * x + 1] * inv);
-  if (a.lse && lane == 0) a.lse[to] = l == 0.f ? SV_NEG_INF : (m + log2f(l)) * 0.693147181f;
+}
+
+// ----------------------------------------------------------------- products
+// One warp.  The scores of a tile are issued before O += P V of the tile before
+// it, across units, so that a softmax never waits for that product.
+template <int kD, typename S>
+__device__ __forceinline__ void fp4_multiply(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, uint32_t q_smem,
+                                             uint32_t p_smem, uint32_t tmem) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t issue = lane == 0;
+  tmem = __shfl_sync(0xffffffffu, tmem, 0);
+  const uint64_t q_desc = tile_desc(q_smem, 16, 1024);
+  const uint64_t p_desc = tile_desc(p_smem, 128 * 128, 1024);
+  int g = 0, rounds = 0;
+  bool ok = true;
+  uint32_t before = 0;   // columns of the tile before, and whether it began its unit
+  bool began = false;
+
+  auto values = [&](int t) -> bool {   // O^T (+)= V^T P^T of tile t
+    const int buf = t % S::kBufs;
+    if (!mbar_wait(smem_addr(&c->v_ready[buf]), (t / S::kBufs) & 1, &c->abort_word, naps_of(a)) ||
+        !mbar_wait(smem_addr(&c->p_ready[t % 2]), (t / 2) & 1, &c->abort_word, naps_of(a)))
+      return false;
+    tc_fence_after();
+    const uint32_t desc = mma_desc(false, 128, (int)before, true);
+    const uint64_t p = p_desc + (t % 2) * (S::kPBytes / 16);
+#pragma unroll
+    for (int x = 0; x < S::kKeys / 16; ++x)
+      mma_tmem(tmem + S::kO, tmem + S::kV + buf * 64 + x * 8, p + x * (16 * 128 / 16), desc, !began || x > 0, issue);
+    tc_commit(smem_addr(&c->v_free[buf]), issue);
+    tc_commit(smem_addr(&c->pv_done[t % 2]), issue);
+    return true;
+  };
+
+#pragma unroll 1
+  for (bool first = true; ok && u.next(first); first = false) {
+    const int n = u.count(0);
+    if (n == 0) continue;
+    const uint32_t cols = (u.rows() + 15) / 16 * 16, desc = mma_desc(false, 128, (int)cols, false);
+    const int q_buf = rounds % 2;
+    if (!(ok = mbar_wait(smem_addr(&c->q_full[q_buf]), (rounds / 2) & 1, &c->abort_word, naps_of(a)))) break;
+    ++rounds;
+    const uint64_t q = q_desc + q_buf * (S::kQBytes / 16);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, ++g) {
+      const int buf = g % S::kBufs;
+      ok = mbar_wait(smem_addr(&c->k_ready[buf]), (g / S::kBufs) & 1, &c->abort_word, naps_of(a)) &&
+           (g < 2 || mbar_wait(smem_addr(&c->s_free[g % 2]), (g / 2 - 1) & 1, &c->abort_word, naps_of(a)));
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int d = 0; d < kD / 16; ++d)
+        mma_tmem(tmem + S::kS + g % 2 * S::kRows, tmem + S::kK + buf * 64 + d * 8,
+                 q + (d / 4) * (S::kRows * 128 / 16) + (d % 4) * 2, desc, d > 0, issue);
+      tc_commit(smem_addr(&c->s_full[g % 2]), issue);
+      tc_commit(smem_addr(&c->k_free[buf]), issue);
+      if (i == n - 1) tc_commit(smem_addr(&c->q_free[q_buf]), issue);
+      if (g > 0 && !(ok = values(g - 1))) break;
+      before = cols;
+      began = i == 0;
+    }
+  }
+  if (ok && g > 0) (void)values(g - 1);
+  // everything issued is done before the CTA's memory goes
+  tc_commit(smem_addr(&c->drain), issue);
+  (void)mbar_poll(smem_addr(&c->drain), 0, &c->calm, kNaps);
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ softmax
+// Sums over the warp of 32 values per lane: lane x gets that of v[x].
+__device__ __forceinline__ float warp_sums(float* v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool high = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = high ? v[i + o] : v[i], give = high ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return v[0];
+}
+
+// A group of four warps: rows [group * kCols, group * kCols + kCols) of the unit.
+// No warp leaves alone: what went wrong is told at the next vote.
+template <typename E, int kD, typename S>
+__device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, uint32_t tmem,
+                                            char* p_ptr, float* stats, long long quota, long long w1) {
+  constexpr int kCols = S::kCols;
+  constexpr bool kKeep = kCols <= 32;                     // scores stay in registers over the vote
+  const int lane = threadIdx.x & 31, x = threadIdx.x % 128, warp = x / 32, group = threadIdx.x / 128;
+  const int id = 1 + group;                               // of the group's barrier
+  const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+  const int my_key = fp4_key(x), place = fp4_place(my_key);
+  float* tops = stats + group * (7 * 64);                 // [warp][64], then of a row:
+  float* refs = tops + 4 * 64;                            // the negative reference
+  float* marks = refs + 64;                               // the reference, or its inverse sum
+  float* factors = marks + 64;
+  char* p_row = p_ptr + (kCols == 64 ? group * (128 * 128) : 0) + place * 128;
+  const uint32_t s_col = tmem + lanes + S::kS + group * kCols, o_col = tmem + lanes + S::kO + group * kCols;
+  int g = 0, rounds = 0, meetings = 0;
+  bool ok = true;
+
+#pragma unroll 1
+  for (bool first = true; u.next(first); first = false) {
+    const int n = u.count(0);
+    const int rows = min(kCols, u.rows() - group * kCols);  // of this group; none or fewer: no work
+    const int cols = (max(rows, 0) + 15) / 16 * 16;
+    float l[kCols];
+#pragma unroll
+    for (int y = 0; y < kCols; ++y) l[y] = 0.f;
+    float f = a.scale_log2;
+    if (n > 0) {
+      const int q_buf = rounds % 2;
+      ok = ok && mbar_wait(smem_addr(&c->q_full[q_buf]), (rounds / 2) & 1, &c->abort_word, naps_of(a));
+      f = ldexpf(f, c->q_exponent[q_buf]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&c->q_free[q_buf]));
+      ++rounds;
+    }
+    if (x < 64) marks[x] = SV_NEG_INF;
+    const unsigned long long f2 = f2_pack(f, f);
+    // keys that every row sees; past them row y sees a key from (key - common) G on
+    const int common = u.units.row.L - u.units.row.n + u.first(0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i, ++g) {
+      const int buf = g % 2, key0 = (u.j0 + i) * S::kKeys;
+      const int from = max(0, key0 + my_key - common) * a.G - group * kCols;   // the first row that sees the key
+      const bool masked = key0 + S::kKeys - 1 > common;
+      ok = ok && mbar_wait(smem_addr(&c->s_full[buf]), (g / 2) & 1, &c->abort_word, naps_of(a));
+      tc_fence_after();
+      const uint32_t s_at = s_col + buf * S::kRows;
+      uint32_t s[32];
+      // 32 scores, or their exponents once `refs` is set
+      auto scores = [&](int y0) {
+#pragma unroll
+        for (int y = 0; y < 32; y += 16)
+          if (y0 + y < cols) tmem_load16(s_at + y0 + y, s + y);
+        tmem_wait_load();
+        tmem_pin<32>(s);
+        if (masked)
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            if (y0 + y < from) s[y] = 0xff800000u;
+      };
+      auto exponents = [&](int y0) {
+#pragma unroll
+        for (int y = 0; y < 32; y += 4) {
+          if (y0 + (y & 16) >= cols) continue;
+          const float4 r = *(const float4*)(refs + y0 + y);
+          float e0, e1, e2, e3;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[y]), __uint_as_float(s[y + 1])), f2, f2_pack(r.x, r.y)), e0, e1);
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(s[y + 2]), __uint_as_float(s[y + 3])), f2, f2_pack(r.z, r.w)), e2, e3);
+          s[y] = __float_as_uint(e0), s[y + 1] = __float_as_uint(e1);
+          s[y + 2] = __float_as_uint(e2), s[y + 3] = __float_as_uint(e3);
+        }
+      };
+      bool raise = i == 0 || !ok;
+      if (!raise) {
+        float top = SV_NEG_INF;
+#pragma unroll
+        for (int y0 = 0; y0 < kCols; y0 += 32) {
+          if (y0 >= cols) continue;
+          scores(y0);
+          exponents(y0);
+#pragma unroll
+          for (int y = 0; y < 32; y += 2)
+            if (y0 + (y & 16) < cols) top = max3(top, __uint_as_float(s[y]), __uint_as_float(s[y + 1]));
+        }
+        raise = top > kSlack;
+      }
+      if (i == 0 || vote_any(id, raise)) {
+        if (!vote_all(id, ok)) return;
+        // maxima of the rows, over the warp's keys and then over the warps
+#pragma unroll 1
+        for (int y0 = 0; y0 < cols; y0 += 32) {
+          scores(y0);
+          float mine = SV_NEG_INF;
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
+            if (y0 + (y & 16) >= cols) continue;
+            const float top = redux_max(__uint_as_float(s[y]));
+            if (lane == y) mine = top;
+          }
+          tops[warp * 64 + y0 + lane] = mine;
+        }
+        (void)vote_any(id, false);
+        if (x < cols) {
+          const float high = fmaxf(fmaxf(tops[x], tops[64 + x]), fmaxf(tops[128 + x], tops[192 + x])) * f;
+          const float old = marks[x];
+          const bool up = i == 0 ? high > old : high > old + kSlack;
+          const float now = up ? high : old;
+          factors[x] = !up ? 1.f : old == SV_NEG_INF ? 0.f : ex2_approx(old - high);
+          marks[x] = now;
+          refs[x] = now == SV_NEG_INF ? 1e30f : -now;   // any finite score of such a row raises it
+        }
+        (void)vote_any(id, false);
+        if (i > 0) {
+#pragma unroll
+          for (int y = 0; y < kCols; ++y)
+            if (y < cols) l[y] *= factors[y];
+          ok = mbar_wait(smem_addr(&c->pv_done[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a));
+          tc_fence_after();
+          if (ok) {
+#pragma unroll 1
+            for (int y0 = 0; y0 < cols; y0 += 16) {
+              uint32_t o[16];
+              tmem_load16(o_col + y0, o);
+              tmem_wait_load();
+              tmem_pin<16>(o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * factors[y0 + y]);
+              tmem_store16(o_col + y0, o);
+            }
+            tmem_wait_store();
+          }
+        }
+        if (kKeep && cols > 0) {
+          scores(0);
+          exponents(0);
+        }
+      }
+      // P of the tile before the last has been read
+      if (ok && g >= 2)
+        ok = mbar_wait(smem_addr(&c->pv_done[buf]), (g / 2 - 1) & 1, &c->abort_word, naps_of(a));
+      if (!ok) continue;
+      char* p_at = p_row + buf * S::kPBytes;
+#pragma unroll
+      for (int y0 = 0; y0 < kCols; y0 += 32) {
+        if (y0 >= cols) continue;
+        if (!kKeep) {
+          scores(y0);
+          exponents(y0);
+        }
+#pragma unroll
+        for (int y = 0; y < 32; y += 8) {
+          if (y0 + (y & 16) >= cols) continue;
+          uint32_t p[4];
+#pragma unroll
+          for (int z = 0; z < 8; z += 2) {
+            const float p0 = ex2_approx(__uint_as_float(s[y + z])), p1 = ex2_approx(__uint_as_float(s[y + z + 1]));
+            f2_unpack(f2_add(f2_pack(l[y0 + y + z], l[y0 + y + z + 1]), f2_pack(p0, p1)), l[y0 + y + z], l[y0 + y + z + 1]);
+            p[z / 2] = pack2(p0, p1, __half());
+          }
+          *(uint4*)(p_at + (((y0 + y) / 8) ^ (place % 8)) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+        }
+      }
+      fence_async_shared();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_addr(&c->s_free[buf]));
+        mbar_arrive(smem_addr(&c->p_ready[buf]));
+      }
+    }
+    // ---- the unit's end: sums over the threads, results or a part of them
+    if (n > 0)
+      ok = ok && mbar_wait(smem_addr(&c->pv_done[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a));
+    tc_fence_after();
+#pragma unroll
+    for (int y0 = 0; y0 < kCols; y0 += 32)
+      if (y0 < cols) tops[warp * 64 + y0 + lane] = warp_sums(l + y0);
+    if (!vote_all(id, ok)) return;
+    const bool whole = u.j0 == 0 && u.j1 == u.tiles;
+    const int cta = blockIdx.x;
+    const long long ahead = w1 - u.left - u.pos - cta * quota;
+    const int c_first = cta - ranges_back(u.pos, quota);
+    const bool begins_late = ahead + (cta - c_first) * quota != 0;
+    const size_t slots = (size_t)gridDim.x * 2;
+    const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
+    const long long out_rows = (long long)a.T * a.Hq, part_rows = min((long long)slots * S::kRows, kAttnRows);
+    const int r0 = group * kCols;
+    const int token0 = u.units.row.begin + u.first(0);
+    if (x < rows) {
+      const float sum = tops[x] + tops[64 + x] + tops[128 + x] + tops[192 + x], mark = marks[x];
+      factors[x] = whole ? row_inverse(sum) * a.v_gain : a.v_gain;
+      if (whole) {
+        const long long row = (long long)(token0 + (r0 + x) / a.G) * a.Hq + u.h * a.G + (r0 + x) % a.G;
+        if (a.lse && in_array(a.flags, row, out_rows)) a.lse[row] = row_lse(mark, sum);
+      } else {
+        const long long row = (long long)slot * S::kRows + r0 + x;
+        if (in_array(a.flags, row, part_rows))
+          ((float2*)(a.partial + slots * S::kRows * kD))[row] = make_float2(mark, sum);
+      }
+    }
+    (void)vote_any(id, false);
+    if (warp < kD / 32) {
+      // lanes 0 to 15 have even columns of the head, 16 to 31 odd ones: they trade, so that a
+      // lane has two neighbours of one of two rows
+      const bool upper = lane >= 16;
+      const int column = warp * 32 + lane % 16 * 2;
+#pragma unroll 1
+      for (int y0 = 0; y0 < cols; y0 += 16) {
+        uint32_t o[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) o[y] = 0;
+        if (n > 0) {
+          tmem_load16(o_col + y0, o);
+          tmem_wait_load();
+          tmem_pin<16>(o);
+        }
+#pragma unroll
+        for (int y = 0; y < 16; y += 2) {
+          const float v0 = __uint_as_float(o[y]) * factors[y0 + y], v1 = __uint_as_float(o[y + 1]) * factors[y0 + y + 1];
+          const float other = __shfl_xor_sync(0xffffffffu, upper ? v0 : v1, 16);
+          const float lo = upper ? other : v0, hi = upper ? v1 : other;
+          const int r = y0 + y + upper;
+          if (r >= rows) continue;
+          if (whole) {
+            const long long row = (long long)(token0 + (r0 + r) / a.G) * a.Hq + u.h * a.G + (r0 + r) % a.G;
+            if (in_array(a.flags, row, out_rows)) *(uint32_t*)(a.out + (row * kD + column) * 2) = pack2(lo, hi, E());
+          } else {
+            const long long row = (long long)slot * S::kRows + r0 + r;
+            if (in_array(a.flags, row, part_rows)) *(float2*)(a.partial + row * kD + column) = make_float2(lo, hi);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+    if (whole) continue;
+    // the CTA that has the unit's last tile; tickets as in attn_softmax
+    const long long end = ahead + (long long)(u.tiles - 1) * S::kKeys;
+    const int c_last = u.j1 == u.tiles ? cta : cta + ranges_ahead(end, quota);
+    ok = soft_meet(c, meetings++, naps_of(a));
+    if (ok && threadIdx.x == 0) {
+      const bool last = in_array(a.flags, c_first, gridDim.x) &&
+                        take_ticket(&a.tickets[c_first]) == c_last - c_first;
+      if (last) a.tickets[c_first] = 0;
+      c->last = last;
+    }
+    ok = soft_meet(c, meetings++, naps_of(a)) && ok;
+    if (ok && c->last) {
+      const int parts = c_last - c_first + 1;
+      if (u.rows() * (kD / 4) <= S::kSoftThreads)
+        attn_join<E, kD, S, kD / 4, 8>(a, u, c_first, parts, begins_late);
+      else
+        attn_join<E, kD, S, 8, 2>(a, u, c_first, parts, begins_late);
+    }
+  }
+}
+
+template <typename E, int kD, int kRows>
+__global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, 1)
+    sv_fp4_attention_kernel(const __grid_constant__ Fp4Args a, const __grid_constant__ CUtensorMap k_map,
+                            const __grid_constant__ CUtensorMap v_map) {
+  using S = Fp4Shape<kD, kRows>;
+  extern __shared__ __align__(1024) char smem[];
+  char* q_ptr = smem;
+  char* p_ptr = q_ptr + 2 * S::kQBytes;
+  char* ring = p_ptr + 2 * S::kPBytes;
+  char* value_scales = ring + S::kStages * S::kStageBytes;
+  float* stats = (float*)(value_scales + 2 * S::kValueScales);
+  Fp4Control* c = (Fp4Control*)((char*)stats + S::kStatBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kSoft = S::kSoftThreads / 32, kKeyWarps = kSoft, kValueWarps = kSoft + 4, kLoader = kSoft + 8;
+
+  if (warp == kLoader && lane == 0) {
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(smem_addr(&c->full[i]), 1);
+      mbar_init(smem_addr(&c->empty[i]), 4);
+    }
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&c->q_full[i]), 1);
+      mbar_init(smem_addr(&c->q_free[i]), 1 + kSoft);
+      mbar_init(smem_addr(&c->k_ready[i]), 4);
+      mbar_init(smem_addr(&c->k_free[i]), 1);
+      mbar_init(smem_addr(&c->v_ready[i]), 4);
+      mbar_init(smem_addr(&c->v_free[i]), 1);
+      mbar_init(smem_addr(&c->s_full[i]), 1);
+      mbar_init(smem_addr(&c->s_free[i]), kSoft);
+      mbar_init(smem_addr(&c->p_ready[i]), kSoft);
+      mbar_init(smem_addr(&c->pv_done[i]), 1);
+    }
+    mbar_init(smem_addr(&c->drain), 1);
+    mbar_init(smem_addr(&c->met), kSoft);
+    mbar_init_fence();
+    c->abort_word = c->calm = 0;
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
+  }
+  if (warp == kLoader + 1) tmem_alloc<S::kTmemCols>(smem_addr(&c->tmem));
+  wait_for_preceding_grid();
+  const AttnRange range = attn_range<S>(a, c);
+  const uint32_t tmem = c->tmem;
+  if (range.w0 < range.w1) {
+    const AttnWalk<S> u(a, c->start, range.w1 - range.w0);
+    // Many rows: five warpgroups launched with 96 registers a thread, and
+    // 2 x 152 + 2 x 64 + 48 = 5 x 96.
+    if (warp < kKeyWarps) {
+      if (S::kGroups > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+      fp4_softmax<E, kD, S>(a, u, c, tmem, p_ptr, stats, range.quota, range.w1);
+    } else if (warp < kLoader) {
+      if (S::kGroups > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      if (warp < kValueWarps) fp4_keys<kD, S>(a, u, c, ring, tmem);
+      else fp4_values<kD, S>(a, u, c, ring, tmem, value_scales);
+    } else {
+      if (S::kGroups > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      if (warp == kLoader) fp4_load<kD, S>(a, u, c, ring, &k_map, &v_map);
+      else if (warp == kLoader + 1) fp4_multiply<kD, S>(a, u, c, smem_addr(q_ptr), smem_addr(p_ptr), tmem);
+      else if (warp == kLoader + 2) fp4_queries<E, kD, S>(a, u, c, q_ptr);
+    }
+  }
+  attn_finish<S, kD>(a, c, range.spoilt);
+  if (warp == kLoader + 1) tmem_free<S::kTmemCols>(tmem);
 }
 
 }  // namespace sv

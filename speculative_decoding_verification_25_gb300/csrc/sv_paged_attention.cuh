@@ -577,7 +577,8 @@ __device__ __forceinline__ float row_max(const uint32_t* bits) {
 }
 
 // All softmax warps meet (their `phase`-th meeting); false if it was given up.
-__device__ __forceinline__ bool soft_meet(AttnControl* c, int phase, int naps) {
+template <typename Control>
+__device__ __forceinline__ bool soft_meet(Control* c, int phase, int naps) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(&c->met));
   return mbar_wait(smem_addr(&c->met), phase & 1, &c->abort_word, naps);
@@ -907,50 +908,17 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
   }
 }
 
-template <typename E, int kD, bool kWide>
-__global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, kWide>::kCtasPerSm)
-    sv_paged_attention_kernel(const __grid_constant__ AttnArgs a,
-                              const __grid_constant__ CUtensorMap q_map,
-                              const __grid_constant__ CUtensorMap k_map,
-                              const __grid_constant__ CUtensorMap v_map) {
-  using S = AttnShape<kD, kWide>;
-  extern __shared__ __align__(1024) char smem[];
-  char* ring_ptr = smem + S::kTiles * S::kQBytes;
-  char* staging = ring_ptr + S::kStages * S::kStageBytes;
-  AttnControl* c = (AttnControl*)(staging + S::kTiles * 4 * S::kStagingBytes);
-  const uint32_t q_smem = smem_addr(smem), ring = smem_addr(ring_ptr);
+// A CTA's range [w0, w1) of the work, where it starts (left in `c->start`), and
+// whether an earlier call spoilt the workspace.  The whole CTA comes here, after
+// the preceding grid.
+struct AttnRange {
+  long long quota, w0, w1;
+  bool spoilt;
+};
+template <typename S, typename Control>
+__device__ __forceinline__ AttnRange attn_range(const AttnArgs& a, Control* c) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kLoader = S::kSoftThreads / 32, kIssuer = kLoader + 1;
-
-  // -------- set-up that reads nothing of the caller's
-  if (warp == kLoader && lane == 0) {
-#pragma unroll 1
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(smem_addr(&c->full[i]), 1);
-      mbar_init(smem_addr(&c->empty[i]), S::kTiles);
-    }
-    mbar_init(smem_addr(&c->q_full), 1);
-    mbar_init(smem_addr(&c->q_empty), S::kTiles);
-    mbar_init(smem_addr(&c->drain), S::kTiles);
-    mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
-#pragma unroll 1
-    for (int t = 0; t < S::kTiles; ++t) {
-      for (int k = 0; k < S::kBufs; ++k) {
-        mbar_init(smem_addr(&c->s_full[t][k]), 1);
-        mbar_init(smem_addr(&c->p_ready[t][k]), S::kTiles > 1 ? 5 : 4);   // with the turn
-      }
-      mbar_init(smem_addr(&c->pv_done[t]), 1);
-    }
-    mbar_init_fence();
-    c->abort_word = c->calm = c->past = 0;
-    tma_prefetch_map(&q_map);
-    tma_prefetch_map(&k_map);
-    tma_prefetch_map(&v_map);
-  }
-  if (warp == kIssuer) tmem_alloc<S::kTmemCols>(smem_addr(&c->tmem));
-  wait_for_preceding_grid();
-
-  // -------- weights of all requests, summed: thread i has rows [r0, r1)
+  // weights of all requests, summed: thread i has rows [r0, r1)
   const int per = (a.B + S::kThreads - 1) / S::kThreads;
   const int r0 = min(a.B, (int)threadIdx.x * per), r1 = min(a.B, r0 + per);
   // in flight with the lengths
@@ -1039,25 +1007,12 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     }
   }
   __syncthreads();
-  const uint32_t tmem = c->tmem;
+  return {quota, w0, w1, spoilt};
+}
 
-  if (w0 < w1) {
-    const AttnWalk<S> u(a, c->start, w1 - w0);
-    // Wide: three warpgroups launched with 168 registers a thread, and
-    // 2 x 216 + 72 = 3 x 168.  Three whole prompts: 633 us with 208 and 88, 629
-    // so, 798 with 224 and 56, which the issuers cannot do with.
-    if (warp >= kLoader) {
-      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      if (warp >= kIssuer && warp < kIssuer + S::kTiles)
-        attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem, warp - kIssuer);
-      else
-        attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map, warp == kLoader,
-                     !kWide || warp != kLoader);
-    } else {
-      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      attn_softmax<E, kD, S>(a, u, c, tmem, staging, quota, w1);
-    }
-  }
+// The rows behind the last request's, and what waits that ran out leave behind.
+template <typename S, int kD, typename Control>
+__device__ __forceinline__ void attn_finish(const AttnArgs& a, Control* c, bool spoilt) {
   // tokens past the last request's, or all of them
   const int used = spoilt ? 0 : min(max(a.cu_new[a.B], 0), a.T);
   const long long spare = (long long)(a.T - used) * a.Hq;
@@ -1081,6 +1036,73 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
     set_flag(a.flags, kDevTimeout);
     set_flag(a.status, kDevTimeout);
   }
+}
+
+template <typename E, int kD, bool kWide>
+__global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, kWide>::kCtasPerSm)
+    sv_paged_attention_kernel(const __grid_constant__ AttnArgs a,
+                              const __grid_constant__ CUtensorMap q_map,
+                              const __grid_constant__ CUtensorMap k_map,
+                              const __grid_constant__ CUtensorMap v_map) {
+  using S = AttnShape<kD, kWide>;
+  extern __shared__ __align__(1024) char smem[];
+  char* ring_ptr = smem + S::kTiles * S::kQBytes;
+  char* staging = ring_ptr + S::kStages * S::kStageBytes;
+  AttnControl* c = (AttnControl*)(staging + S::kTiles * 4 * S::kStagingBytes);
+  const uint32_t q_smem = smem_addr(smem), ring = smem_addr(ring_ptr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kLoader = S::kSoftThreads / 32, kIssuer = kLoader + 1;
+
+  // -------- set-up that reads nothing of the caller's
+  if (warp == kLoader && lane == 0) {
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(smem_addr(&c->full[i]), 1);
+      mbar_init(smem_addr(&c->empty[i]), S::kTiles);
+    }
+    mbar_init(smem_addr(&c->q_full), 1);
+    mbar_init(smem_addr(&c->q_empty), S::kTiles);
+    mbar_init(smem_addr(&c->drain), S::kTiles);
+    mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
+#pragma unroll 1
+    for (int t = 0; t < S::kTiles; ++t) {
+      for (int k = 0; k < S::kBufs; ++k) {
+        mbar_init(smem_addr(&c->s_full[t][k]), 1);
+        mbar_init(smem_addr(&c->p_ready[t][k]), S::kTiles > 1 ? 5 : 4);   // with the turn
+      }
+      mbar_init(smem_addr(&c->pv_done[t]), 1);
+    }
+    mbar_init_fence();
+    c->abort_word = c->calm = c->past = 0;
+    tma_prefetch_map(&q_map);
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
+  }
+  if (warp == kIssuer) tmem_alloc<S::kTmemCols>(smem_addr(&c->tmem));
+  wait_for_preceding_grid();
+
+  const AttnRange range = attn_range<S>(a, c);
+  const long long w0 = range.w0, w1 = range.w1, quota = range.quota;
+  const uint32_t tmem = c->tmem;
+
+  if (w0 < w1) {
+    const AttnWalk<S> u(a, c->start, w1 - w0);
+    // Wide: three warpgroups launched with 168 registers a thread, and
+    // 2 x 216 + 72 = 3 x 168.  Three whole prompts: 633 us with 208 and 88, 629
+    // so, 798 with 224 and 56, which the issuers cannot do with.
+    if (warp >= kLoader) {
+      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      if (warp >= kIssuer && warp < kIssuer + S::kTiles)
+        attn_multiply<E, kD, S>(a, u, c, q_smem, ring, ring_ptr, tmem, warp - kIssuer);
+      else
+        attn_load<S>(a, u, c, q_smem, ring, &q_map, &k_map, &v_map, warp == kLoader,
+                     !kWide || warp != kLoader);
+    } else {
+      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+      attn_softmax<E, kD, S>(a, u, c, tmem, staging, quota, w1);
+    }
+  }
+  attn_finish<S, kD>(a, c, range.spoilt);
   if (warp == kIssuer) tmem_free<S::kTmemCols>(tmem);
 }
 
