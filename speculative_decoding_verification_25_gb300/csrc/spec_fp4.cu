@@ -32,20 +32,22 @@ Fp4Device g_fp4[kMaxDevices];
 
 struct Variant {
   const void* fn;
-  int threads, smem_bytes, rows;
+  int threads, smem_bytes, ctas_per_sm, rows;
 };
 template <typename E, int kD, int kRows>
 Variant variant() {
   using S = sv::Fp4Shape<kD, kRows>;
-  return {(const void*)sv::sv_fp4_attention_kernel<E, kD, kRows>, S::kThreads, S::kSmemBytes, kRows};
+  return {(const void*)sv::sv_fp4_attention_kernel<E, kD, kRows>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, kRows};
 }
-template <typename E>
-Variant variant_of(int D, bool many) {
-  if (D == 128) return many ? variant<E, 128, 128>() : variant<E, 128, 32>();
-  return many ? variant<E, 64, 128>() : variant<E, 64, 32>();
+template <typename E, int kD>
+Variant variant_of(int rows) {
+  return rows <= 16 ? variant<E, kD, 16>() : rows <= 32 ? variant<E, kD, 32>() : variant<E, kD, 128>();
 }
-Variant variant_of(int dtype, int D, bool many) {
-  return dtype == SV_BF16 ? variant_of<__nv_bfloat16>(D, many) : variant_of<__half>(D, many);
+// The variant whose units have at least `rows` rows, or the largest.
+Variant variant_of(int dtype, int D, int rows) {
+  if (dtype == SV_BF16)
+    return D == 128 ? variant_of<__nv_bfloat16, 128>(rows) : variant_of<__nv_bfloat16, 64>(rows);
+  return D == 128 ? variant_of<__half, 128>(rows) : variant_of<__half, 64>(rows);
 }
 
 // SM count, shared memory limits and the tensor map encoder; once per device.
@@ -55,8 +57,8 @@ Fp4Device* fp4_device() {
   Fp4Device& d = g_fp4[dev];
   std::call_once(d.once, [&d, dev]() {
     d.error = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev);
-    for (int i = 0; i < 8 && d.error == cudaSuccess; ++i) {
-      const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, i & 4);
+    for (int i = 0; i < 12 && d.error == cudaSuccess; ++i) {
+      const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, i < 4 ? 16 : i < 8 ? 32 : 128);
       d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
     }
     if (d.error == cudaSuccess) d.error = sv::find_encoder(&d.encode);
@@ -114,9 +116,10 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   if (!dev) return SV_ERR_CUDA;
   const int G = Hq / Hk;
   // The host knows the mean of a request's rows (the G heads of its tokens on one key head) alone.
-  const bool many = G > 32 || (long long)T * G > 32ll * (B > 0 ? B : 1);
-  const Variant v = variant_of(dtype, D, many);
-  const int ctas = dev->sm_count < sv::kAttnMaxCtas ? dev->sm_count : sv::kAttnMaxCtas;
+  const long long mean = ((long long)T * G + (B > 0 ? B : 1) - 1) / (B > 0 ? B : 1);
+  const Variant v = variant_of(dtype, D, mean > G ? (mean < 128 ? (int)mean : 128) : G);
+  int ctas = dev->sm_count * v.ctas_per_sm;
+  if (ctas > sv::kAttnMaxCtas) ctas = sv::kAttnMaxCtas;
 
   sv::Fp4Args a;
   a.block_table = block_table;

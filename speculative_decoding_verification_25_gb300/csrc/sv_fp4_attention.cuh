@@ -50,27 +50,28 @@ struct Fp4Shape {
   static constexpr int kThreads = kSoftThreads + 2 * 128 + 128;
   static constexpr int kBlocks = kD / 64;
   static constexpr int kQBytes = kRows * kD * 2;           // two of them
-  static constexpr int kPBytes = 128 * 128 * ((kRows + 63) / 64);   // two of them
+  static constexpr int kPRow = kRows < 64 ? kRows * 2 : 128;   // bytes of a row of P^T, in blocks of 64 rows of the unit
+  static constexpr int kPBytes = 128 * kPRow * ((kRows + 63) / 64);   // two of them
   static constexpr int kCodeBytes = 128 * kD / 2, kScaleBytes = 128 * kD / 16;
   static constexpr int kStageBytes = kCodeBytes + kScaleBytes;
-  static constexpr int kBufs = kRows > 64 ? 1 : 2;         // of keys and of values in tensor memory
-  static constexpr int kValueScales = 128 * (kD / 16) * 2; // float16, two of them
+  static constexpr int kCtasPerSm = kRows > 16 ? 1 : 2;
+  static constexpr int kTmemCols = 512 / kCtasPerSm;
+  static constexpr int kValueScales = 128 * (kD / 16) * 2; // float16
   static constexpr int kControlBytes = 1024;
   static constexpr int kStatBytes = kGroups * 64 * 4 * (4 + 3);   // of four warps, and three of a row
-  static constexpr int kFixedBytes = 2 * (kQBytes + kPBytes + kValueScales) + kControlBytes + kStatBytes;
-  static constexpr int kMostStages = (227 * 1024 - 1024 - kFixedBytes) / kStageBytes;
-  static constexpr int kStages = kMostStages / 2 * 2 < 16 ? kMostStages / 2 * 2 : 16;
+  static constexpr int kFixedBytes = 2 * (kQBytes + kPBytes) + kValueScales + kControlBytes + kStatBytes;
+  static constexpr int kMostStages = (228 * 1024 / kCtasPerSm - 1024 - kFixedBytes) / kStageBytes;
+  static constexpr int kStages = kMostStages >= 16 ? 16 : kMostStages >= 8 ? 8 : 4;   // a power of two
   static constexpr int kSmemBytes = kFixedBytes + kStages * kStageBytes;
   // columns of tensor memory
-  static constexpr int kS = 0, kO = 2 * kRows, kK = 3 * kRows, kV = kK + kBufs * 64, kTmemCols = 512;
-  static_assert(kV + kBufs * 64 <= kTmemCols, "fits");
-  static_assert(kStages >= 4, "fits");
+  static constexpr int kS = 0, kO = 2 * kRows, kK = 3 * kRows, kV = kK + 64;
+  static_assert(kV + 64 <= kTmemCols, "fits");
+  static_assert(kMostStages >= 4, "fits");
 };
 
 struct Fp4Control {
   uint64_t full[16], empty[16];
-  uint64_t q_full[2], q_free[2], k_ready[2], k_free[2], v_ready[2], v_free[2];
-  uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2];
+  uint64_t q_full[2], q_free[2], k_ready, s_full[2], pv_ready[2], pv_done[2];
   uint64_t drain, met;
   uint32_t tmem;
   int abort_word, calm, last;
@@ -102,17 +103,19 @@ __device__ __forceinline__ float redux_max(float x) {
 }
 
 // ------------------------------------------------------------------- loader
-// Key and value tiles as they are packed, alternating in the ring: lanes 0 to 15
-// bring a page's codes each, lanes 16 to 31 its scales, which lie in a row (a
-// tiled copy wants 128 bytes).  Rows of pages past the request's length stay as
-// they are; a page outside the cache has scales of zero.
+// One warp for keys and one for values: tiles as they are packed, which
+// alternate in the ring.  Lanes 0 to 15 bring a page's codes each, lanes 16 to 31 its
+// scales, which lie in a row (a tiled copy wants 128 bytes).  Rows of pages past the
+// request's length stay as they are; a page outside the cache has scales of zero.
+// A copy's issue takes about 50 clocks: pages of 16 make 16 of a tile.
 template <int kD, typename S>
 __device__ __forceinline__ void fp4_load(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, char* ring,
-                                         const CUtensorMap* k_map, const CUtensorMap* v_map) {
+                                         const CUtensorMap* map, const uint8_t* scales, int values) {
+  constexpr int kAhead = 4;   // tiles whose pages are looked up ahead
   const int lane = threadIdx.x & 31;
   const int page = 1 << a.page_shift, box = min(page, S::kKeys), boxes = S::kKeys / box;
   const int mine = lane % 16, none = (a.n_pages * a.Hk) << a.page_shift;   // one past the cache's rows
-  int it = 0;
+  int it = values;
   bool ok = true, bad = false;
 
   // First row, in the cache, of the lane's box of key tile j; -1 if it has none.
@@ -126,10 +129,10 @@ __device__ __forceinline__ void fp4_load(const Fp4Args& a, AttnWalk<S> u, Fp4Con
     bad = true;
     return none;
   };
-  auto bring = [&](const CUtensorMap* codes, const uint8_t* scales, int y) -> bool {
+  auto bring = [&](int y) -> bool {
     const int stage = it % S::kStages, lap = it / S::kStages;
     if (lap > 0 &&
-        !mbar_wait(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, naps_of(a)))
+        !mbar_await(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, naps_of(a)))
       return false;
     const uint32_t bar = smem_addr(&c->full[stage]);
     char* to = ring + stage * S::kStageBytes;
@@ -144,10 +147,10 @@ __device__ __forceinline__ void fp4_load(const Fp4Args& a, AttnWalk<S> u, Fp4Con
     if (lane == 0)
       mbar_arrive_expect(bar, __popc(code_lanes) * box * (kD / 2) + __popc(scale_lanes) * box * (kD / 16));
     __syncwarp();
-    if (y >= 0 && lane < 16) tma_load_2d(smem_addr(to + mine * box * (kD / 2)), codes, 0, y, bar);
+    if (y >= 0 && lane < 16) tma_load_2d(smem_addr(to + mine * box * (kD / 2)), map, 0, y, bar);
     if (y >= 0 && y < none && lane >= 16)
       bulk_load(smem_addr(scale_to), scales + (long long)y * (kD / 16), box * (kD / 16), bar);
-    ++it;
+    it += 2;
     return true;
   };
 
@@ -155,19 +158,22 @@ __device__ __forceinline__ void fp4_load(const Fp4Args& a, AttnWalk<S> u, Fp4Con
   for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.count(0);
     if (n == 0) continue;
-    int y = box_row(u.j0);
+    int y[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) y[i] = i < n ? box_row(u.j0 + i) : -1;
 #pragma unroll 1
     for (int i = 0; ok && i < n; ++i) {
-      const int next = i + 1 < n ? box_row(u.j0 + i + 1) : -1;
-      ok = bring(k_map, a.k_scales, y);
-      if (ok) ok = bring(v_map, a.v_scales, y);
-      y = next;
+      const int next = i + kAhead < n ? box_row(u.j0 + i + kAhead) : -1;
+      ok = bring(y[0]);
+#pragma unroll
+      for (int x = 0; x + 1 < kAhead; ++x) y[x] = y[x + 1];
+      y[kAhead - 1] = next;
     }
   }
   if (bad) set_flag(a.flags, kDevBadPage);
   // copies in flight land in this CTA's memory, which has to outlive them
 #pragma unroll 1
-  for (int i = max(0, it - S::kStages); i < it; ++i)
+  for (int i = max(values, it - S::kStages); i < it; i += 2)
     (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->calm, kNaps);
   __syncwarp();
 }
@@ -185,7 +191,7 @@ __device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4
   for (bool first = true; u.next(first); first = false) {
     if (u.count(0) == 0) continue;
     const int buf = rounds % 2, rows = u.rows(), cols = (rows + 15) / 16 * 16;
-    if (rounds >= 2 && !mbar_wait(smem_addr(&c->q_free[buf]), (rounds / 2 - 1) & 1, &c->abort_word, naps_of(a)))
+    if (rounds >= 2 && !mbar_await(smem_addr(&c->q_free[buf]), (rounds / 2 - 1) & 1, &c->abort_word, naps_of(a)))
       break;
     char* to = q_ptr + buf * S::kQBytes + (part / 8) * (S::kRows * 128);
     auto load = [&](int row, uint32_t (&w)[4]) {
@@ -238,16 +244,16 @@ __device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4
 }
 
 // --------------------------------------------------------------- unpacking
-// The key of lane x of a tile's 128: chosen so that the 16 of a block come in the
-// order in which the values' columns do (see fp4_values), and that eight lanes in
-// a row meet no bank conflict, neither in the packed keys nor in P.
+// Within a block of 32 keys, key 16 h + 4 c + j.  The values' columns (see
+// fp4_values) put it at place 8 j + 2 c + h of P^T.  The key of lane x is chosen
+// so that eight lanes in a row meet no bank conflict, neither in the packed
+// keys (differing key mod 8) nor in P^T (differing place mod 8).
 __device__ __forceinline__ int fp4_key(int x) {
-  const int a = x % 8 / 2, j = 2 * ((a >= 2) != (x % 16 >= 8)) + x % 2;
-  return x / 16 * 16 + 4 * a + j;
+  const int c = x % 8 / 2, h = x % 2, j = (2 * (c / 2) + h + x % 32 / 8) % 4;
+  return x / 32 * 32 + 16 * h + 4 * c + j;
 }
-// Where P^T has the key: the order of the values' columns within a block.
 __device__ __forceinline__ int fp4_place(int key) {
-  return key / 16 * 16 + key % 4 / 2 * 8 + key % 16 / 4 * 2 + key % 2;
+  return key / 32 * 32 + 8 * (key % 4) + 2 * (key % 16 / 4) + key % 32 / 16;
 }
 // Byte of 16-byte piece `piece` of a row of packed codes, as its TMA load swizzles it.
 template <int kD>
@@ -268,8 +274,8 @@ __device__ __forceinline__ void fp4_keys(const Fp4Args& a, AttnWalk<S> u, Fp4Con
     const int n = u.count(0);
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++g) {
-      const int stage = 2 * g % S::kStages, lap = 2 * g / S::kStages, buf = g % S::kBufs;
-      if (!mbar_wait(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a))) return;
+      const int stage = 2 * g % S::kStages, lap = 2 * g / S::kStages;
+      if (!mbar_await(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a))) return;
       const char* tile = ring + stage * S::kStageBytes;
       uint4 w[kD / 32];
       uint32_t scales[kD / 64];
@@ -280,8 +286,8 @@ __device__ __forceinline__ void fp4_keys(const Fp4Args& a, AttnWalk<S> u, Fp4Con
         scales[p] = *(const uint32_t*)(tile + S::kCodeBytes + key * (kD / 16) + p * 4);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&c->empty[stage]));
-      if (g >= S::kBufs &&
-          !mbar_wait(smem_addr(&c->k_free[buf]), (g / S::kBufs - 1) & 1, &c->abort_word, naps_of(a)))
+      // the scores of the tile before are done, and its keys free
+      if (g > 0 && !mbar_await(smem_addr(&c->s_full[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a)))
         return;
       tc_fence_after();
 #pragma unroll
@@ -295,120 +301,122 @@ __device__ __forceinline__ void fp4_keys(const Fp4Args& a, AttnWalk<S> u, Fp4Con
         fp4_unpack(w[p].w, r + 12);
 #pragma unroll
         for (int y = 0; y < 16; ++y) r[y] = mul_f16x2(r[y], y < 8 ? s0 : s1);
-        tmem_store16(to + buf * 64 + p * 16, r);
+        tmem_store16(to + p * 16, r);
       }
       tmem_wait_store();
-      hand_over(&c->k_ready[buf]);
+      hand_over(&c->k_ready);
     }
   }
 }
 
 // Four warps: 32 columns of the head each, transposed.  ldmatrix gives lane l, of
-// 16 keys and 16 bytes of codes, the bytes l / 4 and l / 4 + 8 of keys 4 (l % 4)
-// to 4 (l % 4) + 3; even columns go to lanes 0 to 15 of tensor memory, odd ones
-// to lanes 16 to 31, two keys a column.  Scales become float16 in shared memory
-// first, by key: those past the request's length 0, whatever they were, so that
-// the values there are 0 too.
+// 16 keys and 16 bytes of codes, the bytes l / 4 and l / 4 + 8 of keys 4 c to
+// 4 c + 3, c = l % 4.  The halves of two blocks' bytes are put together, so that a
+// byte has one column of keys 4 c + j and 16 + 4 c + j and unpacks to a column
+// of tensor memory; even columns of the head go to lanes 0 to 15, odd ones to 16
+// to 31.  Scales become float16 pairs of those keys in shared memory first (the
+// warp's two groups): those past the request's length 0, whatever they were, so
+// that the values there are 0 too.
 template <int kD, typename S>
 __device__ __forceinline__ void fp4_values(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, const char* ring,
                                            uint32_t tmem, char* scale_ptr) {
-  constexpr int kScales = kD / 16;
-  const int lane = threadIdx.x & 31, x = threadIdx.x % 128, warp = x / 32;
+  constexpr uint32_t kLow = 0x0f0f0f0fu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x % 128 / 32;
   const bool active = warp < kD / 32;
   const uint32_t to = tmem + ((uint32_t)(warp * 32) << 16) + S::kV;
+  uint32_t* scales = (uint32_t*)(scale_ptr + (active ? warp : 0) * 512);   // [2][64] pairs
   int g = 0;
-  bool ok = true;
 #pragma unroll 1
   for (bool first = true; u.next(first); first = false) {
     const int n = u.count(0);
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++g) {
-      const int stage = (2 * g + 1) % S::kStages, lap = (2 * g + 1) / S::kStages, buf = g % S::kBufs;
-      ok = ok && mbar_wait(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a));
+      const int stage = (2 * g + 1) % S::kStages, lap = (2 * g + 1) / S::kStages;
+      if (!mbar_await(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a))) return;
       const char* tile = ring + stage * S::kStageBytes;
-      __half* scales = (__half*)(scale_ptr + g % 2 * S::kValueScales);   // [kScales][128]
-      if (ok) {
-        const bool inside = (u.j0 + i) * S::kKeys + x < u.units.row.L;
+      if (active) {
+        const int left = u.units.row.L - (u.j0 + i) * S::kKeys;   // keys of the tile within the request
 #pragma unroll
-        for (int p = 0; p < kScales / 4; ++p) {
-          const uint32_t w = *(const uint32_t*)(tile + S::kCodeBytes + x * kScales + p * 4);
-          const uint32_t s[2] = {inside ? fp4_scales(w) : 0, inside ? fp4_scales(w >> 16) : 0};
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            scales[(p * 4 + 2 * y) * 128 + x] = __low2half(*(const __half2*)&s[y]);
-            scales[(p * 4 + 2 * y + 1) * 128 + x] = __high2half(*(const __half2*)&s[y]);
-          }
+        for (int y = 0; y < 2; ++y) {   // pairs lane and 32 + lane
+          const int key = (y * 2 + lane / 16) * 32 + lane % 16;
+          const char* from = tile + S::kCodeBytes + key * (kD / 16) + warp * 2;
+          const uint32_t s0 = key < left ? fp4_scales(*(const uint16_t*)from) : 0;
+          const uint32_t s1 = key + 16 < left ? fp4_scales(*(const uint16_t*)(from + kD)) : 0;
+          scales[y * 32 + lane] = __byte_perm(s0, s1, 0x5410);
+          scales[64 + y * 32 + lane] = __byte_perm(s0, s1, 0x7632);
         }
       }
-      // all four warps leave together, here
-      if (!vote_all(4, ok)) return;
-      ok = g < S::kBufs ||
-           mbar_wait(smem_addr(&c->v_free[buf]), (g / S::kBufs - 1) & 1, &c->abort_word, naps_of(a));
+      // O += P V of the tile before is done, and its values free
+      if (g > 0 && !mbar_await(smem_addr(&c->pv_done[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a)))
+        return;
       tc_fence_after();
-      if (ok && active) {
+      if (active) {
+        __syncwarp();
 #pragma unroll
-        for (int block = 0; block < 8; block += 2) {
-          const uint32_t from = smem_addr(tile) + fp4_piece<kD>(block * 16 + lane, warp);
-          uint32_t m[4];   // bytes l / 4 and l / 4 + 8 of two blocks of 16 keys
+        for (int block = 0; block < 4; ++block) {   // of 32 keys
+          const uint32_t from = smem_addr(tile) + fp4_piece<kD>(block * 32 + lane, warp);
+          uint32_t m[4];   // bytes l / 4 and l / 4 + 8 of the first 16 keys, and of the others
           asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                        : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3])
                        : "r"(from)
                        : "memory");
           uint32_t even[8], odd[8];
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {   // half y % 2 of the bytes, block y / 2
-            const uint2 s = *(const uint2*)(scales + (warp * 2 + y % 2) * 128 + (block + y / 2) * 16 + lane % 4 * 4);
+          for (int h = 0; h < 2; ++h) {
+            const uint4 s = *(const uint4*)(scales + h * 64 + block * 16 + lane % 4 * 4);
             uint32_t r[4];
-            fp4_unpack(m[y], r);
-            const int at = y / 2 * 4 + y % 2;
-            even[at] = mul_f16x2(__byte_perm(r[0], r[1], 0x5410), s.x);
-            even[at + 2] = mul_f16x2(__byte_perm(r[2], r[3], 0x5410), s.y);
-            odd[at] = mul_f16x2(__byte_perm(r[0], r[1], 0x7632), s.x);
-            odd[at + 2] = mul_f16x2(__byte_perm(r[2], r[3], 0x7632), s.y);
+            fp4_unpack((m[h] & kLow) | (m[2 + h] << 4 & ~kLow), r);
+            even[h] = mul_f16x2(r[0], s.x);
+            even[2 + h] = mul_f16x2(r[1], s.y);
+            even[4 + h] = mul_f16x2(r[2], s.z);
+            even[6 + h] = mul_f16x2(r[3], s.w);
+            fp4_unpack((m[h] >> 4 & kLow) | (m[2 + h] & ~kLow), r);
+            odd[h] = mul_f16x2(r[0], s.x);
+            odd[2 + h] = mul_f16x2(r[1], s.y);
+            odd[4 + h] = mul_f16x2(r[2], s.z);
+            odd[6 + h] = mul_f16x2(r[3], s.w);
           }
-          tmem_store_16x16(to + buf * 64 + block * 8, even);
-          tmem_store_16x16(to + (16u << 16) + buf * 64 + block * 8, odd);
+          tmem_store_16x16(to + block * 16, even);
+          tmem_store_16x16(to + (16u << 16) + block * 16, odd);
         }
         tmem_wait_store();
       }
-      if (ok) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&c->empty[stage]));
-        hand_over(&c->v_ready[buf]);
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&c->empty[stage]));
+      hand_over(&c->pv_ready[g % 2]);
     }
   }
 }
 
 // ----------------------------------------------------------------- products
 // One warp.  The scores of a tile are issued before O += P V of the tile before
-// it, across units, so that a softmax never waits for that product.
+// it, across units, so that a softmax does not wait for that product.  In this
+// order the scores of a tile come after the softmax of the tile whose buffer they
+// take, and when they are done so is O += P V of that tile, which leaves P's.  (A
+// wait sees a phase's parity alone: products are told by two barriers in turn, so
+// that whoever waits for one knows that the one before it on its barrier is done.)
 template <int kD, typename S>
 __device__ __forceinline__ void fp4_multiply(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, uint32_t q_smem,
                                              uint32_t p_smem, uint32_t tmem) {
-  const int lane = threadIdx.x & 31;
-  const uint32_t issue = lane == 0;
-  tmem = __shfl_sync(0xffffffffu, tmem, 0);
   const uint64_t q_desc = tile_desc(q_smem, 16, 1024);
-  const uint64_t p_desc = tile_desc(p_smem, 128 * 128, 1024);
+  const uint64_t p_desc = tile_desc(p_smem, 128 * 128, 8 * S::kPRow, S::kPRow);
   int g = 0, rounds = 0;
   bool ok = true;
   uint32_t before = 0;   // columns of the tile before, and whether it began its unit
   bool began = false;
 
   auto values = [&](int t) -> bool {   // O^T (+)= V^T P^T of tile t
-    const int buf = t % S::kBufs;
-    if (!mbar_wait(smem_addr(&c->v_ready[buf]), (t / S::kBufs) & 1, &c->abort_word, naps_of(a)) ||
-        !mbar_wait(smem_addr(&c->p_ready[t % 2]), (t / 2) & 1, &c->abort_word, naps_of(a)))
-      return false;
+    if (!mbar_await(smem_addr(&c->pv_ready[t % 2]), (t / 2) & 1, &c->abort_word, naps_of(a))) return false;
     tc_fence_after();
     const uint32_t desc = mma_desc(false, 128, (int)before, true);
     const uint64_t p = p_desc + (t % 2) * (S::kPBytes / 16);
+    if (elect_one()) {
 #pragma unroll
-    for (int x = 0; x < S::kKeys / 16; ++x)
-      mma_tmem(tmem + S::kO, tmem + S::kV + buf * 64 + x * 8, p + x * (16 * 128 / 16), desc, !began || x > 0, issue);
-    tc_commit(smem_addr(&c->v_free[buf]), issue);
-    tc_commit(smem_addr(&c->pv_done[t % 2]), issue);
+      for (int x = 0; x < S::kKeys / 16; ++x)
+        mma_tmem_one(tmem + S::kO, tmem + S::kV + x * 8, p + x * S::kPRow, desc, !began || x > 0);
+      tc_commit_one(smem_addr(&c->pv_done[t % 2]));
+    }
+    __syncwarp();
     return true;
   };
 
@@ -418,23 +426,22 @@ __device__ __forceinline__ void fp4_multiply(const Fp4Args& a, AttnWalk<S> u, Fp
     if (n == 0) continue;
     const uint32_t cols = (u.rows() + 15) / 16 * 16, desc = mma_desc(false, 128, (int)cols, false);
     const int q_buf = rounds % 2;
-    if (!(ok = mbar_wait(smem_addr(&c->q_full[q_buf]), (rounds / 2) & 1, &c->abort_word, naps_of(a)))) break;
+    if (!(ok = mbar_await(smem_addr(&c->q_full[q_buf]), (rounds / 2) & 1, &c->abort_word, naps_of(a)))) break;
     ++rounds;
     const uint64_t q = q_desc + q_buf * (S::kQBytes / 16);
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++g) {
-      const int buf = g % S::kBufs;
-      ok = mbar_wait(smem_addr(&c->k_ready[buf]), (g / S::kBufs) & 1, &c->abort_word, naps_of(a)) &&
-           (g < 2 || mbar_wait(smem_addr(&c->s_free[g % 2]), (g / 2 - 1) & 1, &c->abort_word, naps_of(a)));
-      if (!ok) break;
+      if (!(ok = mbar_await(smem_addr(&c->k_ready), g & 1, &c->abort_word, naps_of(a)))) break;
       tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-      for (int d = 0; d < kD / 16; ++d)
-        mma_tmem(tmem + S::kS + g % 2 * S::kRows, tmem + S::kK + buf * 64 + d * 8,
-                 q + (d / 4) * (S::kRows * 128 / 16) + (d % 4) * 2, desc, d > 0, issue);
-      tc_commit(smem_addr(&c->s_full[g % 2]), issue);
-      tc_commit(smem_addr(&c->k_free[buf]), issue);
-      if (i == n - 1) tc_commit(smem_addr(&c->q_free[q_buf]), issue);
+        for (int d = 0; d < kD / 16; ++d)
+          mma_tmem_one(tmem + S::kS + g % 2 * S::kRows, tmem + S::kK + d * 8,
+                       q + (d / 4) * (S::kRows * 128 / 16) + (d % 4) * 2, desc, d > 0);
+        tc_commit_one(smem_addr(&c->s_full[g % 2]));
+        if (i == n - 1) tc_commit_one(smem_addr(&c->q_free[q_buf]));
+      }
+      __syncwarp();
       if (g > 0 && !(ok = values(g - 1))) break;
       before = cols;
       began = i == 0;
@@ -442,17 +449,21 @@ __device__ __forceinline__ void fp4_multiply(const Fp4Args& a, AttnWalk<S> u, Fp
   }
   if (ok && g > 0) (void)values(g - 1);
   // everything issued is done before the CTA's memory goes
-  tc_commit(smem_addr(&c->drain), issue);
+  if (elect_one()) tc_commit_one(smem_addr(&c->drain));
   (void)mbar_poll(smem_addr(&c->drain), 0, &c->calm, kNaps);
   __syncwarp();
 }
 
 // ------------------------------------------------------------------ softmax
-// Sums over the warp of 32 values per lane: lane x gets that of v[x].
+// Sums over the warp of kCount values per lane: lane x gets that of v[x % kCount].
+template <int kCount>
 __device__ __forceinline__ float warp_sums(float* v) {
   const int lane = threadIdx.x & 31;
+  if (kCount == 16)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+    for (int i = 0; i < kCount; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+#pragma unroll
+  for (int o = kCount / 2; o > 0; o >>= 1) {
     const bool high = lane & o;
 #pragma unroll
     for (int i = 0; i < o; ++i) {
@@ -469,6 +480,7 @@ template <typename E, int kD, typename S>
 __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, uint32_t tmem,
                                             char* p_ptr, float* stats, long long quota, long long w1) {
   constexpr int kCols = S::kCols;
+  constexpr int kChunk = kCols < 32 ? kCols : 32;
   constexpr bool kKeep = kCols <= 32;                     // scores stay in registers over the vote
   const int lane = threadIdx.x & 31, x = threadIdx.x % 128, warp = x / 32, group = threadIdx.x / 128;
   const int id = 1 + group;                               // of the group's barrier
@@ -478,7 +490,9 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
   float* refs = tops + 4 * 64;                            // the negative reference
   float* marks = refs + 64;                               // the reference, or its inverse sum
   float* factors = marks + 64;
-  char* p_row = p_ptr + (kCols == 64 ? group * (128 * 128) : 0) + place * 128;
+  // 16-byte pieces of the thread's row of P^T, as the product's layout swizzles them
+  const int turn = S::kPRow == 128 ? place % 8 : S::kPRow == 64 ? place / 2 % 4 : place / 4 % 2;
+  char* p_row = p_ptr + group * (128 * 128) + place * S::kPRow;
   const uint32_t s_col = tmem + lanes + S::kS + group * kCols, o_col = tmem + lanes + S::kO + group * kCols;
   int g = 0, rounds = 0, meetings = 0;
   bool ok = true;
@@ -494,7 +508,7 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
     float f = a.scale_log2;
     if (n > 0) {
       const int q_buf = rounds % 2;
-      ok = ok && mbar_wait(smem_addr(&c->q_full[q_buf]), (rounds / 2) & 1, &c->abort_word, naps_of(a));
+      ok = ok && mbar_await(smem_addr(&c->q_full[q_buf]), (rounds / 2) & 1, &c->abort_word, naps_of(a));
       f = ldexpf(f, c->q_exponent[q_buf]);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&c->q_free[q_buf]));
@@ -509,25 +523,25 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
       const int buf = g % 2, key0 = (u.j0 + i) * S::kKeys;
       const int from = max(0, key0 + my_key - common) * a.G - group * kCols;   // the first row that sees the key
       const bool masked = key0 + S::kKeys - 1 > common;
-      ok = ok && mbar_wait(smem_addr(&c->s_full[buf]), (g / 2) & 1, &c->abort_word, naps_of(a));
+      ok = ok && mbar_await(smem_addr(&c->s_full[buf]), (g / 2) & 1, &c->abort_word, naps_of(a));
       tc_fence_after();
       const uint32_t s_at = s_col + buf * S::kRows;
-      uint32_t s[32];
-      // 32 scores, or their exponents once `refs` is set
+      uint32_t s[kChunk];
+      // a chunk's scores, or their exponents once `refs` is set
       auto scores = [&](int y0) {
 #pragma unroll
-        for (int y = 0; y < 32; y += 16)
+        for (int y = 0; y < kChunk; y += 16)
           if (y0 + y < cols) tmem_load16(s_at + y0 + y, s + y);
         tmem_wait_load();
-        tmem_pin<32>(s);
+        tmem_pin<kChunk>(s);
         if (masked)
 #pragma unroll
-          for (int y = 0; y < 32; ++y)
+          for (int y = 0; y < kChunk; ++y)
             if (y0 + y < from) s[y] = 0xff800000u;
       };
       auto exponents = [&](int y0) {
 #pragma unroll
-        for (int y = 0; y < 32; y += 4) {
+        for (int y = 0; y < kChunk; y += 4) {
           if (y0 + (y & 16) >= cols) continue;
           const float4 r = *(const float4*)(refs + y0 + y);
           float e0, e1, e2, e3;
@@ -541,12 +555,12 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
       if (!raise) {
         float top = SV_NEG_INF;
 #pragma unroll
-        for (int y0 = 0; y0 < kCols; y0 += 32) {
+        for (int y0 = 0; y0 < kCols; y0 += kChunk) {
           if (y0 >= cols) continue;
           scores(y0);
           exponents(y0);
 #pragma unroll
-          for (int y = 0; y < 32; y += 2)
+          for (int y = 0; y < kChunk; y += 2)
             if (y0 + (y & 16) < cols) top = max3(top, __uint_as_float(s[y]), __uint_as_float(s[y + 1]));
         }
         raise = top > kSlack;
@@ -555,16 +569,16 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
         if (!vote_all(id, ok)) return;
         // maxima of the rows, over the warp's keys and then over the warps
 #pragma unroll 1
-        for (int y0 = 0; y0 < cols; y0 += 32) {
+        for (int y0 = 0; y0 < cols; y0 += kChunk) {
           scores(y0);
           float mine = SV_NEG_INF;
 #pragma unroll
-          for (int y = 0; y < 32; ++y) {
+          for (int y = 0; y < kChunk; ++y) {
             if (y0 + (y & 16) >= cols) continue;
             const float top = redux_max(__uint_as_float(s[y]));
             if (lane == y) mine = top;
           }
-          tops[warp * 64 + y0 + lane] = mine;
+          if (lane < kChunk) tops[warp * 64 + y0 + lane] = mine;
         }
         (void)vote_any(id, false);
         if (x < cols) {
@@ -581,7 +595,7 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
 #pragma unroll
           for (int y = 0; y < kCols; ++y)
             if (y < cols) l[y] *= factors[y];
-          ok = mbar_wait(smem_addr(&c->pv_done[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a));
+          ok = mbar_await(smem_addr(&c->pv_done[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a));
           tc_fence_after();
           if (ok) {
 #pragma unroll 1
@@ -602,20 +616,17 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
           exponents(0);
         }
       }
-      // P of the tile before the last has been read
-      if (ok && g >= 2)
-        ok = mbar_wait(smem_addr(&c->pv_done[buf]), (g / 2 - 1) & 1, &c->abort_word, naps_of(a));
       if (!ok) continue;
       char* p_at = p_row + buf * S::kPBytes;
 #pragma unroll
-      for (int y0 = 0; y0 < kCols; y0 += 32) {
+      for (int y0 = 0; y0 < kCols; y0 += kChunk) {
         if (y0 >= cols) continue;
         if (!kKeep) {
           scores(y0);
           exponents(y0);
         }
 #pragma unroll
-        for (int y = 0; y < 32; y += 8) {
+        for (int y = 0; y < kChunk; y += 8) {
           if (y0 + (y & 16) >= cols) continue;
           uint32_t p[4];
 #pragma unroll
@@ -624,24 +635,24 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
             f2_unpack(f2_add(f2_pack(l[y0 + y + z], l[y0 + y + z + 1]), f2_pack(p0, p1)), l[y0 + y + z], l[y0 + y + z + 1]);
             p[z / 2] = pack2(p0, p1, __half());
           }
-          *(uint4*)(p_at + (((y0 + y) / 8) ^ (place % 8)) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
+          *(uint4*)(p_at + (((y0 + y) / 8) ^ turn) * 16) = make_uint4(p[0], p[1], p[2], p[3]);
         }
       }
       fence_async_shared();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_addr(&c->s_free[buf]));
-        mbar_arrive(smem_addr(&c->p_ready[buf]));
-      }
+      if (lane == 0) mbar_arrive(smem_addr(&c->pv_ready[buf]));
     }
     // ---- the unit's end: sums over the threads, results or a part of them
     if (n > 0)
-      ok = ok && mbar_wait(smem_addr(&c->pv_done[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a));
+      ok = ok && mbar_await(smem_addr(&c->pv_done[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a));
     tc_fence_after();
 #pragma unroll
-    for (int y0 = 0; y0 < kCols; y0 += 32)
-      if (y0 < cols) tops[warp * 64 + y0 + lane] = warp_sums(l + y0);
+    for (int y0 = 0; y0 < kCols; y0 += kChunk)
+      if (y0 < cols) {
+        const float sum = warp_sums<kChunk>(l + y0);
+        if (lane < kChunk) tops[warp * 64 + y0 + lane] = sum;
+      }
     if (!vote_all(id, ok)) return;
     const bool whole = u.j0 == 0 && u.j1 == u.tiles;
     const int cta = blockIdx.x;
@@ -722,7 +733,7 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
 }
 
 template <typename E, int kD, int kRows>
-__global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, 1)
+__global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, Fp4Shape<kD, kRows>::kCtasPerSm)
     sv_fp4_attention_kernel(const __grid_constant__ Fp4Args a, const __grid_constant__ CUtensorMap k_map,
                             const __grid_constant__ CUtensorMap v_map) {
   using S = Fp4Shape<kD, kRows>;
@@ -731,7 +742,7 @@ __global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, 1)
   char* p_ptr = q_ptr + 2 * S::kQBytes;
   char* ring = p_ptr + 2 * S::kPBytes;
   char* value_scales = ring + S::kStages * S::kStageBytes;
-  float* stats = (float*)(value_scales + 2 * S::kValueScales);
+  float* stats = (float*)(value_scales + S::kValueScales);
   Fp4Control* c = (Fp4Control*)((char*)stats + S::kStatBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kSoft = S::kSoftThreads / 32, kKeyWarps = kSoft, kValueWarps = kSoft + 4, kLoader = kSoft + 8;
@@ -746,15 +757,11 @@ __global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&c->q_full[i]), 1);
       mbar_init(smem_addr(&c->q_free[i]), 1 + kSoft);
-      mbar_init(smem_addr(&c->k_ready[i]), 4);
-      mbar_init(smem_addr(&c->k_free[i]), 1);
-      mbar_init(smem_addr(&c->v_ready[i]), 4);
-      mbar_init(smem_addr(&c->v_free[i]), 1);
       mbar_init(smem_addr(&c->s_full[i]), 1);
-      mbar_init(smem_addr(&c->s_free[i]), kSoft);
-      mbar_init(smem_addr(&c->p_ready[i]), kSoft);
+      mbar_init(smem_addr(&c->pv_ready[i]), kSoft + 4);
       mbar_init(smem_addr(&c->pv_done[i]), 1);
     }
+    mbar_init(smem_addr(&c->k_ready), 4);
     mbar_init(smem_addr(&c->drain), 1);
     mbar_init(smem_addr(&c->met), kSoft);
     mbar_init_fence();
@@ -768,20 +775,23 @@ __global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, 1)
   const uint32_t tmem = c->tmem;
   if (range.w0 < range.w1) {
     const AttnWalk<S> u(a, c->start, range.w1 - range.w0);
-    // Many rows: five warpgroups launched with 96 registers a thread, and
-    // 2 x 152 + 2 x 64 + 48 = 5 x 96.
+    // Registers: 80 + 2 x 64 + 48 = 4 x 64 of two CTAs per SM, 2 x 152 + 2 x 64 + 48 = 5 x 96
+    // of five warpgroups; four of one CTA have 128 a thread.
+    constexpr bool kFew = S::kCtasPerSm > 1, kMany = S::kGroups > 1;
     if (warp < kKeyWarps) {
-      if (S::kGroups > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+      if (kMany) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+      if (kFew) asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
       fp4_softmax<E, kD, S>(a, u, c, tmem, p_ptr, stats, range.quota, range.w1);
     } else if (warp < kLoader) {
-      if (S::kGroups > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      if (kMany) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
       if (warp < kValueWarps) fp4_keys<kD, S>(a, u, c, ring, tmem);
       else fp4_values<kD, S>(a, u, c, ring, tmem, value_scales);
     } else {
-      if (S::kGroups > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-      if (warp == kLoader) fp4_load<kD, S>(a, u, c, ring, &k_map, &v_map);
+      if (kMany || kFew) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      if (warp == kLoader) fp4_load<kD, S>(a, u, c, ring, &k_map, a.k_scales, 0);
       else if (warp == kLoader + 1) fp4_multiply<kD, S>(a, u, c, smem_addr(q_ptr), smem_addr(p_ptr), tmem);
-      else if (warp == kLoader + 2) fp4_queries<E, kD, S>(a, u, c, q_ptr);
+      else if (warp == kLoader + 2) fp4_load<kD, S>(a, u, c, ring, &v_map, a.v_scales, 1);
+      else fp4_queries<E, kD, S>(a, u, c, q_ptr);
     }
   }
   attn_finish<S, kD>(a, c, range.spoilt);

@@ -63,6 +63,30 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   return ok;
 }
 
+// The same, for warps that wait often: one try and a vote come first (87 clocks
+// when the phase is over; mbar_wait 139), then polls that sleep up to kLongNap
+// nanoseconds, so that waiting warps take few of the SM's instructions.
+constexpr uint32_t kLongNap = 20000;
+__device__ __forceinline__ bool mbar_await(uint32_t bar, uint32_t parity, volatile int* abort_word,
+                                           int naps) {
+  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  uint32_t ok = 0;
+#pragma unroll 1
+  for (int i = 0; i < naps; i += 8) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kLongNap)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (__any_sync(0xffffffffu, *abort_word)) break;
+  }
+  *abort_word = 1;
+  return false;
+}
+
 // ----------------------------------------------------------------------- TMA
 // Loads of one box to shared memory; `bar` counts its bytes.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
@@ -192,10 +216,13 @@ __device__ __forceinline__ void tmem_wait_store() {
 // of them an atom of 1 KB.  Along the swizzled rows (operands whose
 // contraction runs inside a row) `group` is the distance of 8-row groups;
 // for operands whose contraction runs across the rows, `block` is the
-// distance of 128-byte column blocks as well.  Distances in bytes.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t block, uint32_t group) {
+// distance of 128-byte column blocks as well.  Distances in bytes.  Rows of 64 or
+// 32 bytes (atoms of 512 or 256) are swizzled within themselves.
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t block, uint32_t group,
+                                              uint32_t row_bytes = 128) {
   return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(block >> 4) << 16 |
-         (uint64_t)(group >> 4) << 32 | 1ull << 46 | 2ull << 61;
+         (uint64_t)(group >> 4) << 32 | 1ull << 46 |
+         (row_bytes == 128 ? 2ull : row_bytes == 64 ? 4ull : 6ull) << 61;
 }
 
 // Instruction descriptor: 16-bit operands (`bf16`, else f16), float32 sums,
@@ -228,6 +255,33 @@ __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uin
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add), "r"(issue)
       : "memory");
+}
+
+// One lane of a converged warp, by elect.sync: in a branch on it the compiler knows
+// that one lane is active and forms operands once.  A product of 128 x 16 x 16
+// then issues in 9 clocks, 128 x 128 x 16 in 64; under a predicate of the lane's
+// number every product takes 58 to 78.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, e;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+// For the elected lane: d (+)= a b with a in tensor memory, and a commit.
+__device__ __forceinline__ void mma_tmem_one(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_one(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
 }
 
 }  // namespace sv
