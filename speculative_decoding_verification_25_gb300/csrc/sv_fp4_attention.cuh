@@ -277,32 +277,29 @@ __device__ __forceinline__ void fp4_keys(const Fp4Args& a, AttnWalk<S> u, Fp4Con
       const int stage = 2 * g % S::kStages, lap = 2 * g / S::kStages;
       if (!mbar_await(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a))) return;
       const char* tile = ring + stage * S::kStageBytes;
-      uint4 w[kD / 32];
-      uint32_t scales[kD / 64];
-#pragma unroll
-      for (int p = 0; p < kD / 32; ++p) w[p] = *(const uint4*)(tile + fp4_piece<kD>(key, p));
-#pragma unroll
-      for (int p = 0; p < kD / 64; ++p)
-        scales[p] = *(const uint32_t*)(tile + S::kCodeBytes + key * (kD / 16) + p * 4);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&c->empty[stage]));
       // the scores of the tile before are done, and its keys free
       if (g > 0 && !mbar_await(smem_addr(&c->s_full[(g - 1) % 2]), ((g - 1) / 2) & 1, &c->abort_word, naps_of(a)))
         return;
       tc_fence_after();
-#pragma unroll
+      uint4 w = *(const uint4*)(tile + fp4_piece<kD>(key, 0));
+      // rolled up: a role's code is run once a tile by one warp of a scheduler, and
+      // long code waits for its instructions
+#pragma unroll 1
       for (int p = 0; p < kD / 32; ++p) {
-        const uint32_t pair = fp4_scales(scales[p / 2] >> (p % 2 * 16));
+        const uint32_t pair = fp4_scales(*(const uint16_t*)(tile + S::kCodeBytes + key * (kD / 16) + p * 2));
         const uint32_t s0 = __byte_perm(pair, 0, 0x1010), s1 = __byte_perm(pair, 0, 0x3232);
         uint32_t r[16];
-        fp4_unpack(w[p].x, r);
-        fp4_unpack(w[p].y, r + 4);
-        fp4_unpack(w[p].z, r + 8);
-        fp4_unpack(w[p].w, r + 12);
+        fp4_unpack(w.x, r);
+        fp4_unpack(w.y, r + 4);
+        fp4_unpack(w.z, r + 8);
+        fp4_unpack(w.w, r + 12);
+        if (p + 1 < kD / 32) w = *(const uint4*)(tile + fp4_piece<kD>(key, p + 1));
 #pragma unroll
         for (int y = 0; y < 16; ++y) r[y] = mul_f16x2(r[y], y < 8 ? s0 : s1);
         tmem_store16(to + p * 16, r);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&c->empty[stage]));
       tmem_wait_store();
       hand_over(&c->k_ready);
     }
@@ -352,7 +349,7 @@ __device__ __forceinline__ void fp4_values(const Fp4Args& a, AttnWalk<S> u, Fp4C
       tc_fence_after();
       if (active) {
         __syncwarp();
-#pragma unroll
+#pragma unroll 1
         for (int block = 0; block < 4; ++block) {   // of 32 keys
           const uint32_t from = smem_addr(tile) + fp4_piece<kD>(block * 32 + lane, warp);
           uint32_t m[4];   // bytes l / 4 and l / 4 + 8 of the first 16 keys, and of the others
