@@ -3,11 +3,13 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
 #include <mutex>
 
 #include "spec_verify.h"
 #include "sv_fp4_attention.cuh"
+#include "sv_fp4_wide.cuh"
 #include "sv_paged_host.h"
 
 namespace {
@@ -32,7 +34,7 @@ Fp4Device g_fp4[kMaxDevices];
 
 struct Variant {
   const void* fn;
-  int threads, smem_bytes, ctas_per_sm, rows;
+  int threads, smem_bytes, ctas_per_sm, rows;   // rows of a unit, or of a query tile of the wide form
 };
 template <typename E, int kD, int kRows>
 Variant variant() {
@@ -40,8 +42,17 @@ Variant variant() {
   return {(const void*)sv::sv_fp4_attention_kernel<E, kD, kRows>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, kRows};
 }
 template <typename E, int kD>
+Variant wide_variant() {
+  using S = sv::Fp4WideShape<kD>;
+  return {(const void*)sv::sv_fp4_wide_attention_kernel<E, kD>, S::kThreads, S::kSmemBytes, 1, 128};
+}
+constexpr int kWide = 1 << 30;   // rows of the wide form
+template <typename E, int kD>
 Variant variant_of(int rows) {
-  return rows <= 16 ? variant<E, kD, 16>() : rows <= 32 ? variant<E, kD, 32>() : variant<E, kD, 128>();
+  return rows <= 16    ? variant<E, kD, 16>()
+         : rows <= 32  ? variant<E, kD, 32>()
+         : rows < kWide ? variant<E, kD, 128>()
+                        : wide_variant<E, kD>();
 }
 // The variant whose units have at least `rows` rows, or the largest.
 Variant variant_of(int dtype, int D, int rows) {
@@ -57,8 +68,9 @@ Fp4Device* fp4_device() {
   Fp4Device& d = g_fp4[dev];
   std::call_once(d.once, [&d, dev]() {
     d.error = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev);
-    for (int i = 0; i < 12 && d.error == cudaSuccess; ++i) {
-      const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, i < 4 ? 16 : i < 8 ? 32 : 128);
+    const int rows[] = {16, 32, 128, kWide};
+    for (int i = 0; i < 16 && d.error == cudaSuccess; ++i) {
+      const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, rows[i / 4]);
       d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
     }
     if (d.error == cudaSuccess) d.error = sv::find_encoder(&d.encode);
@@ -117,44 +129,64 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   const int G = Hq / Hk;
   // The host knows the mean of a request's rows (the G heads of its tokens on one key head) alone.
   const long long mean = ((long long)T * G + (B > 0 ? B : 1) - 1) / (B > 0 ? B : 1);
-  const Variant v = variant_of(dtype, D, mean > G ? (mean < 128 ? (int)mean : 128) : G);
+  const char* env = getenv("SV_FORM");
+  const bool wide = env ? atoi(env) : mean > 128;
+  const Variant v = variant_of(dtype, D, wide ? kWide : mean > G ? (mean < 128 ? (int)mean : 128) : G);
   int ctas = dev->sm_count * v.ctas_per_sm;
   if (ctas > sv::kAttnMaxCtas) ctas = sv::kAttnMaxCtas;
 
+  auto fill = [&](sv::AttnArgs& a) {
+    a.block_table = block_table;
+    a.cu_new = cu_new;
+    a.kv_len = kv_len;
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hk = Hk;
+    a.G = G;
+    a.page_shift = shift;
+    a.max_pages = max_pages;
+    a.n_pages = n_pages;
+    a.tile_tokens = v.rows / G;
+    a.scale_log2 = (float)((double)scale * sv::kLog2e * k_gain);
+    a.out = (char*)out;
+    a.lse = lse;
+    a.tickets = (int*)workspace;
+    a.status = (unsigned*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES) - 1;
+    a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
+    a.flags = flags;
+    a.naps = g_naps;
+    a.v_gain = v_gain;
+  };
+  const dim3 grid((unsigned)ctas), block((unsigned)v.threads);
+  if (wide) {
+    sv::Fp4WideArgs a;
+    fill(a);
+    a.k_codes = (const char*)k_codes;
+    a.k_scales = (const uint8_t*)k_scales;
+    a.v_codes = (const char*)v_codes;
+    a.v_scales = (const uint8_t*)v_scales;
+    CUtensorMap q_map;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+    const cuuint64_t pitches[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)a.tile_tokens};
+    if (!sv::encode_map(dev->encode, &q_map, dtype, q, 3, dims, pitches, box)) return SV_ERR_CUDA;
+    void* args[] = {&a, &q_map};
+    return done(launch_early(v.fn, grid, block, args, (cudaStream_t)stream, (size_t)v.smem_bytes));
+  }
   sv::Fp4Args a;
-  a.block_table = block_table;
-  a.cu_new = cu_new;
-  a.kv_len = kv_len;
-  a.B = B;
-  a.T = T;
-  a.Hq = Hq;
-  a.Hk = Hk;
-  a.G = G;
-  a.page_shift = shift;
-  a.max_pages = max_pages;
-  a.n_pages = n_pages;
-  a.tile_tokens = v.rows / G;
-  a.scale_log2 = (float)((double)scale * sv::kLog2e * k_gain);
-  a.out = (char*)out;
-  a.lse = lse;
-  a.tickets = (int*)workspace;
-  a.status = (unsigned*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES) - 1;
-  a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
-  a.flags = flags;
-  a.naps = g_naps;
+  fill(a);
   a.q = (const char*)q;
   a.q_pitch = (long long)q_stride * 2;
   a.k_scales = (const uint8_t*)k_scales;
   a.v_scales = (const uint8_t*)v_scales;
-  a.v_gain = v_gain;
   const long long rows = (long long)n_pages * Hk * page_size;
   const int box = page_size < 128 ? page_size : 128;
   CUtensorMap k_map, v_map;
   if (!encode_codes(*dev, &k_map, k_codes, D, rows, box) || !encode_codes(*dev, &v_map, v_codes, D, rows, box))
     return SV_ERR_CUDA;
   void* args[] = {&a, &k_map, &v_map};
-  return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args,
-                           (cudaStream_t)stream, (size_t)v.smem_bytes));
+  return done(launch_early(v.fn, grid, block, args, (cudaStream_t)stream, (size_t)v.smem_bytes));
 }
 
 #ifdef SV_CHECKED

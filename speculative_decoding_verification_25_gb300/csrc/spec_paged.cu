@@ -17,6 +17,7 @@ namespace {
 
 using sv::aligned_to;
 using sv::done;
+using sv::encode_map;
 using sv::EncodeTiled;
 using sv::k2_31;
 using sv::kMaxDevices;
@@ -85,17 +86,6 @@ int g_naps = sv::kNaps;   // tests shorten it
 #else
 constexpr int g_naps = sv::kNaps;
 #endif
-
-// A map of 16-bit elements for boxes of 64 columns (128 bytes, swizzled) by
-// box1 (by box2): dims and boxes innermost first, pitches in bytes.
-bool encode_map(const PagedDevice& d, CUtensorMap* map, int dtype, const void* base, int rank,
-                const cuuint64_t* dims, const cuuint64_t* pitches, const cuuint32_t* box) {
-  const cuuint32_t ones[3] = {1, 1, 1};
-  return d.encode(map, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                  (cuuint32_t)rank, const_cast<void*>(base), dims, pitches, box, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 }  // namespace
 
@@ -286,9 +276,9 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)n_pages * Hk * page_size};
   const cuuint64_t pitches[1] = {(cuuint64_t)D * 2};
   const cuuint32_t box[2] = {64, (cuuint32_t)(page_size < v.keys ? page_size : v.keys)};
-  if (!encode_map(*dev, &q_map, dtype, q, 3, q_dims, q_pitches, q_box) ||
-      !encode_map(*dev, &k_map, dtype, k_cache, 2, dims, pitches, box) ||
-      !encode_map(*dev, &v_map, dtype, v_cache, 2, dims, pitches, box))
+  if (!encode_map(dev->encode, &q_map, dtype, q, 3, q_dims, q_pitches, q_box) ||
+      !encode_map(dev->encode, &k_map, dtype, k_cache, 2, dims, pitches, box) ||
+      !encode_map(dev->encode, &v_map, dtype, v_cache, 2, dims, pitches, box))
     return SV_ERR_CUDA;
   void* args[] = {&a, &q_map, &k_map, &v_map};
   return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args,

@@ -35,7 +35,6 @@ struct Fp4Args : AttnArgs {
   long long q_pitch;   // bytes between tokens
   const uint8_t* k_scales;
   const uint8_t* v_scales;
-  float v_gain;
 };
 
 template <int kD, int kRowsMost>

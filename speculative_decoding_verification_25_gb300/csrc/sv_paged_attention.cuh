@@ -84,6 +84,7 @@ struct AttnArgs {
   float* partial;               // [CTA][2][rows][D], then [CTA][2][rows][2]
   unsigned* flags;
   int naps;                     // checked build: polls after which a wait is given up
+  float v_gain = 1.f;           // 4-bit cache: a factor of the results
 };
 // A constant in the plain build (an argument there: verify 98.3 against 97.9 us,
 // ragged chunks 54.7 against 54.2).
@@ -91,6 +92,7 @@ __device__ __forceinline__ int naps_of(const AttnArgs& a) { return kChecked ? a.
 
 template <int kD, bool kWide>
 struct AttnShape {
+  static constexpr bool kFp4 = false;                // the 4-bit cache's shape has it true
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kKeys = kWide ? 128 : 64;
   static constexpr int kBufs = kWide ? 1 : 2;        // S buffers per query tile
@@ -408,7 +410,8 @@ __device__ __forceinline__ void attn_load(const AttnArgs& a, AttnWalk<S> u, Attn
 // A count and not a barrier: a tile without products may be units ahead, and a
 // wait for a phase sees its parity alone.  A turn sleeps about a sixteenth of
 // what a poll of a barrier does.
-__device__ __forceinline__ bool wait_past(AttnControl* c, int units, int naps) {
+template <typename Control>
+__device__ __forceinline__ bool wait_past(Control* c, int units, int naps) {
   bool ok = c->past >= units;
 #pragma unroll 1
   for (int i = 0; !ok && i < 16 * naps && !*(volatile int*)&c->abort_word; ++i) {
@@ -429,8 +432,8 @@ __device__ __forceinline__ bool wait_past(AttnControl* c, int units, int naps) {
 // keys follows O += P V, whose P lies where S goes.
 // Columns of tensor memory: kBufs S buffers per query tile, then one O per
 // query tile.
-template <typename E, int kD, typename S>
-__device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
+template <typename E, int kD, typename S, typename Control>
+__device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, Control* c,
                                               uint32_t q_smem, uint32_t ring, char* ring_ptr,
                                               uint32_t tmem, int t) {
   constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
@@ -701,8 +704,10 @@ __device__ __forceinline__ void hand_over(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_addr(bar));
 }
 
-template <typename E, int kD, typename S>
-__device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, AttnControl* c,
+// `E` is the operands' type, `Out` the result's.  Over a 4-bit cache a query tile
+// carries a power of two.
+template <typename E, typename Out, int kD, typename S, typename Control>
+__device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, Control* c,
                                              uint32_t tmem, char* staging, long long quota,
                                              long long w1) {
   const int warp = threadIdx.x >> 5, t = warp / 4;
@@ -712,7 +717,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
   const uint32_t o_col = tmem + lanes + S::kTiles * S::kBufs * S::kKeys + t * kD;
   char* stage = staging + warp * S::kStagingBytes;
   int done = 0;                                    // tiles of S taken before this unit
-  int meetings = 0, rounds = 0;
+  int meetings = 0, rounds = 0, units = 0;
+  float scale = a.scale_log2;
   bool ok = true;
 #pragma unroll 1
   for (bool first = true; ok && u.next(first); first = false) {
@@ -735,6 +741,8 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
                            naps_of(a))))
         break;
       tc_fence_after();
+      if constexpr (S::kFp4)
+        if (i == 0) scale = ldexpf(a.scale_log2, c->q_exponent[units % 2][t]);
       // With two S buffers the scores do not tell that the last O += P V is
       // done; the wait keeps at most one of them open, as a wait that sees a
       // phase's parity alone needs.
@@ -759,7 +767,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
             if (x >= left) bits[x] = 0xff800000u;
         }
         // The reference follows the maximum where that rises by more than kSlack.
-        const float high = row_max<S::kKeys>(bits) * a.scale_log2;
+        const float high = row_max<S::kKeys>(bits) * scale;
         const bool raise = mine && (i == 0 ? high > m : high > m + kSlack);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (m == SV_NEG_INF ? 0.f : ex2_approx(m - high)) : 1.f;
@@ -785,7 +793,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           }
         }
         const float ref = m == SV_NEG_INF ? 0.f : m;
-        const unsigned long long scale2 = f2_pack(a.scale_log2, a.scale_log2);
+        const unsigned long long scale2 = f2_pack(scale, scale);
         const unsigned long long ref2 = f2_pack(-ref, -ref);
 #pragma unroll
         for (int x = 0; x < S::kKeys; x += 32) {
@@ -823,6 +831,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     if (!ok) break;
     u.unpark((const int4*)stage);
     done += n;
+    units += S::kFp4 && u.most() > 0;
     // one S buffer: one arrival per unit, else one per tile
     if (n > 0)
       ok = mbar_wait(smem_addr(&c->pv_done[t]), (S::kBufs > 1 ? done - 1 : rounds++) & 1,
@@ -841,7 +850,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     const size_t slots = (size_t)gridDim.x * 2;
     const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
     if (any) {
-      const float inv = row_inverse(l);
+      const float inv = S::kFp4 ? row_inverse(l) * a.v_gain : row_inverse(l);
       // rows of `out` from the unit's first token and head, or rows of the slot
       const long long unit = (long long)(u.units.row.begin + u.first(0)) * a.Hq + u.h * a.G;
       const int to = !mine ? -1 : whole ? (token - u.first(0)) * a.Hq + r_head : t * 128 + r;
@@ -856,12 +865,15 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
           tmem_wait_load();
           tmem_pin<32>(bits);
         }
+        if (S::kFp4 && !whole)
+#pragma unroll
+          for (int y = 0; y < 32; ++y) bits[y] = __float_as_uint(__uint_as_float(bits[y]) * a.v_gain);
         if (whole) {   // 64 columns make a segment
           uint32_t p[16];
 #pragma unroll
           for (int y = 0; y < 16; ++y)
             p[y] = pack2(__uint_as_float(bits[2 * y]) * inv, __uint_as_float(bits[2 * y + 1]) * inv,
-                         E());
+                         Out());
 #pragma unroll
           for (int y = 0; y < 4; ++y)
             stage_piece(stage, x / 8 % 8 + y, p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
@@ -901,9 +913,9 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, A
     if (c->last) {
       const int parts = c_last - c_first + 1;
       if (u.rows() * (kD / 4) <= S::kSoftThreads)
-        attn_join<E, kD, S, kD / 4, 8>(a, u, c_first, parts, begins_late);
+        attn_join<Out, kD, S, kD / 4, 8>(a, u, c_first, parts, begins_late);
       else
-        attn_join<E, kD, S, 8, 2>(a, u, c_first, parts, begins_late);
+        attn_join<Out, kD, S, 8, 2>(a, u, c_first, parts, begins_late);
     }
   }
 }
@@ -1099,7 +1111,7 @@ __global__ void __launch_bounds__(AttnShape<kD, kWide>::kThreads, AttnShape<kD, 
                      !kWide || warp != kLoader);
     } else {
       if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      attn_softmax<E, kD, S>(a, u, c, tmem, staging, quota, w1);
+      attn_softmax<E, E, kD, S>(a, u, c, tmem, staging, quota, w1);
     }
   }
   attn_finish<S, kD>(a, c, range.spoilt);

@@ -38,4 +38,15 @@ inline cudaError_t find_encoder(EncodeTiled* encode) {
   return e;
 }
 
+// A map of 16-bit elements for boxes of 64 columns (128 bytes, swizzled) by
+// box1 (by box2): dims and boxes innermost first, pitches in bytes.
+inline bool encode_map(EncodeTiled encode, CUtensorMap* map, int dtype, const void* base, int rank,
+                const cuuint64_t* dims, const cuuint64_t* pitches, const cuuint32_t* box) {
+  const cuuint32_t ones[3] = {1, 1, 1};
+  return encode(map, dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  (cuuint32_t)rank, const_cast<void*>(base), dims, pitches, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace sv
