@@ -9,7 +9,7 @@
 
 #include "spec_verify.h"
 #include "sv_fp4_attention.cuh"
-#include "sv_fp4_wide.cuh"
+#include "sv_fp4_rows.cuh"
 #include "sv_paged_host.h"
 
 namespace {
@@ -41,24 +41,22 @@ Variant variant() {
   using S = sv::Fp4Shape<kD, kRows>;
   return {(const void*)sv::sv_fp4_attention_kernel<E, kD, kRows>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, kRows};
 }
-template <typename E, int kD>
-Variant wide_variant() {
-  using S = sv::Fp4WideShape<kD>;
-  return {(const void*)sv::sv_fp4_wide_attention_kernel<E, kD>, S::kThreads, S::kSmemBytes, 1, 128};
+template <typename E, int kD, bool kWide>
+Variant rows_variant() {
+  using S = sv::Fp4RowsShape<kD, kWide>;
+  return {(const void*)sv::sv_fp4_rows_attention_kernel<E, kD, kWide>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, 128};
 }
-constexpr int kWide = 1 << 30;   // rows of the wide form
+enum Form { kFew, kNarrow, kWide, kForms };
 template <typename E, int kD>
-Variant variant_of(int rows) {
-  return rows <= 16    ? variant<E, kD, 16>()
-         : rows <= 32  ? variant<E, kD, 32>()
-         : rows < kWide ? variant<E, kD, 128>()
-                        : wide_variant<E, kD>();
+Variant variant_of(Form form) {
+  return form == kFew      ? variant<E, kD, 16>()
+         : form == kNarrow ? rows_variant<E, kD, false>()
+                           : rows_variant<E, kD, true>();
 }
-// The variant whose units have at least `rows` rows, or the largest.
-Variant variant_of(int dtype, int D, int rows) {
+Variant variant_of(int dtype, int D, Form form) {
   if (dtype == SV_BF16)
-    return D == 128 ? variant_of<__nv_bfloat16, 128>(rows) : variant_of<__nv_bfloat16, 64>(rows);
-  return D == 128 ? variant_of<__half, 128>(rows) : variant_of<__half, 64>(rows);
+    return D == 128 ? variant_of<__nv_bfloat16, 128>(form) : variant_of<__nv_bfloat16, 64>(form);
+  return D == 128 ? variant_of<__half, 128>(form) : variant_of<__half, 64>(form);
 }
 
 // SM count, shared memory limits and the tensor map encoder; once per device.
@@ -68,9 +66,8 @@ Fp4Device* fp4_device() {
   Fp4Device& d = g_fp4[dev];
   std::call_once(d.once, [&d, dev]() {
     d.error = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev);
-    const int rows[] = {16, 32, 128, kWide};
-    for (int i = 0; i < 16 && d.error == cudaSuccess; ++i) {
-      const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, rows[i / 4]);
+    for (int i = 0; i < 4 * kForms && d.error == cudaSuccess; ++i) {
+      const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, (Form)(i / 4));
       d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
     }
     if (d.error == cudaSuccess) d.error = sv::find_encoder(&d.encode);
@@ -87,6 +84,7 @@ bool encode_codes(const Fp4Device& d, CUtensorMap* map, const void* base, int D,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
 #ifdef SV_CHECKED
 int g_naps = sv::kNaps;   // tests shorten it
 #else
@@ -128,65 +126,58 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   if (!dev) return SV_ERR_CUDA;
   const int G = Hq / Hk;
   // The host knows the mean of a request's rows (the G heads of its tokens on one key head) alone.
-  const long long mean = ((long long)T * G + (B > 0 ? B : 1) - 1) / (B > 0 ? B : 1);
+  const long long rows_of_all = (long long)T * G, requests = B > 0 ? B : 1;
   const char* env = getenv("SV_FORM");
-  const bool wide = env ? atoi(env) : mean > 128;
-  const Variant v = variant_of(dtype, D, wide ? kWide : mean > G ? (mean < 128 ? (int)mean : 128) : G);
+  const Form form = env ? (Form)atoi(env)
+                    : rows_of_all > 128 * requests ? kWide
+                    : G > 16 || rows_of_all > 16 * requests ? kNarrow : kFew;
+  const Variant v = variant_of(dtype, D, form);
   int ctas = dev->sm_count * v.ctas_per_sm;
   if (ctas > sv::kAttnMaxCtas) ctas = sv::kAttnMaxCtas;
 
-  auto fill = [&](sv::AttnArgs& a) {
-    a.block_table = block_table;
-    a.cu_new = cu_new;
-    a.kv_len = kv_len;
-    a.B = B;
-    a.T = T;
-    a.Hq = Hq;
-    a.Hk = Hk;
-    a.G = G;
-    a.page_shift = shift;
-    a.max_pages = max_pages;
-    a.n_pages = n_pages;
-    a.tile_tokens = v.rows / G;
-    a.scale_log2 = (float)((double)scale * sv::kLog2e * k_gain);
-    a.out = (char*)out;
-    a.lse = lse;
-    a.tickets = (int*)workspace;
-    a.status = (unsigned*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES) - 1;
-    a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
-    a.flags = flags;
-    a.naps = g_naps;
-    a.v_gain = v_gain;
-  };
-  const dim3 grid((unsigned)ctas), block((unsigned)v.threads);
-  if (wide) {
-    sv::Fp4WideArgs a;
-    fill(a);
-    a.k_codes = (const char*)k_codes;
-    a.k_scales = (const uint8_t*)k_scales;
-    a.v_codes = (const char*)v_codes;
-    a.v_scales = (const uint8_t*)v_scales;
-    CUtensorMap q_map;
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
-    const cuuint64_t pitches[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)a.tile_tokens};
-    if (!sv::encode_map(dev->encode, &q_map, dtype, q, 3, dims, pitches, box)) return SV_ERR_CUDA;
-    void* args[] = {&a, &q_map};
-    return done(launch_early(v.fn, grid, block, args, (cudaStream_t)stream, (size_t)v.smem_bytes));
-  }
   sv::Fp4Args a;
-  fill(a);
+  a.block_table = block_table;
+  a.cu_new = cu_new;
+  a.kv_len = kv_len;
+  a.B = B;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.G = G;
+  a.page_shift = shift;
+  a.max_pages = max_pages;
+  a.n_pages = n_pages;
+  a.tile_tokens = v.rows / G;
+  a.scale_log2 = (float)((double)scale * sv::kLog2e * k_gain);
+  a.out = (char*)out;
+  a.lse = lse;
+  a.tickets = (int*)workspace;
+  a.status = (unsigned*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES) - 1;
+  a.partial = (float*)((char*)workspace + SV_ATTENTION_COUNTER_BYTES);
+  a.flags = flags;
+  a.naps = g_naps;
+  a.v_gain = v_gain;
   a.q = (const char*)q;
   a.q_pitch = (long long)q_stride * 2;
-  a.k_scales = (const uint8_t*)k_scales;
-  a.v_scales = (const uint8_t*)v_scales;
+  a.k_scales = (const char*)k_scales;
+  a.v_scales = (const char*)v_scales;
   const long long rows = (long long)n_pages * Hk * page_size;
   const int box = page_size < 128 ? page_size : 128;
-  CUtensorMap k_map, v_map;
+  CUtensorMap q_map, k_map, v_map;
   if (!encode_codes(*dev, &k_map, k_codes, D, rows, box) || !encode_codes(*dev, &v_map, v_codes, D, rows, box))
     return SV_ERR_CUDA;
-  void* args[] = {&a, &k_map, &v_map};
-  return done(launch_early(v.fn, grid, block, args, (cudaStream_t)stream, (size_t)v.smem_bytes));
+  if (form == kFew) {
+    void* args[] = {&a, &k_map, &v_map};
+    return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args, (cudaStream_t)stream,
+                             (size_t)v.smem_bytes));
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)T};
+  const cuuint64_t pitches[2] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2};
+  const cuuint32_t q_box[3] = {64, (cuuint32_t)G, (cuuint32_t)a.tile_tokens};
+  if (!sv::encode_map(dev->encode, &q_map, dtype, q, 3, dims, pitches, q_box)) return SV_ERR_CUDA;
+  void* args[] = {&a, &q_map, &k_map, &v_map};
+  return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args, (cudaStream_t)stream,
+                           (size_t)v.smem_bytes));
 }
 
 #ifdef SV_CHECKED

@@ -25,17 +25,9 @@
 // Work is cut into ranges and joined as in sv_paged_attention.cuh.
 #pragma once
 
-#include "sv_fp4.cuh"
-#include "sv_paged_attention.cuh"
+#include "sv_fp4_load.cuh"
 
 namespace sv {
-
-struct Fp4Args : AttnArgs {
-  const char* q;
-  long long q_pitch;   // bytes between tokens
-  const uint8_t* k_scales;
-  const uint8_t* v_scales;
-};
 
 template <int kD, int kRowsMost>
 struct Fp4Shape {
@@ -51,8 +43,7 @@ struct Fp4Shape {
   static constexpr int kQBytes = kRows * kD * 2;           // two of them
   static constexpr int kPRow = kRows < 64 ? kRows * 2 : 128;   // bytes of a row of P^T, in blocks of 64 rows of the unit
   static constexpr int kPBytes = 128 * kPRow * ((kRows + 63) / 64);   // two of them
-  static constexpr int kCodeBytes = 128 * kD / 2, kScaleBytes = 128 * kD / 16;
-  static constexpr int kStageBytes = kCodeBytes + kScaleBytes;
+  static constexpr int kStageBytes = Fp4Tile<kD>::kBytes;
   static constexpr int kCtasPerSm = kRows > 16 ? 1 : 2;
   static constexpr int kTmemCols = 512 / kCtasPerSm;
   static constexpr int kValueScales = 128 * (kD / 16) * 2; // float16
@@ -60,8 +51,8 @@ struct Fp4Shape {
   static constexpr int kStatBytes = kGroups * 64 * 4 * (4 + 3);   // of four warps, and three of a row
   static constexpr int kFixedBytes = 2 * (kQBytes + kPBytes) + kValueScales + kControlBytes + kStatBytes;
   static constexpr int kMostStages = (228 * 1024 / kCtasPerSm - 1024 - kFixedBytes) / kStageBytes;
-  static constexpr int kStages = kMostStages >= 16 ? 16 : kMostStages >= 8 ? 8 : 4;   // a power of two
-  static constexpr int kSmemBytes = kFixedBytes + kStages * kStageBytes;
+  static constexpr int kPackedStages = kMostStages >= 16 ? 16 : kMostStages >= 8 ? 8 : 4;   // a power of two
+  static constexpr int kSmemBytes = kFixedBytes + kPackedStages * kStageBytes;
   // columns of tensor memory
   static constexpr int kS = 0, kO = 2 * kRows, kK = 3 * kRows, kV = kK + 64;
   static_assert(kV + 64 <= kTmemCols, "fits");
@@ -99,82 +90,6 @@ __device__ __forceinline__ float redux_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
   return r;
-}
-
-// ------------------------------------------------------------------- loader
-// One warp for keys and one for values: tiles as they are packed, which
-// alternate in the ring.  Lanes 0 to 15 bring a page's codes each, lanes 16 to 31 its
-// scales, which lie in a row (a tiled copy wants 128 bytes).  Rows of pages past the
-// request's length stay as they are; a page outside the cache has scales of zero.
-// A copy's issue takes about 50 clocks: pages of 16 make 16 of a tile.
-template <int kD, typename S>
-__device__ __forceinline__ void fp4_load(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, char* ring,
-                                         const CUtensorMap* map, const uint8_t* scales, int values) {
-  constexpr int kAhead = 4;   // tiles whose pages are looked up ahead
-  const int lane = threadIdx.x & 31;
-  const int page = 1 << a.page_shift, box = min(page, S::kKeys), boxes = S::kKeys / box;
-  const int mine = lane % 16, none = (a.n_pages * a.Hk) << a.page_shift;   // one past the cache's rows
-  int it = values;
-  bool ok = true, bad = false;
-
-  // First row, in the cache, of the lane's box of key tile j; -1 if it has none.
-  auto box_row = [&](int j) -> int {
-    const int key = j * S::kKeys + mine * box;
-    if (mine >= boxes || key >= u.units.row.L) return -1;
-    const int pg = key >> a.page_shift;
-    if (!in_array(a.flags, u.b, a.B) || !in_array(a.flags, pg, a.max_pages)) return -1;
-    const int id = a.block_table[(long long)u.b * a.max_pages + pg];
-    if (id >= 0 && id < a.n_pages) return ((id * a.Hk + u.h) << a.page_shift) + (key & (page - 1));
-    bad = true;
-    return none;
-  };
-  auto bring = [&](int y) -> bool {
-    const int stage = it % S::kStages, lap = it / S::kStages;
-    if (lap > 0 &&
-        !mbar_await(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, naps_of(a)))
-      return false;
-    const uint32_t bar = smem_addr(&c->full[stage]);
-    char* to = ring + stage * S::kStageBytes;
-    char* scale_to = to + S::kCodeBytes + mine * box * (kD / 16);
-    const unsigned code_lanes = __ballot_sync(0xffffffffu, y >= 0 && lane < 16);
-    const unsigned scale_lanes = __ballot_sync(0xffffffffu, y >= 0 && y < none && lane >= 16);
-    if (y == none && lane >= 16) {
-      for (int x = 0; x < box * (kD / 16); x += 4) *(uint32_t*)(scale_to + x) = 0;
-      fence_async_shared();   // before the copy of the slot's next lap
-    }
-    __syncwarp();
-    if (lane == 0)
-      mbar_arrive_expect(bar, __popc(code_lanes) * box * (kD / 2) + __popc(scale_lanes) * box * (kD / 16));
-    __syncwarp();
-    if (y >= 0 && lane < 16) tma_load_2d(smem_addr(to + mine * box * (kD / 2)), map, 0, y, bar);
-    if (y >= 0 && y < none && lane >= 16)
-      bulk_load(smem_addr(scale_to), scales + (long long)y * (kD / 16), box * (kD / 16), bar);
-    it += 2;
-    return true;
-  };
-
-#pragma unroll 1
-  for (bool first = true; ok && u.next(first); first = false) {
-    const int n = u.count(0);
-    if (n == 0) continue;
-    int y[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) y[i] = i < n ? box_row(u.j0 + i) : -1;
-#pragma unroll 1
-    for (int i = 0; ok && i < n; ++i) {
-      const int next = i + kAhead < n ? box_row(u.j0 + i + kAhead) : -1;
-      ok = bring(y[0]);
-#pragma unroll
-      for (int x = 0; x + 1 < kAhead; ++x) y[x] = y[x + 1];
-      y[kAhead - 1] = next;
-    }
-  }
-  if (bad) set_flag(a.flags, kDevBadPage);
-  // copies in flight land in this CTA's memory, which has to outlive them
-#pragma unroll 1
-  for (int i = max(values, it - S::kStages); i < it; i += 2)
-    (void)mbar_poll(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->calm, kNaps);
-  __syncwarp();
 }
 
 // ------------------------------------------------------------------ queries
@@ -254,12 +169,6 @@ __device__ __forceinline__ int fp4_key(int x) {
 __device__ __forceinline__ int fp4_place(int key) {
   return key / 32 * 32 + 8 * (key % 4) + 2 * (key % 16 / 4) + key % 32 / 16;
 }
-// Byte of 16-byte piece `piece` of a row of packed codes, as its TMA load swizzles it.
-template <int kD>
-__device__ __forceinline__ uint32_t fp4_piece(int row, int piece) {
-  return kD == 128 ? row * 64 + ((piece ^ (row / 2 % 4)) * 16) : row * 32 + ((piece ^ (row / 4 % 2)) * 16);
-}
-
 // Four warps: a thread unpacks a key to its lane of tensor memory, two columns
 // of the head a column.
 template <int kD, typename S>
@@ -273,7 +182,7 @@ __device__ __forceinline__ void fp4_keys(const Fp4Args& a, AttnWalk<S> u, Fp4Con
     const int n = u.count(0);
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++g) {
-      const int stage = 2 * g % S::kStages, lap = 2 * g / S::kStages;
+      const int stage = 2 * g % S::kPackedStages, lap = 2 * g / S::kPackedStages;
       if (!mbar_await(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a))) return;
       const char* tile = ring + stage * S::kStageBytes;
       // the scores of the tile before are done, and its keys free
@@ -285,7 +194,7 @@ __device__ __forceinline__ void fp4_keys(const Fp4Args& a, AttnWalk<S> u, Fp4Con
       // long code waits for its instructions
 #pragma unroll 1
       for (int p = 0; p < kD / 32; ++p) {
-        const uint32_t pair = fp4_scales(*(const uint16_t*)(tile + S::kCodeBytes + key * (kD / 16) + p * 2));
+        const uint32_t pair = fp4_scales(*(const uint16_t*)(tile + Fp4Tile<kD>::kCodeBytes + key * (kD / 16) + p * 2));
         const uint32_t s0 = __byte_perm(pair, 0, 0x1010), s1 = __byte_perm(pair, 0, 0x3232);
         uint32_t r[16];
         fp4_unpack(w.x, r);
@@ -327,7 +236,7 @@ __device__ __forceinline__ void fp4_values(const Fp4Args& a, AttnWalk<S> u, Fp4C
     const int n = u.count(0);
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++g) {
-      const int stage = (2 * g + 1) % S::kStages, lap = (2 * g + 1) / S::kStages;
+      const int stage = (2 * g + 1) % S::kPackedStages, lap = (2 * g + 1) / S::kPackedStages;
       if (!mbar_await(smem_addr(&c->full[stage]), lap & 1, &c->abort_word, naps_of(a))) return;
       const char* tile = ring + stage * S::kStageBytes;
       if (active) {
@@ -335,7 +244,7 @@ __device__ __forceinline__ void fp4_values(const Fp4Args& a, AttnWalk<S> u, Fp4C
 #pragma unroll
         for (int y = 0; y < 2; ++y) {   // pairs lane and 32 + lane
           const int key = (y * 2 + lane / 16) * 32 + lane % 16;
-          const char* from = tile + S::kCodeBytes + key * (kD / 16) + warp * 2;
+          const char* from = tile + Fp4Tile<kD>::kCodeBytes + key * (kD / 16) + warp * 2;
           const uint32_t s0 = key < left ? fp4_scales(*(const uint16_t*)from) : 0;
           const uint32_t s1 = key + 16 < left ? fp4_scales(*(const uint16_t*)(from + kD)) : 0;
           scales[y * 32 + lane] = __byte_perm(s0, s1, 0x5410);
@@ -737,7 +646,7 @@ __global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, Fp4Shape<kD, kR
   char* q_ptr = smem;
   char* p_ptr = q_ptr + 2 * S::kQBytes;
   char* ring = p_ptr + 2 * S::kPBytes;
-  char* value_scales = ring + S::kStages * S::kStageBytes;
+  char* value_scales = ring + S::kPackedStages * S::kStageBytes;
   float* stats = (float*)(value_scales + S::kValueScales);
   Fp4Control* c = (Fp4Control*)((char*)stats + S::kStatBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -745,8 +654,8 @@ __global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, Fp4Shape<kD, kR
 
   if (warp == kLoader && lane == 0) {
 #pragma unroll 1
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(smem_addr(&c->full[i]), 1);
+    for (int i = 0; i < S::kPackedStages; ++i) {
+      mbar_init(smem_addr(&c->full[i]), 33);   // the boxes' and the lanes'
       mbar_init(smem_addr(&c->empty[i]), 4);
     }
 #pragma unroll 1
@@ -784,9 +693,9 @@ __global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, Fp4Shape<kD, kR
       else fp4_values<kD, S>(a, u, c, ring, tmem, value_scales);
     } else {
       if (kMany || kFew) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-      if (warp == kLoader) fp4_load<kD, S>(a, u, c, ring, &k_map, a.k_scales, 0);
+      if (warp == kLoader) fp4_load<kD, S>(a, u, c, c->full, c->empty, ring, &k_map, &v_map, true, false);
       else if (warp == kLoader + 1) fp4_multiply<kD, S>(a, u, c, smem_addr(q_ptr), smem_addr(p_ptr), tmem);
-      else if (warp == kLoader + 2) fp4_load<kD, S>(a, u, c, ring, &v_map, a.v_scales, 1);
+      else if (warp == kLoader + 2) fp4_load<kD, S>(a, u, c, c->full, c->empty, ring, &k_map, &v_map, false, true);
       else fp4_queries<E, kD, S>(a, u, c, q_ptr);
     }
   }

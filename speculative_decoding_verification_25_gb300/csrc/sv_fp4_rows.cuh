@@ -1,0 +1,262 @@
+// Attention over the 4-bit cache for more than a few query rows a request: the
+// products and the softmax of sv_paged_attention.cuh, in its wide and narrow forms,
+// over tiles that four warps unpack to 16 bits in shared memory, from a ring of
+// packed ones.
+//
+// Operands are float16 as in sv_fp4_attention.cuh: bfloat16 queries are
+// converted in shared memory, each query tile with a power of two of its own.
+#pragma once
+
+#include "sv_fp4_load.cuh"
+
+namespace sv {
+
+// The wide form's shape, and a narrow one: one query tile against tiles of 128 keys
+// with two S buffers, one CTA per SM.
+template <int kD, bool kWide>
+struct Fp4RowsShape : AttnShape<kD, true> {
+  using Base = AttnShape<kD, true>;
+  static constexpr bool kFp4 = true;
+  static constexpr int kTiles = kWide ? 2 : 1;
+  static constexpr int kBufs = kWide ? 1 : 2;
+  static constexpr int kStages = kD == 128 ? 3 : 6;           // unpacked
+  static constexpr int kPackedStages = kWide ? (kD == 128 ? 2 : 4) : kD == 128 ? 8 : 16;
+  static constexpr int kSoftThreads = 128 * kTiles;
+  static constexpr int kThreads = kSoftThreads + 256;   // whole warpgroups
+  static constexpr int kUnitCost = kWide ? 256 : 64;
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kControlBytes = 1024;
+  static constexpr int kSmemBytes = kTiles * (Base::kQBytes + 4 * Base::kStagingBytes) +
+                                    kStages * Base::kStageBytes + kPackedStages * Fp4Tile<kD>::kBytes +
+                                    kControlBytes;
+};
+
+struct Fp4RowsControl {   // as AttnControl, and:
+  uint64_t full[8], empty[8];
+  uint64_t q_full, q_empty, drain, met;
+  uint64_t s_full[2][2], p_ready[2][2];
+  uint64_t pv_done[2];
+  uint64_t q_raw;             // queries have arrived, not converted
+  uint64_t packed_full[16], packed_empty[16];
+  uint32_t tmem;
+  volatile int past;
+  int abort_word, calm, last;
+  unsigned status;
+  int q_exponent[2][2];       // [unit % 2][query tile]
+  AttnStart start;
+  long long sums[16];
+};
+static_assert(sizeof(Fp4RowsControl) <= 1024, "fits kControlBytes");
+
+// One warp brings a unit's queries and converts its rows in place where they are
+// bfloat16.
+template <typename E, int kD, typename S>
+__device__ __forceinline__ void fp4_rows_queries(const Fp4Args& a, AttnWalk<S> u, Fp4RowsControl* c,
+                                                 char* q_ptr, const CUtensorMap* q_map) {
+  const int lane = threadIdx.x & 31;
+  int rounds = 0, brought = 0;
+#pragma unroll 1
+  for (bool first = true; u.next(first); first = false) {
+    if (u.most() == 0) continue;
+    if (rounds > 0 && !mbar_wait(smem_addr(&c->q_empty), (rounds - 1) & 1, &c->abort_word, naps_of(a)))
+      break;
+    const uint32_t bar = smem_addr(&c->q_raw);
+    const int q_tile = lane / S::kBlocks, block = lane % S::kBlocks;
+    const bool mine = q_tile < S::kTiles && u.count(q_tile) > 0;
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) mbar_arrive_expect(bar, __popc(who) * a.tile_tokens * a.G * 128);
+    __syncwarp();
+    if (mine)
+      tma_load_3d(smem_addr(q_ptr) + q_tile * S::kQBytes + block * 128 * 128, q_map, block * 64, u.h * a.G,
+                  u.units.row.begin + u.first(q_tile), bar);
+    ++brought;
+    if (!mbar_wait(bar, rounds & 1, &c->abort_word, naps_of(a))) break;
+#pragma unroll 1
+    for (int t = 0; t < S::kTiles; ++t) {
+      int exponent = 0;
+      if (std::is_same<E, __nv_bfloat16>::value && u.count(t) > 0) {
+        const int pieces = (u.last(t) - u.first(t)) * a.G * 8;   // of 16 bytes in a block of 64 columns
+        float top = 0.f;
+#pragma unroll 1
+        for (int b = 0; b < S::kBlocks; ++b) {
+          const char* tile = q_ptr + t * S::kQBytes + b * 128 * 128;
+#pragma unroll 4
+          for (int x = lane; x < pieces; x += 32) {
+            const uint4 w = *(const uint4*)(tile + x * 16);
+            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float lo = fabsf(__uint_as_float(v[y] << 16)), hi = fabsf(__uint_as_float(v[y] & 0xffff0000u));
+              if (lo < 3.4e38f) top = fmaxf(top, lo);   // neither infinities nor NaN
+              if (hi < 3.4e38f) top = fmaxf(top, hi);
+            }
+          }
+        }
+        top = warp_max(top);
+        // magnitudes between 2^-2 and 2^15 need no scaling
+        if (!(top == 0.f || (top >= 0.25f && top < 32768.f)))
+          exponent = (int)(__float_as_uint(top) >> 23) - 127 - 14;   // subnormal: as if 2^-127
+        // 2^-exponent in two factors, each of which is a normal number
+        const float f0 = ldexpf(1.f, -exponent / 2), f1 = ldexpf(1.f, -exponent - -exponent / 2);
+#pragma unroll 1
+        for (int b = 0; b < S::kBlocks; ++b) {
+          char* tile = q_ptr + t * S::kQBytes + b * 128 * 128;
+#pragma unroll 4
+          for (int x = lane; x < pieces; x += 32) {
+            const uint4 w = *(const uint4*)(tile + x * 16);
+            uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              v[y] = pack2(__uint_as_float(v[y] << 16) * f0 * f1, __uint_as_float(v[y] & 0xffff0000u) * f0 * f1,
+                           __half());
+            *(uint4*)(tile + x * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+      if (lane == 0) c->q_exponent[rounds % 2][t] = exponent;
+    }
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_addr(&c->q_full));
+    ++rounds;
+  }
+  // a copy in flight lands in this CTA's memory
+  if (brought > 0) (void)mbar_poll(smem_addr(&c->q_raw), (brought - 1) & 1, &c->calm, kNaps);
+  __syncwarp();
+}
+
+// Four warps unpack, a key per thread, in the order in which the products take
+// tiles: kBufs tiles of keys, then values and keys in turn.  The two rings need not
+// keep step: keys have the packed one's even slots, values the odd ones.
+template <int kD, typename S>
+__device__ __forceinline__ void fp4_rows_unpack(const Fp4Args& a, AttnWalk<S> u, Fp4RowsControl* c,
+                                                const char* packed, char* ring) {
+  const int key = threadIdx.x % 128, lane = threadIdx.x & 31;
+  int it = 0, done = 0;   // unpacked tiles; key tiles of the units before
+  auto unpack = [&](int tile, bool values) -> bool {
+    const int from = 2 * (done + tile) + values, slot = from % S::kPackedStages;
+    const int stage = it % S::kStages, lap = it / S::kStages;
+    if (!mbar_await(smem_addr(&c->packed_full[slot]), (from / S::kPackedStages) & 1, &c->abort_word, naps_of(a)) ||
+        (lap > 0 && !mbar_await(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, naps_of(a))))
+      return false;
+    const char* codes = packed + slot * Fp4Tile<kD>::kBytes;
+    const char* scales = codes + Fp4Tile<kD>::kCodeBytes + key * (kD / 16);
+    char* to = ring + stage * S::kStageBytes + key * 128;
+    // rolled up as in fp4_keys
+#pragma unroll 1
+    for (int p = 0; p < kD / 32; ++p) {
+      const uint4 w4 = *(const uint4*)(codes + fp4_piece<kD>(key, p));
+      const uint32_t pair = fp4_scales(*(const uint16_t*)(scales + p * 2));
+      const uint32_t s[2] = {__byte_perm(pair, 0, 0x1010), __byte_perm(pair, 0, 0x3232)};
+      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      char* block = to + (p / 2) * (S::kKeys * 128);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t v[4];
+        fp4_unpack(w[x], v);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) v[y] = mul_f16x2(v[y], s[x / 2]);
+        *(uint4*)(block + ((p % 2 * 4 + x) ^ (key % 8)) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(smem_addr(&c->packed_empty[slot]));
+      mbar_arrive(smem_addr(&c->full[stage]));
+    }
+    ++it;
+    return true;
+  };
+#pragma unroll 1
+  for (bool first = true; u.next(first); first = false) {
+    const int n = u.most(), lead = min(n, S::kBufs);
+#pragma unroll 1
+    for (int i = -lead; i < n; ++i) {
+      // values of tile i, then keys of the one kBufs ahead; keys alone at first
+      if (i >= 0 && !unpack(i, true)) return;
+      if (i + lead < n && !unpack(i + lead, false)) return;
+    }
+    done += n;
+  }
+}
+
+template <typename E, int kD, bool kWide>
+__global__ void __launch_bounds__(Fp4RowsShape<kD, kWide>::kThreads, Fp4RowsShape<kD, kWide>::kCtasPerSm)
+    sv_fp4_rows_attention_kernel(const __grid_constant__ Fp4Args a, const __grid_constant__ CUtensorMap q_map,
+                                 const __grid_constant__ CUtensorMap k_map,
+                                 const __grid_constant__ CUtensorMap v_map) {
+  using S = Fp4RowsShape<kD, kWide>;
+  extern __shared__ __align__(1024) char smem[];
+  char* ring = smem + S::kTiles * S::kQBytes;
+  char* staging = ring + S::kStages * S::kStageBytes;
+  char* packed = staging + S::kTiles * 4 * S::kStagingBytes;
+  Fp4RowsControl* c = (Fp4RowsControl*)(packed + S::kPackedStages * Fp4Tile<kD>::kBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kQueries = S::kSoftThreads / 32, kLoader = kQueries + 1, kIssuer = kQueries + 2;
+  constexpr int kUnpack = kQueries + 4;
+
+  if (warp == kQueries && lane == 0) {
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) {
+      mbar_init(smem_addr(&c->full[i]), 4);
+      mbar_init(smem_addr(&c->empty[i]), S::kTiles);
+    }
+#pragma unroll 1
+    for (int i = 0; i < S::kPackedStages; ++i) {
+      mbar_init(smem_addr(&c->packed_full[i]), 33);   // the boxes' and the lanes'
+      mbar_init(smem_addr(&c->packed_empty[i]), 4);
+    }
+    mbar_init(smem_addr(&c->q_raw), 1);
+    mbar_init(smem_addr(&c->q_full), 1);
+    mbar_init(smem_addr(&c->q_empty), S::kTiles);
+    mbar_init(smem_addr(&c->drain), S::kTiles);
+    mbar_init(smem_addr(&c->met), S::kSoftThreads / 32);
+#pragma unroll 1
+    for (int t = 0; t < S::kTiles; ++t) {
+      for (int k = 0; k < S::kBufs; ++k) {
+        mbar_init(smem_addr(&c->s_full[t][k]), 1);
+        mbar_init(smem_addr(&c->p_ready[t][k]), S::kTiles > 1 ? 5 : 4);   // with the turn
+      }
+      mbar_init(smem_addr(&c->pv_done[t]), 1);
+    }
+    mbar_init_fence();
+    c->abort_word = c->calm = c->past = 0;
+    tma_prefetch_map(&q_map);
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
+  }
+  if (warp == kIssuer) tmem_alloc<S::kTmemCols>(smem_addr(&c->tmem));
+  wait_for_preceding_grid();
+  const AttnRange range = attn_range<S>(a, c);
+  const uint32_t tmem = c->tmem;
+  if (range.w0 < range.w1) {
+    const AttnWalk<S> u(a, c->start, range.w1 - range.w0);
+    // Wide: launched with 128 registers a thread, and 2 x 184 + 72 + 72 = 4 x 128;
+    // narrow: 168, and 232 + 120 + 152 = 3 x 168.
+    if (warp >= kUnpack) {
+      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
+      fp4_rows_unpack<kD, S>(a, u, c, packed, ring);
+    } else if (warp >= kQueries) {
+      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+      // narrow: a loader each for keys and values
+      if (warp >= kIssuer && warp < kIssuer + S::kTiles)
+        attn_multiply<__half, kD, S>(a, u, c, smem_addr(smem), smem_addr(ring), ring, tmem, warp - kIssuer);
+      else if (warp == kQueries)
+        fp4_rows_queries<E, kD, S>(a, u, c, smem, &q_map);
+      else
+        fp4_load<kD, S>(a, u, c, c->packed_full, c->packed_empty, packed, &k_map, &v_map, warp == kLoader,
+                        kWide || warp != kLoader);
+    } else {
+      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      else asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+      attn_softmax<__half, E, kD, S>(a, u, c, tmem, staging, range.quota, range.w1);
+    }
+  }
+  attn_finish<S, kD>(a, c, range.spoilt);
+  if (warp == kIssuer) tmem_free<S::kTmemCols>(tmem);
+}
+
+}  // namespace sv

@@ -431,7 +431,7 @@ __device__ __forceinline__ bool wait_past(Control* c, int units, int naps) {
 // The products of one warp run in the order of their issue: S of the next
 // keys follows O += P V, whose P lies where S goes.
 // Columns of tensor memory: kBufs S buffers per query tile, then one O per
-// query tile.
+// query tile.  Over a 4-bit cache an elected lane issues.
 template <typename E, int kD, typename S, typename Control>
 __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, Control* c,
                                               uint32_t q_smem, uint32_t ring, char* ring_ptr,
@@ -466,19 +466,35 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
   // which last about as long as the other warp takes to see it
   auto scores = [&](int k, int stage, bool pass) {
     const uint64_t k0 = k_desc + stage * (S::kStageBytes / 16);
+    if constexpr (S::kFp4) {
+      if (elect_one()) {
 #pragma unroll
-    for (int d = 0; d < kD / 16; ++d) {
-      if (S::kTiles > 1 && d == kD / 16 - 2) pass_turn(pass);
-      mma_smem(s_col(k), q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
-               k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0, issue);
+        for (int d = 0; d < kD / 16; ++d) {
+          if (S::kTiles > 1 && d == kD / 16 - 2 && pass) mbar_arrive(smem_addr(&c->p_ready[1 - t][0]));
+          mma_smem_one(s_col(k), q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
+                       k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0);
+        }
+        tc_commit_one(smem_addr(&c->s_full[t][k % S::kBufs]));
+      }
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int d = 0; d < kD / 16; ++d) {
+        if (S::kTiles > 1 && d == kD / 16 - 2) pass_turn(pass);
+        mma_smem(s_col(k), q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
+                 k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0, issue);
+      }
+      tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]), issue);
     }
-    tc_commit(smem_addr(&c->s_full[t][k % S::kBufs]), issue);
   };
   // A slot is free once every issuer's products with it are done; one that
   // has none waits for the slot to be full all the same, so that its arrivals
   // keep to the slot's laps.
   auto release = [&](uint64_t* bar, bool used) {
-    if (used) tc_commit(smem_addr(bar), issue);
+    if (used && S::kFp4) {
+      if (elect_one()) tc_commit_one(smem_addr(bar));
+      __syncwarp();
+    } else if (used) tc_commit(smem_addr(bar), issue);
     else if (lane == 0) mbar_arrive(smem_addr(bar));
   };
 
@@ -538,6 +554,14 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       const bool pass = active && (t == 0 ? i < other : i + 1 < other);
       if (active) {
         const uint64_t v0 = v_desc + (v_it % S::kStages) * (S::kStageBytes / 16);
+        if constexpr (S::kFp4) {
+          if (elect_one()) {
+#pragma unroll
+            for (int x = 0; x < S::kKeys / 16; ++x)
+              mma_tmem_one(o, s_col(k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0);
+          }
+          __syncwarp();
+        } else
 #pragma unroll
         for (int x = 0; x < S::kKeys / 16; ++x)
           mma_tmem(o, s_col(k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0, issue);
