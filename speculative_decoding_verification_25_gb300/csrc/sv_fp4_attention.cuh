@@ -36,7 +36,7 @@ struct Fp4Shape {
   static constexpr int kRows = kRowsMost;                  // query rows of a unit, at most
   static constexpr int kGroups = kRows > 64 ? 2 : 1;       // groups of four softmax warps
   static constexpr int kCols = kRows / kGroups;            // rows of such a group
-  static constexpr int kUnitCost = 64;
+  static constexpr int kUnitCost = 768;
   static constexpr int kSoftThreads = 128 * kGroups;
   static constexpr int kThreads = kSoftThreads + 2 * 128 + 128;
   static constexpr int kBlocks = kD / 64;

@@ -20,10 +20,10 @@ struct Fp4RowsShape : AttnShape<kD, true> {
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kBufs = kWide ? 1 : 2;
   static constexpr int kStages = kD == 128 ? 3 : 6;           // unpacked
-  static constexpr int kPackedStages = kWide ? (kD == 128 ? 2 : 4) : kD == 128 ? 8 : 16;
+  static constexpr int kPackedStages = kWide ? (kD == 128 ? 3 : 8) : kD == 128 ? 8 : 16;
   static constexpr int kSoftThreads = 128 * kTiles;
   static constexpr int kThreads = kSoftThreads + 256;   // whole warpgroups
-  static constexpr int kUnitCost = kWide ? 256 : 64;
+  static constexpr int kUnitCost = kWide ? 256 : 512;
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kControlBytes = 1024;
   static constexpr int kSmemBytes = kTiles * (Base::kQBytes + 4 * Base::kStagingBytes) +
@@ -76,21 +76,28 @@ __device__ __forceinline__ void fp4_rows_queries(const Fp4Args& a, AttnWalk<S> u
       int exponent = 0;
       if (std::is_same<E, __nv_bfloat16>::value && u.count(t) > 0) {
         const int pieces = (u.last(t) - u.first(t)) * a.G * 8;   // of 16 bytes in a block of 64 columns
-        float top = 0.f;
+        char* tile = q_ptr + t * S::kQBytes;
+        // magnitudes as integers, two a word, in the order of their numbers
+        uint32_t high = 0;
 #pragma unroll 1
-        for (int b = 0; b < S::kBlocks; ++b) {
-          const char* tile = q_ptr + t * S::kQBytes + b * 128 * 128;
-#pragma unroll 4
+        for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll 8
           for (int x = lane; x < pieces; x += 32) {
-            const uint4 w = *(const uint4*)(tile + x * 16);
-            const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float lo = fabsf(__uint_as_float(v[y] << 16)), hi = fabsf(__uint_as_float(v[y] & 0xffff0000u));
-              if (lo < 3.4e38f) top = fmaxf(top, lo);   // neither infinities nor NaN
-              if (hi < 3.4e38f) top = fmaxf(top, hi);
-            }
+            const uint4 w = *(const uint4*)(tile + b * 128 * 128 + x * 16);
+            high = __vmaxu2(__vmaxu2(high, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
+            high = __vmaxu2(__vmaxu2(high, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
           }
+        float top = __uint_as_float(max(high >> 16, high & 0xffffu) << 16);
+        if (__any_sync(0xffffffffu, !(top <= 3.4e38f))) {   // an infinity or NaN: the largest of the others
+          top = 0.f;
+#pragma unroll 1
+          for (int b = 0; b < S::kBlocks; ++b)
+#pragma unroll 1
+            for (int x = lane; x < pieces * 8; x += 32) {
+              const float v =
+                  __uint_as_float((uint32_t)(*(const uint16_t*)(tile + b * 128 * 128 + x * 2) & 0x7fffu) << 16);
+              if (v <= 3.4e38f) top = fmaxf(top, v);
+            }
         }
         top = warp_max(top);
         // magnitudes between 2^-2 and 2^15 need no scaling
@@ -99,19 +106,19 @@ __device__ __forceinline__ void fp4_rows_queries(const Fp4Args& a, AttnWalk<S> u
         // 2^-exponent in two factors, each of which is a normal number
         const float f0 = ldexpf(1.f, -exponent / 2), f1 = ldexpf(1.f, -exponent - -exponent / 2);
 #pragma unroll 1
-        for (int b = 0; b < S::kBlocks; ++b) {
-          char* tile = q_ptr + t * S::kQBytes + b * 128 * 128;
+        for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll 4
           for (int x = lane; x < pieces; x += 32) {
-            const uint4 w = *(const uint4*)(tile + x * 16);
-            uint32_t v[4] = {w.x, w.y, w.z, w.w};
+            uint4* at = (uint4*)(tile + b * 128 * 128 + x * 16);
+            uint32_t v[4] = {at->x, at->y, at->z, at->w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
-              v[y] = pack2(__uint_as_float(v[y] << 16) * f0 * f1, __uint_as_float(v[y] & 0xffff0000u) * f0 * f1,
-                           __half());
-            *(uint4*)(tile + x * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+            for (int y = 0; y < 4; ++y) {
+              float lo = __uint_as_float(v[y] << 16), hi = __uint_as_float(v[y] & 0xffff0000u);
+              if (exponent != 0) lo = lo * f0 * f1, hi = hi * f0 * f1;
+              v[y] = pack2(lo, hi, __half());
+            }
+            *at = make_uint4(v[0], v[1], v[2], v[3]);
           }
-        }
       }
       if (lane == 0) c->q_exponent[rounds % 2][t] = exponent;
     }
