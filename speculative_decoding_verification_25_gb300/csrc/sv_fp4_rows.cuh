@@ -17,16 +17,19 @@ template <int kD, bool kWide>
 struct Fp4RowsShape : AttnShape<kD, true> {
   using Base = AttnShape<kD, true>;
   static constexpr bool kFp4 = true;
+  // wide: a fourth unpacked tile in place of the staging (prompt chunks 445 and 396 us)
+  static constexpr bool kStaged = !kWide;
+  static constexpr int kStagingBytes = kWide ? 64 : Base::kStagingBytes;
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kBufs = kWide ? 1 : 2;
-  static constexpr int kStages = kD == 128 ? 3 : 6;           // unpacked
+  static constexpr int kStages = (kWide ? 4 : 3) * (128 / kD);   // unpacked
   static constexpr int kPackedStages = kWide ? (kD == 128 ? 3 : 8) : kD == 128 ? 8 : 16;
   static constexpr int kSoftThreads = 128 * kTiles;
   static constexpr int kThreads = kSoftThreads + 256;   // whole warpgroups
   static constexpr int kUnitCost = kWide ? 256 : 512;
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kControlBytes = 1024;
-  static constexpr int kSmemBytes = kTiles * (Base::kQBytes + 4 * Base::kStagingBytes) +
+  static constexpr int kSmemBytes = kTiles * (Base::kQBytes + 4 * kStagingBytes) +
                                     kStages * Base::kStageBytes + kPackedStages * Fp4Tile<kD>::kBytes +
                                     kControlBytes;
 };
@@ -132,9 +135,10 @@ __device__ __forceinline__ void fp4_rows_queries(const Fp4Args& a, AttnWalk<S> u
   __syncwarp();
 }
 
-// Four warps unpack, a key per thread, in the order in which the products take
-// tiles: kBufs tiles of keys, then values and keys in turn.  The two rings need not
-// keep step: keys have the packed one's even slots, values the odd ones.
+// Four warps unpack, a key per thread, in the order in which the products take tiles:
+// kBufs tiles of keys, then values and keys in turn.  The two rings need not keep
+// step: keys have the packed one's even places, values the odd.  (A group of four
+// warps each for keys and values is slower: 64 x 5 tokens 118 and 133 us.)
 template <int kD, typename S>
 __device__ __forceinline__ void fp4_rows_unpack(const Fp4Args& a, AttnWalk<S> u, Fp4RowsControl* c,
                                                 const char* packed, char* ring) {
@@ -240,14 +244,14 @@ __global__ void __launch_bounds__(Fp4RowsShape<kD, kWide>::kThreads, Fp4RowsShap
   if (range.w0 < range.w1) {
     const AttnWalk<S> u(a, c->start, range.w1 - range.w0);
     // Wide: launched with 128 registers a thread, and 2 x 184 + 72 + 72 = 4 x 128;
-    // narrow: 168, and 232 + 120 + 152 = 3 x 168.
+    // narrow: 168, and 232 + 2 x 136 = 3 x 168.
     if (warp >= kUnpack) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      else asm volatile("setmaxnreg.dec.sync.aligned.u32 152;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
       fp4_rows_unpack<kD, S>(a, u, c, packed, ring);
     } else if (warp >= kQueries) {
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-      else asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
       // narrow: a loader each for keys and values
       if (warp >= kIssuer && warp < kIssuer + S::kTiles)
         attn_multiply<__half, kD, S>(a, u, c, smem_addr(smem), smem_addr(ring), ring, tmem, warp - kIssuer);

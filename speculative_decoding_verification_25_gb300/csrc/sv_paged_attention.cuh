@@ -93,6 +93,7 @@ __device__ __forceinline__ int naps_of(const AttnArgs& a) { return kChecked ? a.
 template <int kD, bool kWide>
 struct AttnShape {
   static constexpr bool kFp4 = false;                // the 4-bit cache's shape has it true
+  static constexpr bool kStaged = true;              // rows pass through shared memory on their way out
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kKeys = kWide ? 128 : 64;
   static constexpr int kBufs = kWide ? 1 : 2;        // S buffers per query tile
@@ -658,6 +659,15 @@ __device__ __forceinline__ void store_staged(unsigned* flags, const char* stage,
   __syncwarp();
 }
 
+// The same without: 16-byte pieces of the lane's own row.
+__device__ __forceinline__ void store_row(unsigned* flags, char* to, bool mine, const uint32_t* words,
+                                          int pieces, const void* array, long long all) {
+#pragma unroll
+  for (int i = 0; i < pieces; ++i)
+    if (mine && in_array(flags, (to - (const char*)array) / 16 + i, all))
+      ((uint4*)to)[i] = make_uint4(words[4 * i], words[4 * i + 1], words[4 * i + 2], words[4 * i + 3]);
+}
+
 // Joins the partial sums of the unit's CTAs in their order.  kSpan threads
 // share a row, each kD / kSpan of its columns, and take kAhead parts at a
 // time, so that their loads are in flight together: many rows have few parts
@@ -898,15 +908,23 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
           for (int y = 0; y < 16; ++y)
             p[y] = pack2(__uint_as_float(bits[2 * y]) * inv, __uint_as_float(bits[2 * y + 1]) * inv,
                          Out());
+          if constexpr (!S::kStaged) {
+            store_row(a.flags, base + (long long)to * (kD * 2) + x * 2, to >= 0, p, 4, a.out, out_rows * (kD / 8));
+          } else {
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            stage_piece(stage, x / 8 % 8 + y, p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
+            for (int y = 0; y < 4; ++y)
+              stage_piece(stage, x / 8 % 8 + y, p[4 * y], p[4 * y + 1], p[4 * y + 2], p[4 * y + 3]);
+          }
           if (x % 64 == 0) continue;
+        } else if constexpr (!S::kStaged) {
+          store_row(a.flags, base + (long long)to * (kD * 4) + x * 4, to >= 0, bits, 8, a.partial,
+                    part_rows * (kD / 4));
         } else {
 #pragma unroll
           for (int y = 0; y < 8; ++y)
             stage_piece(stage, y, bits[4 * y], bits[4 * y + 1], bits[4 * y + 2], bits[4 * y + 3]);
         }
+        if (!S::kStaged) continue;
         store_staged(a.flags, stage, base, to, whole ? kD * 2 : kD * 4, rows,
                      whole ? (const void*)a.out : a.partial,
                      whole ? out_rows * (kD / 8) : part_rows * (kD / 4));
