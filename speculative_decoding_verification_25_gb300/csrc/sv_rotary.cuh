@@ -20,6 +20,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "sv_fp4.cuh"
 #include "sv_paged.cuh"
 
@@ -298,7 +300,8 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
     *(float4*)angles.s = *(const float4*)(table + a.rot / 2 + at);
     *(float4*)(angles.s + 4) = *(const float4*)(table + a.rot / 2 + next);
   };
-  auto finish = [&](int h, const uint32_t* w) {
+  auto finish = [&](int h, const uint32_t* w, auto coded) {   // `coded`: keys and values become codes
+    constexpr bool kCoded = decltype(coded)::value;
     const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hk;
     const int hk = is_k ? h - a.Hq : h - a.Hq - a.Hk;
     const bool goes = !is_q && stored && h < heads &&
@@ -311,7 +314,7 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
     const bool turn = rotated && placed && (is_q || is_k);
     if (turn) rotate<float, kNeighbours>(angles, in, x);
     const long long row = slot_row + ((long long)hk << a.page_shift);
-    if (is_q || (!kFp4 && goes)) {
+    if (is_q || (!kCoded && goes)) {
       char* to = is_q ? a.q_out + token * a.out_pitch + (long long)h * kD * 2
                       : (is_k ? a.k_cache : a.v_cache) + row * kD * 2;
       uint32_t o[8];
@@ -320,7 +323,7 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
       *(uint4*)(to + p0 * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       *(uint4*)(to + p1 * 16) = make_uint4(o[4], o[5], o[6], o[7]);
     }
-    if (kFp4) {
+    if constexpr (kCoded) {
       if (!__any_sync(0xffffffffu, goes)) return;
       uint32_t scale[2], codes[2];
       const bool exact = !turn && (is_k ? a.k_plain : a.v_plain);
@@ -339,14 +342,15 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
     }
   };
 
-  if (kFp4) {   // the quantisation is long code: one copy of it, the next head on its way meanwhile
+  if (kFp4 && first_head + kRotaryHeads * kPass > a.Hq) {
+    // the quantisation is long code: one copy of it, the next head on its way meanwhile
     uint32_t w[2][8];
     load(mine, w[0]);
     look_up();
 #pragma unroll 1
     for (int u = 0; u < kRotaryHeads; ++u) {
       if (u + 1 < kRotaryHeads) load(mine + (u + 1) * kPass, w[1]);
-      finish(mine + u * kPass, w[0]);
+      finish(mine + u * kPass, w[0], std::integral_constant<bool, kFp4>());
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[0][i] = w[1][i];
     }
@@ -356,12 +360,12 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
     for (int u = 0; u < kRotaryHeads; ++u) load(mine + u * kPass, w[u]);
     look_up();
 #pragma unroll
-    for (int u = 0; u < kRotaryHeads; ++u) finish(mine + u * kPass, w[u]);
+    for (int u = 0; u < kRotaryHeads; ++u) finish(mine + u * kPass, w[u], std::false_type());
   }
 }
 
 template <typename E, int kD, bool kFp4>
-__global__ void __launch_bounds__(kRotaryThreads, kFp4 ? 3 : 2) sv_rotary_kernel(RotaryArgs a) {
+__global__ void __launch_bounds__(kRotaryThreads, 3) sv_rotary_kernel(RotaryArgs a) {
   wait_for_preceding_grid();
   allow_dependent_launch();
   constexpr int kHeads = kRotaryHeads * 32 / (kD / 16);   // of a warp
