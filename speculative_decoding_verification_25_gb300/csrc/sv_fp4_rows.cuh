@@ -19,6 +19,7 @@ struct Fp4RowsShape : AttnShape<kD, true> {
   static constexpr bool kFp4 = true;
   // wide: a fourth unpacked tile in place of the staging (prompt chunks 445 and 396 us)
   static constexpr bool kStaged = !kWide;
+  static constexpr int kChunk = kWide ? 128 : 64;
   static constexpr int kStagingBytes = kWide ? 64 : Base::kStagingBytes;
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kBufs = kWide ? 1 : 2;

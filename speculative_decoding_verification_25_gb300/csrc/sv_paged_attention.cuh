@@ -97,6 +97,7 @@ struct AttnShape {
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kKeys = kWide ? 128 : 64;
   static constexpr int kBufs = kWide ? 1 : 2;        // S buffers per query tile
+  static constexpr int kChunk = kKeys;               // scores that a thread takes at a time
   static constexpr int kBlocks = kD / 64;            // 128-byte column blocks of a row
   static constexpr int kQBytes = 128 * kD * 2;
   static constexpr int kStageBytes = kKeys * kD * 2;
@@ -789,19 +790,34 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
       };
       if (any) {
         const uint32_t s_col = tmem + lanes + (t * S::kBufs + buf) * S::kKeys;
-        uint32_t bits[S::kKeys];
-#pragma unroll
-        for (int x = 0; x < S::kKeys; x += 32) tmem_load32(s_col + x, bits + x);
-        tmem_wait_load();
-        tmem_pin<S::kKeys>(bits);
         const int left = seen - key0;   // keys of the tile that the row sees
-        if (fewest < key0 + S::kKeys) {
+        const bool masked = fewest < key0 + S::kKeys;
+        uint32_t bits[S::kChunk];
+        auto take = [&](int x0) {
 #pragma unroll
-          for (int x = 0; x < S::kKeys; ++x)
-            if (x >= left) bits[x] = 0xff800000u;
+          for (int x = 0; x < S::kChunk; x += 32) tmem_load32(s_col + x0 + x, bits + x);
+          tmem_wait_load();
+          tmem_pin<S::kChunk>(bits);
+          if (masked) {
+#pragma unroll
+            for (int x = 0; x < S::kChunk; ++x)
+              if (x0 + x >= left) bits[x] = 0xff800000u;
+          }
+        };
+        float top;
+        if constexpr (S::kChunk == S::kKeys) {
+          take(0);
+          top = row_max<S::kKeys>(bits);
+        } else {   // the maximum first, the scores once more for their exponentials
+          top = SV_NEG_INF;
+#pragma unroll 1
+          for (int x0 = 0; x0 < S::kKeys; x0 += S::kChunk) {
+            take(x0);
+            top = fmaxf(top, row_max<S::kChunk>(bits));
+          }
         }
         // The reference follows the maximum where that rises by more than kSlack.
-        const float high = row_max<S::kKeys>(bits) * scale;
+        const float high = top * scale;
         const bool raise = mine && (i == 0 ? high > m : high > m + kSlack);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (m == SV_NEG_INF ? 0.f : ex2_approx(m - high)) : 1.f;
@@ -829,8 +845,9 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
         const float ref = m == SV_NEG_INF ? 0.f : m;
         const unsigned long long scale2 = f2_pack(scale, scale);
         const unsigned long long ref2 = f2_pack(-ref, -ref);
+        auto exponentials = [&](int x0) {   // P of a chunk, in the place of S before it
 #pragma unroll
-        for (int x = 0; x < S::kKeys; x += 32) {
+        for (int x = 0; x < S::kChunk; x += 32) {
           uint32_t p[16];
 #pragma unroll
           for (int y = 0; y < 32; y += 2) {
@@ -844,20 +861,35 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
             bits[x + y + 1] = __float_as_uint(p1);
             p[y / 2] = pack2(p0, p1, E());
           }
-          tmem_store16(s_col + x / 2, p);
+          tmem_store16(s_col + (x0 + x) / 2, p);
+        }
+        };
+        // The sum of a chunk, of P before rounding.
+        auto add_up = [&]() {
+          unsigned long long sums[2] = {0, 0};
+#pragma unroll
+          for (int x = 0; x < S::kChunk; x += 2)
+            sums[(x / 2) % 2] = f2_add(sums[(x / 2) % 2], f2_pack(__uint_as_float(bits[x]),
+                                                                  __uint_as_float(bits[x + 1])));
+          float s0, s1;
+          f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
+          l += s0 + s1;
+        };
+        if constexpr (S::kChunk == S::kKeys) {
+          exponentials(0);
+        } else {
+#pragma unroll 1
+          for (int x0 = 0; x0 < S::kKeys; x0 += S::kChunk) {
+            take(x0);
+            exponentials(x0);
+            add_up();
+          }
         }
         tmem_wait_store();
         if (!(ok = give())) break;
-        // The row's sum, of P before rounding, off the chain (three whole prompts:
-        // 629 us; summed along with the exponentials, 642).
-        unsigned long long sums[2] = {0, 0};
-#pragma unroll
-        for (int x = 0; x < S::kKeys; x += 2)
-          sums[(x / 2) % 2] = f2_add(sums[(x / 2) % 2], f2_pack(__uint_as_float(bits[x]),
-                                                                __uint_as_float(bits[x + 1])));
-        float s0, s1;
-        f2_unpack(f2_add(sums[0], sums[1]), s0, s1);
-        l += s0 + s1;
+        // The row's sum, off the chain (three whole prompts: 629 us; summed along with
+        // the exponentials, 642).
+        if constexpr (S::kChunk == S::kKeys) add_up();
       } else if (!(ok = give())) {
         break;
       }
