@@ -46,10 +46,11 @@ Variant rows_variant() {
   using S = sv::Fp4RowsShape<kD, kWide>;
   return {(const void*)sv::sv_fp4_rows_attention_kernel<E, kD, kWide>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, 128};
 }
-enum Form { kFew, kNarrow, kWide, kForms };
+enum Form { kFew16, kFew32, kNarrow, kWide, kForms };
 template <typename E, int kD>
 Variant variant_of(Form form) {
-  return form == kFew      ? variant<E, kD, 16>()
+  return form == kFew16    ? variant<E, kD, 16>()
+         : form == kFew32  ? variant<E, kD, 32>()
          : form == kNarrow ? rows_variant<E, kD, false>()
                            : rows_variant<E, kD, true>();
 }
@@ -130,7 +131,8 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   const char* env = getenv("SV_FORM");
   const Form form = env ? (Form)atoi(env)
                     : rows_of_all > 128 * requests ? kWide
-                    : G > 16 || rows_of_all > 16 * requests ? kNarrow : kFew;
+                    : G > 32 || rows_of_all > 32 * requests ? kNarrow
+                    : G > 16 || rows_of_all > 16 * requests ? kFew32 : kFew16;
   const Variant v = variant_of(dtype, D, form);
   int ctas = dev->sm_count * v.ctas_per_sm;
   if (ctas > sv::kAttnMaxCtas) ctas = sv::kAttnMaxCtas;
@@ -166,7 +168,7 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   CUtensorMap q_map, k_map, v_map;
   if (!encode_codes(*dev, &k_map, k_codes, D, rows, box) || !encode_codes(*dev, &v_map, v_codes, D, rows, box))
     return SV_ERR_CUDA;
-  if (form == kFew) {
+  if (form <= kFew32) {
     void* args[] = {&a, &k_map, &v_map};
     return done(launch_early(v.fn, dim3((unsigned)ctas), dim3((unsigned)v.threads), args, (cudaStream_t)stream,
                              (size_t)v.smem_bytes));

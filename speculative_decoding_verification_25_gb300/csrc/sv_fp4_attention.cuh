@@ -34,21 +34,19 @@ struct Fp4Shape {
   static constexpr int kTiles = 1;
   static constexpr int kKeys = 128;
   static constexpr int kRows = kRowsMost;                  // query rows of a unit, at most
-  static constexpr int kGroups = kRows > 64 ? 2 : 1;       // groups of four softmax warps
-  static constexpr int kCols = kRows / kGroups;            // rows of such a group
   static constexpr int kUnitCost = 768;
-  static constexpr int kSoftThreads = 128 * kGroups;
+  static constexpr int kSoftThreads = 128;
   static constexpr int kThreads = kSoftThreads + 2 * 128 + 128;
   static constexpr int kBlocks = kD / 64;
   static constexpr int kQBytes = kRows * kD * 2;           // two of them
-  static constexpr int kPRow = kRows < 64 ? kRows * 2 : 128;   // bytes of a row of P^T, in blocks of 64 rows of the unit
-  static constexpr int kPBytes = 128 * kPRow * ((kRows + 63) / 64);   // two of them
+  static constexpr int kPRow = kRows * 2;                  // bytes of a row of P^T
+  static constexpr int kPBytes = 128 * kPRow;              // two of them
   static constexpr int kStageBytes = Fp4Tile<kD>::kBytes;
-  static constexpr int kCtasPerSm = kRows > 16 ? 1 : 2;
+  static constexpr int kCtasPerSm = 2;
   static constexpr int kTmemCols = 512 / kCtasPerSm;
   static constexpr int kValueScales = 128 * (kD / 16) * 2; // float16
   static constexpr int kControlBytes = 1024;
-  static constexpr int kStatBytes = kGroups * 64 * 4 * (4 + 3);   // of four warps, and three of a row
+  static constexpr int kStatBytes = kRows * 4 * (4 + 3);   // of four warps, and three of a row
   static constexpr int kFixedBytes = 2 * (kQBytes + kPBytes) + kValueScales + kControlBytes + kStatBytes;
   static constexpr int kMostStages = (228 * 1024 / kCtasPerSm - 1024 - kFixedBytes) / kStageBytes;
   static constexpr int kPackedStages = kMostStages >= 16 ? 16 : kMostStages >= 8 ? 8 : 4;   // a power of two
@@ -379,34 +377,31 @@ __device__ __forceinline__ float warp_sums(float* v) {
   return v[0];
 }
 
-// A group of four warps: rows [group * kCols, group * kCols + kCols) of the unit.
-// No warp leaves alone: what went wrong is told at the next vote.
+// Four warps; none leaves alone: what went wrong is told at the next vote.
 template <typename E, int kD, typename S>
 __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4Control* c, uint32_t tmem,
                                             char* p_ptr, float* stats, long long quota, long long w1) {
-  constexpr int kCols = S::kCols;
-  constexpr int kChunk = kCols < 32 ? kCols : 32;
-  constexpr bool kKeep = kCols <= 32;                     // scores stay in registers over the vote
-  const int lane = threadIdx.x & 31, x = threadIdx.x % 128, warp = x / 32, group = threadIdx.x / 128;
-  const int id = 1 + group;                               // of the group's barrier
+  constexpr int kCols = S::kRows, kChunk = 16;
+  constexpr bool kKeep = kCols == kChunk;                 // scores stay in registers over the vote
+  constexpr int id = 1;                                   // of the barrier
+  const int lane = threadIdx.x & 31, x = threadIdx.x, warp = x / 32;
   const uint32_t lanes = (uint32_t)(warp * 32) << 16;
   const int my_key = fp4_key(x), place = fp4_place(my_key);
-  float* tops = stats + group * (7 * 64);                 // [warp][64], then of a row:
-  float* refs = tops + 4 * 64;                            // the negative reference
-  float* marks = refs + 64;                               // the reference, or its inverse sum
-  float* factors = marks + 64;
+  float* tops = stats;                                    // [warp][kCols], then of a row:
+  float* refs = tops + 4 * kCols;                            // the negative reference
+  float* marks = refs + kCols;                               // the reference, or its inverse sum
+  float* factors = marks + kCols;
   // 16-byte pieces of the thread's row of P^T, as the product's layout swizzles them
-  const int turn = S::kPRow == 128 ? place % 8 : S::kPRow == 64 ? place / 2 % 4 : place / 4 % 2;
-  char* p_row = p_ptr + group * (128 * 128) + place * S::kPRow;
-  const uint32_t s_col = tmem + lanes + S::kS + group * kCols, o_col = tmem + lanes + S::kO + group * kCols;
+  const int turn = S::kPRow == 64 ? place / 2 % 4 : place / 4 % 2;
+  char* p_row = p_ptr + place * S::kPRow;
+  const uint32_t s_col = tmem + lanes + S::kS, o_col = tmem + lanes + S::kO;
   int g = 0, rounds = 0, meetings = 0;
   bool ok = true;
 
 #pragma unroll 1
   for (bool first = true; u.next(first); first = false) {
     const int n = u.count(0);
-    const int rows = min(kCols, u.rows() - group * kCols);  // of this group; none or fewer: no work
-    const int cols = (max(rows, 0) + 15) / 16 * 16;
+    const int rows = u.rows(), cols = (rows + 15) / 16 * 16;
     float l[kCols];
 #pragma unroll
     for (int y = 0; y < kCols; ++y) l[y] = 0.f;
@@ -419,14 +414,14 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
       if (lane == 0) mbar_arrive(smem_addr(&c->q_free[q_buf]));
       ++rounds;
     }
-    if (x < 64) marks[x] = SV_NEG_INF;
+    if (x < kCols) marks[x] = SV_NEG_INF;
     const unsigned long long f2 = f2_pack(f, f);
     // keys that every row sees; past them row y sees a key from (key - common) G on
     const int common = u.units.row.L - u.units.row.n + u.first(0);
 #pragma unroll 1
     for (int i = 0; i < n; ++i, ++g) {
       const int buf = g % 2, key0 = (u.j0 + i) * S::kKeys;
-      const int from = max(0, key0 + my_key - common) * a.G - group * kCols;   // the first row that sees the key
+      const int from = max(0, key0 + my_key - common) * a.G;   // the first row that sees the key
       const bool masked = key0 + S::kKeys - 1 > common;
       ok = ok && mbar_await(smem_addr(&c->s_full[buf]), (g / 2) & 1, &c->abort_word, naps_of(a));
       tc_fence_after();
@@ -483,11 +478,11 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
             const float top = redux_max(__uint_as_float(s[y]));
             if (lane == y) mine = top;
           }
-          if (lane < kChunk) tops[warp * 64 + y0 + lane] = mine;
+          if (lane < kChunk) tops[warp * kCols + y0 + lane] = mine;
         }
         (void)vote_any(id, false);
         if (x < cols) {
-          const float high = fmaxf(fmaxf(tops[x], tops[64 + x]), fmaxf(tops[128 + x], tops[192 + x])) * f;
+          const float high = fmaxf(fmaxf(tops[x], tops[kCols + x]), fmaxf(tops[2 * kCols + x], tops[3 * kCols + x])) * f;
           const float old = marks[x];
           const bool up = i == 0 ? high > old : high > old + kSlack;
           const float now = up ? high : old;
@@ -556,7 +551,7 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
     for (int y0 = 0; y0 < kCols; y0 += kChunk)
       if (y0 < cols) {
         const float sum = warp_sums<kChunk>(l + y0);
-        if (lane < kChunk) tops[warp * 64 + y0 + lane] = sum;
+        if (lane < kChunk) tops[warp * kCols + y0 + lane] = sum;
       }
     if (!vote_all(id, ok)) return;
     const bool whole = u.j0 == 0 && u.j1 == u.tiles;
@@ -567,16 +562,15 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
     const size_t slots = (size_t)gridDim.x * 2;
     const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
     const long long out_rows = (long long)a.T * a.Hq, part_rows = min((long long)slots * S::kRows, kAttnRows);
-    const int r0 = group * kCols;
     const int token0 = u.units.row.begin + u.first(0);
     if (x < rows) {
-      const float sum = tops[x] + tops[64 + x] + tops[128 + x] + tops[192 + x], mark = marks[x];
+      const float sum = tops[x] + tops[kCols + x] + tops[2 * kCols + x] + tops[3 * kCols + x], mark = marks[x];
       factors[x] = whole ? row_inverse(sum) * a.v_gain : a.v_gain;
       if (whole) {
-        const long long row = (long long)(token0 + (r0 + x) / a.G) * a.Hq + u.h * a.G + (r0 + x) % a.G;
+        const long long row = (long long)(token0 + x / a.G) * a.Hq + u.h * a.G + x % a.G;
         if (a.lse && in_array(a.flags, row, out_rows)) a.lse[row] = row_lse(mark, sum);
       } else {
-        const long long row = (long long)slot * S::kRows + r0 + x;
+        const long long row = (long long)slot * S::kRows + x;
         if (in_array(a.flags, row, part_rows))
           ((float2*)(a.partial + slots * S::kRows * kD))[row] = make_float2(mark, sum);
       }
@@ -605,10 +599,10 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
           const int r = y0 + y + upper;
           if (r >= rows) continue;
           if (whole) {
-            const long long row = (long long)(token0 + (r0 + r) / a.G) * a.Hq + u.h * a.G + (r0 + r) % a.G;
+            const long long row = (long long)(token0 + r / a.G) * a.Hq + u.h * a.G + r % a.G;
             if (in_array(a.flags, row, out_rows)) *(uint32_t*)(a.out + (row * kD + column) * 2) = pack2(lo, hi, E());
           } else {
-            const long long row = (long long)slot * S::kRows + r0 + r;
+            const long long row = (long long)slot * S::kRows + r;
             if (in_array(a.flags, row, part_rows)) *(float2*)(a.partial + row * kD + column) = make_float2(lo, hi);
           }
         }
@@ -680,19 +674,18 @@ __global__ void __launch_bounds__(Fp4Shape<kD, kRows>::kThreads, Fp4Shape<kD, kR
   const uint32_t tmem = c->tmem;
   if (range.w0 < range.w1) {
     const AttnWalk<S> u(a, c->start, range.w1 - range.w0);
-    // Registers: 80 + 2 x 64 + 48 = 4 x 64 of two CTAs per SM, 2 x 152 + 2 x 64 + 48 = 5 x 96
-    // of five warpgroups; four of one CTA have 128 a thread.
-    constexpr bool kFew = S::kCtasPerSm > 1, kMany = S::kGroups > 1;
+    // Launched with 64 registers a thread in four warpgroups; 16 rows 80 + 2 x 64 + 48,
+    // 32 rows 96 + 2 x 56 + 48.
     if (warp < kKeyWarps) {
-      if (kMany) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-      if (kFew) asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+      if (kRows == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 80;");
+      else asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
       fp4_softmax<E, kD, S>(a, u, c, tmem, p_ptr, stats, range.quota, range.w1);
     } else if (warp < kLoader) {
-      if (kMany) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+      if (kRows > 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
       if (warp < kValueWarps) fp4_keys<kD, S>(a, u, c, ring, tmem);
       else fp4_values<kD, S>(a, u, c, ring, tmem, value_scales);
     } else {
-      if (kMany || kFew) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
       if (warp == kLoader) fp4_load<kD, S>(a, u, c, c->full, c->empty, ring, &k_map, &v_map, true, false);
       else if (warp == kLoader + 1) fp4_multiply<kD, S>(a, u, c, smem_addr(q_ptr), smem_addr(p_ptr), tmem);
       else if (warp == kLoader + 2) fp4_load<kD, S>(a, u, c, c->full, c->empty, ring, &k_map, &v_map, false, true);
