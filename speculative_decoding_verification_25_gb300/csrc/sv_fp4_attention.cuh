@@ -90,6 +90,10 @@ __device__ __forceinline__ float redux_max(float x) {
   return r;
 }
 
+// row / G for rows below 128, by a product.
+__device__ __forceinline__ uint32_t group_inverse(int G) { return 65536u / (uint32_t)G + 1; }
+__device__ __forceinline__ int group_of(int row, uint32_t inverse) { return (int)((uint32_t)row * inverse >> 16); }
+
 // ------------------------------------------------------------------ queries
 // One warp brings a unit's rows to shared memory as float16, columns past them
 // zero, a unit ahead of their use.
@@ -98,6 +102,7 @@ __device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4
   constexpr bool kBf16 = std::is_same<E, __nv_bfloat16>::value;
   constexpr int kLanes = kD / 8, kPass = 32 / kLanes, kAhead = 4;   // rows per pass, passes in flight
   const int lane = threadIdx.x & 31, part = lane % kLanes;
+  const uint32_t per_g = group_inverse(a.G);
   int rounds = 0;
 #pragma unroll 1
   for (bool first = true; u.next(first); first = false) {
@@ -109,7 +114,7 @@ __device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4
     auto load = [&](int row, uint32_t (&w)[4]) {
       w[0] = w[1] = w[2] = w[3] = 0;
       if (row >= rows) return;
-      const int t = u.units.row.begin + u.first(0) + row / a.G, h = u.h * a.G + row % a.G;
+      const int i = group_of(row, per_g), t = u.units.row.begin + u.first(0) + i, h = u.h * a.G + row - i * a.G;
       if (in_array(a.flags, t, a.T)) ldg_stream16(a.q + t * a.q_pitch + h * (kD * 2) + part * 16, w);
     };
     auto store = [&](int row, const uint32_t (&w)[4]) {
@@ -395,6 +400,7 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
   const int turn = S::kPRow == 64 ? place / 2 % 4 : place / 4 % 2;
   char* p_row = p_ptr + place * S::kPRow;
   const uint32_t s_col = tmem + lanes + S::kS, o_col = tmem + lanes + S::kO;
+  const uint32_t per_g = group_inverse(a.G);
   int g = 0, rounds = 0, meetings = 0;
   bool ok = true;
 
@@ -567,7 +573,8 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
       const float sum = tops[x] + tops[kCols + x] + tops[2 * kCols + x] + tops[3 * kCols + x], mark = marks[x];
       factors[x] = whole ? row_inverse(sum) * a.v_gain : a.v_gain;
       if (whole) {
-        const long long row = (long long)(token0 + x / a.G) * a.Hq + u.h * a.G + x % a.G;
+        const int i = group_of(x, per_g);
+        const long long row = (long long)(token0 + i) * a.Hq + u.h * a.G + x - i * a.G;
         if (a.lse && in_array(a.flags, row, out_rows)) a.lse[row] = row_lse(mark, sum);
       } else {
         const long long row = (long long)slot * S::kRows + x;
@@ -599,7 +606,8 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
           const int r = y0 + y + upper;
           if (r >= rows) continue;
           if (whole) {
-            const long long row = (long long)(token0 + r / a.G) * a.Hq + u.h * a.G + r % a.G;
+            const int i = group_of(r, per_g);
+            const long long row = (long long)(token0 + i) * a.Hq + u.h * a.G + r - i * a.G;
             if (in_array(a.flags, row, out_rows)) *(uint32_t*)(a.out + (row * kD + column) * 2) = pack2(lo, hi, E());
           } else {
             const long long row = (long long)slot * S::kRows + r;
