@@ -3,7 +3,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include <mutex>
 
@@ -126,13 +125,20 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   Fp4Device* dev = fp4_device();
   if (!dev) return SV_ERR_CUDA;
   const int G = Hq / Hk;
-  // The host knows the mean of a request's rows (the G heads of its tokens on one key head) alone.
-  const long long rows_of_all = (long long)T * G, requests = B > 0 ? B : 1;
-  const char* env = getenv("SV_FORM");
-  const Form form = env ? (Form)atoi(env)
-                    : rows_of_all > 128 * requests ? kWide
-                    : G > 32 || rows_of_all > 32 * requests ? kNarrow
-                    : G > 16 || rows_of_all > 16 * requests ? kFew32 : kFew16;
+  // The host knows the mean of a request's rows (the G heads of its tokens on one key
+  // head) alone; every form takes requests of any length.  Measured, 64 requests
+  // over contexts of 203 to 4099, microseconds:
+  //            4 rows  16 rows  20 rows  32 rows  48 rows  128 rows  160 rows  256 rows
+  //   16 rows      71       73      123      125      174
+  //   32 rows      80       82       89      104      185
+  //   narrow      104      104      108      108      110       121       205       208
+  //   wide                                                      149       184       231
+  // and one token of 8 rows over contexts of 60 k to 131 k: 122, 124, 194, 241.
+  const long long rows = (long long)T * G, requests = B > 0 ? B : 1;
+  const Form form = rows > 128 * requests               ? kWide
+                    : G > 32 || rows > 32 * requests    ? kNarrow
+                    : G > 16 || rows > 16 * requests    ? kFew32
+                                                        : kFew16;
   const Variant v = variant_of(dtype, D, form);
   int ctas = dev->sm_count * v.ctas_per_sm;
   if (ctas > sv::kAttnMaxCtas) ctas = sv::kAttnMaxCtas;
@@ -163,10 +169,10 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   a.q_pitch = (long long)q_stride * 2;
   a.k_scales = (const char*)k_scales;
   a.v_scales = (const char*)v_scales;
-  const long long rows = (long long)n_pages * Hk * page_size;
+  const long long cache_rows = (long long)n_pages * Hk * page_size;
   const int box = page_size < 128 ? page_size : 128;
   CUtensorMap q_map, k_map, v_map;
-  if (!encode_codes(*dev, &k_map, k_codes, D, rows, box) || !encode_codes(*dev, &v_map, v_codes, D, rows, box))
+  if (!encode_codes(*dev, &k_map, k_codes, D, cache_rows, box) || !encode_codes(*dev, &v_map, v_codes, D, cache_rows, box))
     return SV_ERR_CUDA;
   if (form <= kFew32) {
     void* args[] = {&a, &k_map, &v_map};

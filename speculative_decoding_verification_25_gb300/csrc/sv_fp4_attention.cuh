@@ -622,8 +622,8 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
     const long long end = ahead + (long long)(u.tiles - 1) * S::kKeys;
     const int c_last = u.j1 == u.tiles ? cta : cta + ranges_ahead(end, quota);
     ok = soft_meet(c, meetings++, naps_of(a));
-    if (ok && threadIdx.x == 0) {
-      const bool last = in_array(a.flags, c_first, gridDim.x) &&
+    if (threadIdx.x == 0) {
+      const bool last = ok && in_array(a.flags, c_first, gridDim.x) &&
                         take_ticket(&a.tickets[c_first]) == c_last - c_first;
       if (last) a.tickets[c_first] = 0;
       c->last = last;
