@@ -609,26 +609,28 @@ def _append_inputs(q, k_new, v_new, positions, cos_sin, slot_map, q_out, dtype, 
     else:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [max_positions, rotary_dim]")
-        _check(cos_sin, "cos_sin", dtype=torch.float32, device=dev)
+        if not (cos_sin.dtype is torch.float32 and cos_sin.device == dev and cos_sin.is_cuda and cos_sin.is_contiguous()):
+            _check(cos_sin, "cos_sin", dtype=torch.float32, device=dev)   # says what is wrong
         table = (_ints(positions, "positions", (T,), dev), cos_sin.data_ptr(), *cos_sin.shape)
-    k_stride = _check_packed(k_new, "k_new", dtype, (T, Hk, D), dev)
-    v_stride = _check_packed(v_new, "v_new", dtype, (T, Hk, D), dev)
-    queries, results = (None, 0), (None, 0)
-    Hq = 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
-        Hq = q.shape[1]
-        queries = (q, _check_packed(q, "q", dtype, (T, Hq, D), dev))
-        if q_out is None:
-            with _on(stream):   # outputs belong to the stream that writes them
-                q_out = torch.empty(T, Hq, D, dtype=dtype, device=dev)
-        results = (q_out, _check_packed(q_out, "q_out", dtype, (T, Hq, D), dev))
-    elif q_out is not None:
-        raise ValueError("q_out needs q")
-    address = lambda t: None if t is None else t.data_ptr()
-    ins = (address(queries[0]), queries[1], k_new.data_ptr(), k_stride, v_new.data_ptr(), v_stride, *table)
-    return ins, _ints(slot_map, "slot_map", (T,), dev), T, Hq, (address(results[0]), results[1]), q_out
+    ins = (k_new.data_ptr(), _check_packed(k_new, "k_new", dtype, (T, Hk, D), dev),
+           v_new.data_ptr(), _check_packed(v_new, "v_new", dtype, (T, Hk, D), dev), *table)
+    slots = _ints(slot_map, "slot_map", (T,), dev)
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out needs q")
+        return (None, 0, *ins), slots, T, 0, (None, 0), None
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
+    Hq = q.shape[1]
+    shape = (T, Hq, D)
+    stride = _check_packed(q, "q", dtype, shape, dev)
+    if q_out is None:
+        with _on(stream):   # outputs belong to the stream that writes them
+            q_out = torch.empty(shape, dtype=dtype, device=dev)
+        out_stride = Hq * D
+    else:
+        out_stride = _check_packed(q_out, "q_out", dtype, shape, dev)
+    return (q.data_ptr(), stride, *ins), slots, T, Hq, (q_out.data_ptr(), out_stride), q_out
 
 
 def paged_append_rotary(q: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor,
