@@ -5,6 +5,12 @@
 //
 // Operands are float16 as in sv_fp4_attention.cuh: bfloat16 queries are
 // converted in shared memory, each query tile with a power of two of its own.
+//
+// Bound by a tile's chain.  Narrow, 256 x 9 tokens over 2 k to 10 k keys, 64/8
+// heads of 128: 861 us for 1.87 GB, about 2650 clocks per tile of 128 keys, of
+// which each half's unpacking takes 700 (transposed as in sv_fp4_attention.cuh
+// 1726 us).  Wide, 2 x 2048 tokens over 5 k to 7 k: 387 us, 1.2 PFLOP/s, beside 310 of
+// 16 bits: the unpacking shares the schedulers with the softmax.
 #pragma once
 
 #include "sv_fp4_load.cuh"
@@ -17,7 +23,7 @@ template <int kD, bool kWide>
 struct Fp4RowsShape : AttnShape<kD, true> {
   using Base = AttnShape<kD, true>;
   static constexpr bool kFp4 = true;
-  // wide: a fourth unpacked tile in place of the staging (prompt chunks 445 and 396 us)
+  // wide: a fourth unpacked tile in place of the staging (prompt chunks 446 and 392 us)
   static constexpr bool kStaged = !kWide;
   static constexpr int kChunk = kWide ? 128 : 64;
   static constexpr int kStagingBytes = kWide ? 64 : Base::kStagingBytes;
