@@ -72,6 +72,7 @@ struct Fp4Control {
   unsigned status;
   int q_exponent[2];
   AttnStart start;
+  long long sums[20];
 };
 static_assert(sizeof(Fp4Control) <= 1024, "fits kControlBytes");
 

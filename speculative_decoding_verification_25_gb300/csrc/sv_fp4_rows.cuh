@@ -54,6 +54,7 @@ struct Fp4RowsControl {   // as AttnControl, and:
   unsigned status;
   int q_exponent[2][2];       // [unit % 2][query tile]
   AttnStart start;
+  long long sums[16];
 };
 static_assert(sizeof(Fp4RowsControl) <= 1024, "fits kControlBytes");
 
