@@ -129,11 +129,11 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   // head) alone; every form takes requests of any length.  Measured, 64 requests
   // over contexts of 203 to 4099, microseconds:
   //            4 rows  16 rows  20 rows  32 rows  48 rows  128 rows  160 rows  256 rows
-  //   16 rows      71       73      123      125      174
-  //   32 rows      80       82       89      104      185
-  //   narrow      104      104      108      108      110       121       205       208
+  //   16 rows      73       74      123      125      174
+  //   32 rows      80       82       90       91      185
+  //   narrow       98      100      102      102      106       116       195       202
   //   wide                                                      149       184       231
-  // and one token of 8 rows over contexts of 60 k to 131 k: 122, 124, 194, 241.
+  // and one token of 8 rows over contexts of 60 k to 131 k: 120, 124, 175, 241.
   const long long rows = (long long)T * G, requests = B > 0 ? B : 1;
   const Form form = rows > 128 * requests               ? kWide
                     : G > 32 || rows > 32 * requests    ? kNarrow

@@ -7,9 +7,10 @@
 // converted in shared memory, each query tile with a power of two of its own.
 //
 // Bound by a tile's chain.  Narrow, 256 x 9 tokens over 2 k to 10 k keys, 64/8
-// heads of 128: 861 us for 1.87 GB, about 2650 clocks per tile of 128 keys, of
-// which each half's unpacking takes 700 (transposed as in sv_fp4_attention.cuh
-// 1726 us).  Wide, 2 x 2048 tokens over 5 k to 7 k: 387 us, 1.2 PFLOP/s, beside 310 of
+// heads of 128: 780 us for 1.87 GB, about 2400 clocks per tile of 128 keys: 1716 of
+// them are waits and handing over (measured without unpacking, exponentials and all
+// but one step of each product), the rest is what unpacking and softmax add
+// (transposed as in sv_fp4_attention.cuh 1726 us).  Wide, 2 x 2048 tokens over 5 k to 7 k: 387 us, 1.2 PFLOP/s, beside 310 of
 // 16 bits: the unpacking shares the schedulers with the softmax.
 #pragma once
 
@@ -26,6 +27,9 @@ struct Fp4RowsShape : AttnShape<kD, true> {
   // wide: a fourth unpacked tile in place of the staging (prompt chunks 446 and 392 us)
   static constexpr bool kStaged = !kWide;
   static constexpr int kChunk = kWide ? 128 : 64;
+  // the unpacking's loads a step ahead: narrow 816 and 780 us (256 x 9 tokens); wide the
+  // softmax of two tiles is the longer, and loses what it gains: chunks 392 and 404
+  static constexpr bool kAhead = !kWide;
   static constexpr int kStagingBytes = kWide ? 64 : Base::kStagingBytes;
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kBufs = kWide ? 1 : 2;
@@ -145,7 +149,7 @@ __device__ __forceinline__ void fp4_rows_queries(const Fp4Args& a, AttnWalk<S> u
 // Four warps unpack, a key per thread, in the order in which the products take tiles:
 // kBufs tiles of keys, then values and keys in turn.  The two rings need not keep
 // step: keys have the packed one's even places, values the odd.  (A group of four
-// warps each for keys and values is slower: 64 x 5 tokens 118 and 133 us.)
+// warps each for keys and values is slower: 256 x 9 tokens 816 and 843 us.)
 template <int kD, typename S>
 __device__ __forceinline__ void fp4_rows_unpack(const Fp4Args& a, AttnWalk<S> u, Fp4RowsControl* c,
                                                 const char* packed, char* ring) {
@@ -154,19 +158,29 @@ __device__ __forceinline__ void fp4_rows_unpack(const Fp4Args& a, AttnWalk<S> u,
   auto unpack = [&](int tile, bool values) -> bool {
     const int from = 2 * (done + tile) + values, slot = from % S::kPackedStages;
     const int stage = it % S::kStages, lap = it / S::kStages;
-    if (!mbar_await(smem_addr(&c->packed_full[slot]), (from / S::kPackedStages) & 1, &c->abort_word, naps_of(a)) ||
-        (lap > 0 && !mbar_await(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, naps_of(a))))
+    if (!mbar_await(smem_addr(&c->packed_full[slot]), (from / S::kPackedStages) & 1, &c->abort_word, naps_of(a)))
       return false;
     const char* codes = packed + slot * Fp4Tile<kD>::kBytes;
     const char* scales = codes + Fp4Tile<kD>::kCodeBytes + key * (kD / 16);
+    auto load = [&](int p) { return *(const uint4*)(codes + fp4_piece<kD>(key, p)); };
+    uint4 w4;
+    uint2 bytes;
+    if (S::kAhead) {
+      w4 = load(0);
+      bytes = kD == 128 ? *(const uint2*)scales : make_uint2(*(const uint32_t*)scales, 0);
+    }
+    if (lap > 0 && !mbar_await(smem_addr(&c->empty[stage]), (lap - 1) & 1, &c->abort_word, naps_of(a))) return false;
     char* to = ring + stage * S::kStageBytes + key * 128;
     // rolled up as in fp4_keys
-#pragma unroll 1
+#pragma unroll(S::kAhead ? 2 : 1)
     for (int p = 0; p < kD / 32; ++p) {
-      const uint4 w4 = *(const uint4*)(codes + fp4_piece<kD>(key, p));
-      const uint32_t pair = fp4_scales(*(const uint16_t*)(scales + p * 2));
+      if (!S::kAhead) w4 = load(p);
+      const uint32_t pair = fp4_scales(S::kAhead ? bytes.x & 0xffff : *(const uint16_t*)(scales + p * 2));
+      bytes.x = __funnelshift_r(bytes.x, bytes.y, 16);
+      bytes.y >>= 16;
       const uint32_t s[2] = {__byte_perm(pair, 0, 0x1010), __byte_perm(pair, 0, 0x3232)};
       const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+      if (S::kAhead && p + 1 < kD / 32) w4 = load(p + 1);
       char* block = to + (p / 2) * (S::kKeys * 128);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -197,6 +211,87 @@ __device__ __forceinline__ void fp4_rows_unpack(const Fp4Args& a, AttnWalk<S> u,
     }
     done += n;
   }
+}
+
+// The narrow form's products, one warp: attn_multiply for one query tile, with as
+// little between the products as can be, and P handed over before the last
+// product is done (256 x 9 tokens 871 and 816 us).
+template <int kD, typename S>
+__device__ __forceinline__ void fp4_rows_multiply(const Fp4Args& a, AttnWalk<S> u, Fp4RowsControl* c,
+                                                  uint32_t q_smem, uint32_t ring, char* ring_ptr, uint32_t tmem) {
+  constexpr uint32_t s_desc = mma_desc(false, 128, S::kKeys, false);
+  constexpr uint32_t o_desc = mma_desc(false, 128, kD, true);
+  const int lane = threadIdx.x & 31;
+  const uint64_t q_desc = tile_desc(q_smem, 16, 1024);
+  const uint64_t k_desc = tile_desc(ring, 16, 1024);
+  const uint64_t v_desc = tile_desc(ring, S::kKeys * 128, 1024);
+  const uint32_t o = tmem + S::kBufs * S::kKeys;
+  int it = 0, rounds = 0, k = 0;   // unpacked tiles, units, tiles of S whose values are next
+  bool ok = true;
+  auto arrived = [&](int i) {
+    const bool there = mbar_await(smem_addr(&c->full[i % S::kStages]), (i / S::kStages) & 1, &c->abort_word, naps_of(a));
+    tc_fence_after();
+    return there;
+  };
+  auto scores = [&](int tile, int i, bool last) {
+    const uint64_t from = k_desc + i % S::kStages * (S::kStageBytes / 16);
+    if (elect_one()) {
+#pragma unroll
+      for (int d = 0; d < kD / 16; ++d)
+        mma_smem_one(tmem + tile % S::kBufs * S::kKeys, q_desc + (d / 4) * (128 * 128 / 16) + (d % 4) * 2,
+                     from + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0);
+      tc_commit_one(smem_addr(&c->s_full[0][tile % S::kBufs]));
+      tc_commit_one(smem_addr(&c->empty[i % S::kStages]));
+      if (last) tc_commit_one(smem_addr(&c->q_empty));
+    }
+    __syncwarp();
+  };
+#pragma unroll 1
+  for (bool first = true; ok && u.next(first); first = false) {
+    const int n = u.count(0);
+    if (n == 0) continue;
+    if (!(ok = mbar_await(smem_addr(&c->q_full), rounds++ & 1, &c->abort_word, naps_of(a)))) break;
+#pragma unroll 1
+    for (int i = 0; i < min(n, S::kBufs); ++i, ++it) {
+      if (!(ok = arrived(it))) break;
+      scores(k + i, it, i + 1 == n);
+    }
+#pragma unroll 1
+    for (int i = 0; ok && i < n; ++i, ++k) {
+      const int stage = it % S::kStages;
+      if (!(ok = arrived(it++))) break;
+      const int valid = u.units.row.L - (u.j0 + i) * S::kKeys;
+      if (valid < S::kKeys) {   // values past the request's length: 0 * NaN is NaN
+        char* v0 = ring_ptr + stage * S::kStageBytes;
+        const int pieces = (S::kKeys - valid) * 8;
+#pragma unroll 1
+        for (int x = lane; x < pieces * S::kBlocks; x += 32)
+          *(uint4*)(v0 + ((x / pieces) * S::kKeys + valid) * 128 + (x % pieces) * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_shared();
+        __syncwarp();
+      }
+      if (!(ok = mbar_await(smem_addr(&c->p_ready[0][k % S::kBufs]), (k / S::kBufs) & 1, &c->abort_word, naps_of(a))))
+        break;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t from = v_desc + stage * (S::kStageBytes / 16);
+#pragma unroll
+        for (int x = 0; x < S::kKeys / 16; ++x)
+          mma_tmem_one(o, tmem + k % S::kBufs * S::kKeys + x * 8, from + x * (16 * 128 / 16), o_desc, i > 0 || x > 0);
+        tc_commit_one(smem_addr(&c->pv_done[k % 2]));
+        tc_commit_one(smem_addr(&c->empty[stage]));
+      }
+      __syncwarp();
+      if (i + S::kBufs < n) {
+        if (!(ok = arrived(it))) break;
+        scores(k + S::kBufs, it++, i + S::kBufs + 1 == n);
+      }
+    }
+  }
+  // everything issued is done before the CTA's memory goes
+  if (elect_one()) tc_commit_one(smem_addr(&c->drain));
+  (void)mbar_poll(smem_addr(&c->drain), 0, &c->calm, kNaps);
+  __syncwarp();
 }
 
 template <typename E, int kD, bool kWide>
@@ -236,8 +331,9 @@ __global__ void __launch_bounds__(Fp4RowsShape<kD, kWide>::kThreads, Fp4RowsShap
         mbar_init(smem_addr(&c->s_full[t][k]), 1);
         mbar_init(smem_addr(&c->p_ready[t][k]), S::kTiles > 1 ? 5 : 4);   // with the turn
       }
-      mbar_init(smem_addr(&c->pv_done[t]), 1);
     }
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) mbar_init(smem_addr(&c->pv_done[t]), 1);
     mbar_init_fence();
     c->abort_word = c->calm = c->past = 0;
     tma_prefetch_map(&q_map);
@@ -260,7 +356,9 @@ __global__ void __launch_bounds__(Fp4RowsShape<kD, kWide>::kThreads, Fp4RowsShap
       if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
       else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
       // narrow: a loader each for keys and values
-      if (warp >= kIssuer && warp < kIssuer + S::kTiles)
+      if (!kWide && warp == kIssuer)
+        fp4_rows_multiply<kD, S>(a, u, c, smem_addr(smem), smem_addr(ring), ring, tmem);
+      else if (kWide && warp >= kIssuer && warp < kIssuer + S::kTiles)
         attn_multiply<__half, kD, S>(a, u, c, smem_addr(smem), smem_addr(ring), ring, tmem, warp - kIssuer);
       else if (warp == kQueries)
         fp4_rows_queries<E, kD, S>(a, u, c, smem, &q_map);

@@ -755,6 +755,15 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
   int meetings = 0, rounds = 0, units = 0;
   float scale = a.scale_log2;
   bool ok = true;
+  // Whether O += P V of tile k is done.  A wait sees a phase's parity alone, so that
+  // on one barrier at most one product may be open (with two S buffers the scores
+  // do not tell that the last one is done); two barriers in turn may have two.
+  constexpr bool kInTurn = S::kFp4 && S::kBufs > 1;
+  auto wait = [&](uint64_t* bar, int phase) {
+    return kInTurn ? mbar_await(smem_addr(bar), phase & 1, &c->abort_word, naps_of(a))
+                   : mbar_wait(smem_addr(bar), phase & 1, &c->abort_word, naps_of(a));
+  };
+  auto products = [&](int k) { return wait(&c->pv_done[kInTurn ? k % 2 : t], kInTurn ? k / 2 : k); };
 #pragma unroll 1
   for (bool first = true; ok && u.next(first); first = false) {
     const int n = u.count(t);
@@ -772,19 +781,12 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
 #pragma unroll 1
     for (int i = 0; i < n; ++i, key0 += S::kKeys) {
       const int k = done + i, buf = k % S::kBufs;
-      if (!(ok = mbar_wait(smem_addr(&c->s_full[t][buf]), (k / S::kBufs) & 1, &c->abort_word,
-                           naps_of(a))))
-        break;
+      if (!(ok = wait(&c->s_full[t][buf], k / S::kBufs))) break;
       tc_fence_after();
       if constexpr (S::kFp4)
         if (i == 0) scale = ldexpf(a.scale_log2, c->q_exponent[units % 2][t]);
-      // With two S buffers the scores do not tell that the last O += P V is
-      // done; the wait keeps at most one of them open, as a wait that sees a
-      // phase's parity alone needs.
       auto give = [&]() -> bool {
-        if (S::kBufs > 1 && i > 0 &&
-            !mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word, naps_of(a)))
-          return false;
+        if (S::kBufs > 1 && !kInTurn && i > 0 && !products(k - 1)) return false;
         hand_over(&c->p_ready[t][buf]);
         return true;
       };
@@ -825,9 +827,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
           l *= f;
           if (i > 0) {   // what was summed before, once the products are done
             if (S::kBufs > 1) {
-              if (!(ok = mbar_wait(smem_addr(&c->pv_done[t]), (k - 1) & 1, &c->abort_word,
-                                   naps_of(a))))
-                break;
+              if (!(ok = products(k - 1))) break;
               tc_fence_after();
             }
 #pragma unroll 1
@@ -900,8 +900,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
     units += S::kFp4 && u.most() > 0;
     // one S buffer: one arrival per unit, else one per tile
     if (n > 0)
-      ok = mbar_wait(smem_addr(&c->pv_done[t]), (S::kBufs > 1 ? done - 1 : rounds++) & 1,
-                     &c->abort_word, naps_of(a));
+      ok = products(S::kBufs > 1 ? done - 1 : rounds++);
     if (!ok) break;
     tc_fence_after();
     // A unit that is all this CTA's is written out; a part of one goes to the
