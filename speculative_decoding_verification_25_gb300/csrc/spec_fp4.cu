@@ -132,7 +132,7 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   //   16 rows      73       74      123      125      174
   //   32 rows      80       82       90       91      185
   //   narrow       98      100      102      102      106       116       195       202
-  //   wide                                                      149       184       231
+  //   wide                                                      149       177       231
   // and one token of 8 rows over contexts of 60 k to 131 k: 120, 124, 175, 241.
   const long long rows = (long long)T * G, requests = B > 0 ? B : 1;
   const Form form = rows > 128 * requests               ? kWide

@@ -10,8 +10,9 @@
 // heads of 128: 780 us for 1.87 GB, about 2400 clocks per tile of 128 keys: 1716 of
 // them are waits and handing over (measured without unpacking, exponentials and all
 // but one step of each product), the rest is what unpacking and softmax add
-// (transposed as in sv_fp4_attention.cuh 1726 us).  Wide, 2 x 2048 tokens over 5 k to 7 k: 387 us, 1.2 PFLOP/s, beside 310 of
-// 16 bits: the unpacking shares the schedulers with the softmax.
+// (transposed as in sv_fp4_attention.cuh 1726 us).  Wide, 2 x 2048 tokens over 5 k
+// to 7 k: 375 us, 1.26 PFLOP/s, beside 310 of 16 bits: the unpacking shares the
+// schedulers with the softmax.
 #pragma once
 
 #include "sv_fp4_load.cuh"
@@ -346,14 +347,14 @@ __global__ void __launch_bounds__(Fp4RowsShape<kD, kWide>::kThreads, Fp4RowsShap
   const uint32_t tmem = c->tmem;
   if (range.w0 < range.w1) {
     const AttnWalk<S> u(a, c->start, range.w1 - range.w0);
-    // Wide: launched with 128 registers a thread, and 2 x 184 + 72 + 72 = 4 x 128;
-    // narrow: 168, and 232 + 2 x 136 = 3 x 168.
+    // Wide: launched with 128 registers a thread, and 2 x 176 + 80 + 80 = 4 x 128 (chunks 375
+    // us; 184 and 72: 385, 168 and 88: 404); narrow: 168, and 232 + 2 x 136 = 3 x 168.
     if (warp >= kUnpack) {
-      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
       fp4_rows_unpack<kD, S>(a, u, c, packed, ring);
     } else if (warp >= kQueries) {
-      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      if (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       else asm volatile("setmaxnreg.dec.sync.aligned.u32 136;");
       // narrow: a loader each for keys and values
       if (!kWide && warp == kIssuer)
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(Fp4RowsShape<kD, kWide>::kThreads, Fp4RowsShap
         fp4_load<kD, S>(a, u, c, c->packed_full, c->packed_empty, packed, &k_map, &v_map, warp == kLoader,
                         kWide || warp != kLoader);
     } else {
-      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+      if (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
       else asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
       attn_softmax<__half, E, kD, S>(a, u, c, tmem, staging, range.quota, range.w1);
     }

@@ -477,6 +477,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
                        k0 + (d / 4) * (S::kKeys * 128 / 16) + (d % 4) * 2, s_desc, d > 0);
         }
         tc_commit_one(smem_addr(&c->s_full[t][k % S::kBufs]));
+        tc_commit_one(smem_addr(&c->empty[stage]));
       }
       __syncwarp();
     } else {
@@ -515,7 +516,7 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       if (!(ok = wait_stage(it))) break;
       tc_fence_after();
       if (i < cnt) scores(done + i, it % S::kStages, false);
-      release(&c->empty[it % S::kStages], i < cnt);
+      if (!S::kFp4 || i >= cnt) release(&c->empty[it % S::kStages], i < cnt);
       ++it;
     }
     if (ok && cnt <= S::kBufs) release(&c->q_empty, cnt > 0);   // its last scores are issued
@@ -561,6 +562,9 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
 #pragma unroll
             for (int x = 0; x < S::kKeys / 16; ++x)
               mma_tmem_one(o, s_col(k) + x * 8, v0 + x * (16 * 128 / 16), o_desc, i > 0 || x > 0);
+            // now, not after the scores: the unpacking has the slot sooner (prompt chunks 388, not
+            // 392 us; a commit less between products 385)
+            tc_commit_one(smem_addr(&c->empty[v_it % S::kStages]));
           }
           __syncwarp();
         } else
@@ -576,8 +580,8 @@ __device__ __forceinline__ void attn_multiply(const AttnArgs& a, AttnWalk<S> u, 
       }
       if (next) scores(k + S::kBufs, k_it % S::kStages, pass);
       else if (S::kTiles > 1) pass_turn(pass);
-      release(&c->empty[v_it % S::kStages], active);
-      if (another) release(&c->empty[k_it % S::kStages], next);
+      if (!S::kFp4 || !active) release(&c->empty[v_it % S::kStages], active);
+      if (another && (!S::kFp4 || !next)) release(&c->empty[k_it % S::kStages], next);
       if (next && i + S::kBufs + 1 == cnt) release(&c->q_empty, true);
     }
     done += cnt;
