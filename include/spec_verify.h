@@ -597,8 +597,9 @@ int spec_paged_read_fp4(const void* k_codes, const void* k_scales, const void* v
  * spec_paged_attention over a 4-bit cache: the same tokens, masks, results and
  * arguments, its workspace (spec_paged_attention_workspace_bytes, which calls
  * of both kinds may share, one after the other) and its waits, with the cache in
- * four arrays, 16-byte aligned, and its gains.  scale * log2(e) * k_gain is a
- * normal float32 number.
+ * four arrays, 16-byte aligned, and its gains.  As there, a request's values may
+ * not be NaN where a token does not see them, its keys may.
+ * scale * log2(e) * k_gain is a normal float32 number.
  */
 int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_codes, const void* k_scales,
                              const void* v_codes, const void* v_scales, int dtype,
