@@ -191,8 +191,7 @@ def prepare(case, seed):
     g = _generator(seed)
     page, dt, Hq, Hk, D = case["page"], DTYPES[case["dtype"]], case["Hq"], case["Hk"], case["D"]
     if case["op"] != "attention4":
-        T, length, rot = case["T"], case["run"], case["rot"]
-        far = max(case["far"], length)   # the table reaches past every position
+        T, length, far, rot = case["T"], case["run"], case["far"], case["rot"]
         n_slots, each = _slots(case)
         n_pages = n_slots // page
         # the projection's output holds queries, keys and values of a token side by side
