@@ -599,7 +599,8 @@ int spec_paged_read_fp4(const void* k_codes, const void* k_scales, const void* v
  * of both kinds may share, one after the other) and its waits, with the cache in
  * four arrays, 16-byte aligned, and its gains.  As there, a request's values may
  * not be NaN where a token does not see them, its keys may.
- * scale * log2(e) * k_gain is a normal float32 number.
+ * scale * log2(e) * k_gain is a normal float32 number, and max_pages * page_size
+ * <= 2^31 - 1024.
  */
 int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_codes, const void* k_scales,
                              const void* v_codes, const void* v_scales, int dtype,

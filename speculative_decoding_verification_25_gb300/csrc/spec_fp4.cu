@@ -21,7 +21,16 @@ using sv::page_shift_of;
 
 using sv::EncodeTiled;
 using sv::kMaxDevices;
-using sv::kMostKeys;
+
+// Most keys of a request: the walk looks up to two key tiles past the last key, and a
+// unit's cost, which is higher here than over 16 bits, past its keys, in 32 bits.
+constexpr long long kMostFp4Keys = k2_31 - 1024;
+template <typename S>
+constexpr bool fits = S::kUnitCost + 2 * S::kKeys <= k2_31 - kMostFp4Keys && kMostFp4Keys % S::kKeys == 0;
+static_assert(fits<sv::Fp4Shape<64, 16>> && fits<sv::Fp4Shape<64, 32>> && fits<sv::Fp4Shape<128, 16>> &&
+                  fits<sv::Fp4Shape<128, 32>>, "fits");
+static_assert(fits<sv::Fp4RowsShape<64, false>> && fits<sv::Fp4RowsShape<64, true>> &&
+                  fits<sv::Fp4RowsShape<128, false>> && fits<sv::Fp4RowsShape<128, true>>, "fits");
 
 struct Fp4Device {
   std::once_flag once;
@@ -106,7 +115,7 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
   const int shift = page_shift_of(page_size);
   if (shift < 0 || B < 0 || T < 0 || Hk < 1 || Hq < Hk || Hq % Hk || Hq / Hk > 128 || Hq > 4096 ||
       (D != 64 && D != 128) || max_pages < 1 || n_pages < 1 ||
-      (long long)max_pages * page_size > kMostKeys ||
+      (long long)max_pages * page_size > kMostFp4Keys ||
       (long long)n_pages * page_size * Hk >= k2_31 || q_stride < (int64_t)Hq * D ||
       !(k_gain >= 1e-30f && k_gain <= 1e30f) || !(v_gain >= 1e-30f && v_gain <= 1e30f) ||
       !(scale > 0.f && (double)scale * sv::kLog2e * k_gain <= 3.4e38 &&

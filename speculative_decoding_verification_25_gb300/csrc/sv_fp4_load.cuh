@@ -51,8 +51,9 @@ __device__ __forceinline__ void fp4_load(const Fp4Args& a, AttnWalk<S> u, Contro
 
   // First row, in the cache, of the lane's page of key tile j; -1 if it has none.
   auto box_row = [&](int j) -> int {
+    if (lane >= boxes) return -1;
     const int key = j * S::kKeys + lane * box;
-    if (lane >= boxes || key >= u.units.row.L) return -1;
+    if (key >= u.units.row.L) return -1;
     const int pg = key >> a.page_shift;
     if (!in_array(a.flags, u.b, a.B) || !in_array(a.flags, pg, a.max_pages)) return -1;
     const int id = a.block_table[(long long)u.b * a.max_pages + pg];

@@ -13,8 +13,8 @@ namespace sv {
 
 constexpr int kMaxDevices = 64;
 constexpr long long k2_31 = 1ll << 31;
-// Most keys of a request: the attention's walk looks up to two key tiles (of
-// 128 at most) past the last key, and a unit's cost past its keys, in 32 bits.
+// Most keys of a request over 16 bits: the attention's walk looks up to two key tiles
+// (of 128 at most) past the last key, and a unit's cost past its keys, in 32 bits.
 constexpr long long kMostKeys = k2_31 - 512;
 
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);

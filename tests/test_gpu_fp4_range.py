@@ -1,0 +1,75 @@
+"""Attention over the 4-bit cache at the ends of its arguments' ranges: gains, scales
+and queries far from 1, rows whose probabilities differ by far, the longest context."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+from fp4_util import Fp4Case
+from oracle import paged as paged_oracle
+from oracle import paged_fp4 as oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+# new tokens of a request that take each form, with groups of 4
+FORMS = {"16": 3, "32": 7, "narrow": 20, "wide": 70}
+PAGE = 256
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    import torch
+    from speculative_decoding_verification_25_gb300 import build as b
+    b.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+
+
+def _shared(k, v, q, B, repeat=1, gains=(1.0, 1.0), scale=1.0, cut=0):
+    """B requests of the same queries [n, G, D] on one key head, whose cache is the pages
+    of k and v [L, D] `repeat` times, without the last `cut` keys."""
+    import torch
+    from speculative_decoding_verification_25_gb300 import api
+    (L, D), (n, G, _) = k.shape, q.shape
+    pages = L // PAGE
+    parts = []
+    for x, gain in ((k, gains[0]), (v, gains[1])):
+        codes, scales = oracle.encode(x.reshape(pages, 1, PAGE, D), gain)
+        parts += [torch.from_numpy(codes).to(DEV), torch.from_numpy(scales).to(DEV).view(torch.float8_e4m3fn)]
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).repeat(B, repeat)
+    length = torch.full((B,), L * repeat - cut, dtype=torch.int32, device=DEV)
+    queries = torch.from_numpy(q).to(torch.bfloat16).to(DEV).repeat(B, 1, 1)
+    cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device=DEV)
+    return api.paged_attention_fp4(queries, api.PagedCacheFp4(*parts), table, cu, length, scale=scale, k_gain=gains[0],
+                                   v_gain=gains[1], want_lse=True)
+
+
+def _bf16(x):
+    import torch
+    return torch.from_numpy(np.asarray(x, np.float64)).to(torch.bfloat16).double().numpy()
+
+
+@pytest.mark.parametrize("cut", [0, 5])
+@pytest.mark.parametrize("form", FORMS)
+def test_attention_over_the_most_keys(form, cut):
+    """2^31 - 1024 keys, the same pages over and over: each has its weight among the 1024."""
+    n, G, D, L, repeat = FORMS[form], 4, 64, 4 * PAGE, 2 ** 21 - 1
+    rng = np.random.default_rng(len(form))
+    k, v = rng.normal(size=(2, L, D))
+    q = _bf16(rng.normal(size=(n, G, D)) / 8)
+    r = _shared(k, v, q, 1, repeat=repeat, cut=cut)
+    k, v = (oracle.decode(*oracle.encode(x))[None, None] for x in (k, v))
+    # every token sees all of a period: as if the queries stood behind them
+    want = paged_oracle.attention(np.broadcast_to(q, (n, G, D)).reshape(1, n * G, D), k, v, np.zeros((1, 1), int), [0, 1], [L],
+                                  1.0, "f16")
+    out, lse = r.out.double().cpu().numpy().reshape(1, n * G, D), r.lse.double().cpu().numpy().reshape(1, n * G)
+    # Float32 sums of up to 2^31 / 152 keys, 16 at a time, which may truncate, and of as many
+    # parts as there are CTAs; up to n + cut of the 2^31 keys are not seen.  One rounding to bfloat16.
+    adds = (2.0 ** 31 / 152 / 16 + 320) * 2.0 ** -23
+    few = (n + cut) / 2.0 ** 31
+    weights = np.exp(q.reshape(n * G, D) @ k[0, 0].T)
+    spread = weights / weights.sum(-1, keepdims=True) @ np.abs(v[0, 0])
+    tol = want.out_tol + 2 * (adds + few * L) * spread + 2.0 ** -8 * np.abs(want.out)
+    assert (np.abs(out - want.out) <= tol).all()
+    assert (np.abs(lse - want.lse - math.log(repeat)) <= want.lse_tol + adds + few * L + 2.0 ** -20).all()
