@@ -42,17 +42,17 @@ Fp4Device g_fp4[kMaxDevices];
 
 struct Variant {
   const void* fn;
-  int threads, smem_bytes, ctas_per_sm, rows;   // rows of a unit, or of a query tile of the wide form
+  int threads, smem_bytes, ctas_per_sm, unit_rows, rows;   // rows: of a query tile
 };
 template <typename E, int kD, int kRows>
 Variant variant() {
   using S = sv::Fp4Shape<kD, kRows>;
-  return {(const void*)sv::sv_fp4_attention_kernel<E, kD, kRows>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, kRows};
+  return {(const void*)sv::sv_fp4_attention_kernel<E, kD, kRows>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, S::kRows, kRows};
 }
 template <typename E, int kD, bool kWide>
 Variant rows_variant() {
   using S = sv::Fp4RowsShape<kD, kWide>;
-  return {(const void*)sv::sv_fp4_rows_attention_kernel<E, kD, kWide>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, 128};
+  return {(const void*)sv::sv_fp4_rows_attention_kernel<E, kD, kWide>, S::kThreads, S::kSmemBytes, S::kCtasPerSm, S::kRows, 128};
 }
 enum Form { kFew16, kFew32, kNarrow, kWide, kForms };
 template <typename E, int kD>
@@ -149,8 +149,7 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
                     : G > 16 || rows > 16 * requests    ? kFew32
                                                         : kFew16;
   const Variant v = variant_of(dtype, D, form);
-  int ctas = dev->sm_count * v.ctas_per_sm;
-  if (ctas > sv::kAttnMaxCtas) ctas = sv::kAttnMaxCtas;
+  const int ctas = sv::range_ctas(dev->sm_count * v.ctas_per_sm, v.unit_rows);
 
   sv::Fp4Args a;
   a.block_table = block_table;

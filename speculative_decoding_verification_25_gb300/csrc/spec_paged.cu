@@ -38,13 +38,13 @@ PagedDevice g_paged[kMaxDevices];
 // The attention kernel's variants.
 struct AttentionVariant {
   const void* fn;
-  int threads, smem_bytes, ctas_per_sm, keys;
+  int threads, smem_bytes, ctas_per_sm, keys, unit_rows;
 };
 template <typename E, int kD, bool kWide>
 AttentionVariant variant() {
   using S = sv::AttnShape<kD, kWide>;
   return {(const void*)sv::sv_paged_attention_kernel<E, kD, kWide>, S::kThreads, S::kSmemBytes,
-          S::kCtasPerSm, S::kKeys};
+          S::kCtasPerSm, S::kKeys, S::kRows};
 }
 AttentionVariant attention_variant(int dtype, int D, bool wide) {
   if (dtype == SV_BF16) {
@@ -244,9 +244,7 @@ int spec_paged_attention(const void* q, int64_t q_stride, const void* k_cache, c
   // rows (37 ragged requests, D = 64) 70 and 54, 8192 rows 449 and 308.
   const bool wide = (long long)T * G > 128ll * (B > 0 ? B : 1);
   const AttentionVariant v = attention_variant(dtype, D, wide);
-  int ctas = dev->sm_count * v.ctas_per_sm;
-  const int most = sv::kAttnMaxCtas * v.ctas_per_sm / 2;
-  if (ctas > most) ctas = most;
+  const int ctas = sv::range_ctas(dev->sm_count * v.ctas_per_sm, v.unit_rows);
 
   sv::AttnArgs a;
   a.block_table = block_table;

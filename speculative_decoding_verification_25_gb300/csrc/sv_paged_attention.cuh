@@ -65,10 +65,6 @@ namespace sv {
 constexpr float kLog2e = 1.44269504f;
 constexpr float kLn2 = 0.693147181f;
 constexpr float kSlack = 8.f;        // in log2: probabilities up to 256, exact in both types' range
-constexpr int kAttnMaxCtas = 320;    // resident CTAs that the workspace has room for (narrow)
-constexpr int kAttnRowsPerSlot = 128;
-// rows of partial sums in the workspace, for both forms
-constexpr long long kAttnRows = 2ll * kAttnMaxCtas * kAttnRowsPerSlot;
 
 struct AttnArgs {
   const int32_t* block_table;   // [B, max_pages]

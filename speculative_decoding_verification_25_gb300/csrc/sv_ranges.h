@@ -1,4 +1,4 @@
-// Arithmetic of the attention's ranges, for the kernel and for host tests:
+// Arithmetic of the attention's ranges, for the host, the kernel and host tests:
 // the work is `total` keys, cut into equal ranges of `quota` keys, a CTA each.
 // Divisions are 32 bits wide where their operands are: a 64-bit one is a
 // hundred instructions at a CTA's start.
@@ -13,6 +13,17 @@
 #endif
 
 namespace sv {
+
+constexpr int kAttnMaxCtas = 320;    // CTAs that the workspace has tickets for
+// Rows of partial sums in the workspace: two slots a CTA, of 128 rows; forms whose
+// units have more rows have fewer CTAs.
+constexpr long long kAttnRows = 2ll * kAttnMaxCtas * 128;
+
+// CTAs of a grid: as many as are resident, and as the workspace has room for.
+inline int range_ctas(int resident, int unit_rows) {
+  const long long room = kAttnRows / (2 * unit_rows), most = room < kAttnMaxCtas ? room : kAttnMaxCtas;
+  return resident < most ? resident : (int)most;
+}
 
 // Keys of a range: total / ctas rounded up, at least `least`.
 SV_HOST_DEVICE long long range_quota(long long total, unsigned ctas, int least) {
