@@ -598,7 +598,9 @@ int spec_paged_read_fp4(const void* k_codes, const void* k_scales, const void* v
  * arguments, its workspace (spec_paged_attention_workspace_bytes, which calls
  * of both kinds may share, one after the other) and its waits, with the cache in
  * four arrays, 16-byte aligned, and its gains.  As there, a request's values may
- * not be NaN where a token does not see them, its keys may.
+ * not be NaN where a token does not see them, its keys may.  Probabilities are
+ * rounded to 11 bits for both types, and to steps of 2^-31 of a row's largest
+ * where they are less than 2^-21 of it.
  * scale * log2(e) * k_gain is a normal float32 number, and max_pages * page_size
  * <= 2^31 - 1024.
  */

@@ -13,12 +13,12 @@
 // Operands are float16 whatever the queries' type.  A code times a scale is exact
 // there.  bfloat16 queries are too, scaled by a power of two that a unit's rows
 // share, except that steps are 2^-40 of the unit's largest magnitude or less.
-// Probabilities (at most 2^kSlack) are rounded to 11 bits.  The caller's gains
-// go into the scores' factor and into the results'.
+// Probabilities are rounded to 11 bits (see kFp4Below).  The caller's gains go into
+// the scores' factor and into the results'.
 //
 // A thread of the softmax has a key and the scores of all rows.  A row's
-// reference is common to the tile: it changes only when some score exceeds
-// it by more than kSlack, which one vote of the warps tells; then the maxima are
+// reference is common to the tile: it changes only when some score exceeds the
+// maximum that set it by more than kSlack, which one vote of the warps tells; then the maxima are
 // taken across the threads, and what was summed is scaled.  Row sums stay
 // with the threads until the unit ends.
 //
@@ -475,7 +475,7 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
           for (int y = 0; y < kChunk; y += 2)
             if (y0 + (y & 16) < cols) top = max3(top, __uint_as_float(s[y]), __uint_as_float(s[y + 1]));
         }
-        raise = top > kSlack;
+        raise = top > kFp4Below + kSlack;
       }
       if (i == 0 || vote_any(id, raise)) {
         if (!vote_all(id, ok)) return;
@@ -494,7 +494,8 @@ __device__ __forceinline__ void fp4_softmax(const Fp4Args& a, AttnWalk<S> u, Fp4
         }
         (void)vote_any(id, false);
         if (x < cols) {
-          const float high = fmaxf(fmaxf(tops[x], tops[kCols + x]), fmaxf(tops[2 * kCols + x], tops[3 * kCols + x])) * f;
+          const float high = fmaf(fmaxf(fmaxf(tops[x], tops[kCols + x]), fmaxf(tops[2 * kCols + x], tops[3 * kCols + x])), f,
+                                  -kFp4Below);
           const float old = marks[x];
           const bool up = i == 0 ? high > old : high > old + kSlack;
           const float now = up ? high : old;

@@ -7,6 +7,14 @@
 
 namespace sv {
 
+// P is float16 here whatever the queries' type, and float16 has 11 bits from 2^-14
+// and steps of 2^-24: so a reference is set this far below a row's maximum (in log2),
+// and P is at most 2^(kFp4Below + kSlack) = 2^15.  A probability then has its 11 bits
+// down to 2^-21 of the largest, and steps of 2^-31 of it below that; with the reference at
+// the maximum, keys 17.5 (natural units) below the first one gave 0 where 4096 of them
+// are 1e-4 of the result.  No instruction is added.
+constexpr float kFp4Below = 7.f;
+
 struct Fp4Args : AttnArgs {
   const char* q;
   long long q_pitch;   // bytes between tokens

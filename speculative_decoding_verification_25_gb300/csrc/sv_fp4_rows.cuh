@@ -25,6 +25,7 @@ template <int kD, bool kWide>
 struct Fp4RowsShape : AttnShape<kD, true> {
   using Base = AttnShape<kD, true>;
   static constexpr bool kFp4 = true;
+  static constexpr float kBelow = kFp4Below;
   // wide: a fourth unpacked tile in place of the staging (prompt chunks 446 and 392 us)
   static constexpr bool kStaged = !kWide;
   static constexpr int kChunk = kWide ? 128 : 64;

@@ -89,6 +89,7 @@ __device__ __forceinline__ int naps_of(const AttnArgs& a) { return kChecked ? a.
 template <int kD, bool kWide>
 struct AttnShape {
   static constexpr bool kFp4 = false;                // the 4-bit cache's shape has it true
+  static constexpr float kBelow = 0.f;               // what a new reference lies below the maximum
   static constexpr bool kStaged = true;              // rows pass through shared memory on their way out
   static constexpr int kTiles = kWide ? 2 : 1;
   static constexpr int kKeys = kWide ? 128 : 64;
@@ -819,7 +820,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
           }
         }
         // The reference follows the maximum where that rises by more than kSlack.
-        const float high = top * scale;
+        const float high = S::kFp4 ? fmaf(top, scale, -S::kBelow) : top * scale;
         const bool raise = mine && (i == 0 ? high > m : high > m + kSlack);
         if (__any_sync(0xffffffffu, raise)) {
           const float f = raise ? (m == SV_NEG_INF ? 0.f : ex2_approx(m - high)) : 1.f;

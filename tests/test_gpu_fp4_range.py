@@ -73,3 +73,26 @@ def test_attention_over_the_most_keys(form, cut):
     tol = want.out_tol + 2 * (adds + few * L) * spread + 2.0 ** -8 * np.abs(want.out)
     assert (np.abs(out - want.out) <= tol).all()
     assert (np.abs(lse - want.lse - math.log(repeat)) <= want.lse_tol + adds + few * L + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("below", [6.0, 14.0, 16.0, 17.5])
+@pytest.mark.parametrize("form", FORMS)
+def test_a_key_that_outweighs_the_others(form, below):
+    """The first key's score is `below` above all others', its value is 0: what remains
+    are the others' small probabilities.  They are rounded to 11 bits, or where they are
+    less than 2^-21 of the largest to steps of 2^-31 of it, so by half of that."""
+    n, G, D, L, B = FORMS[form], 4, 64, 4096, 320
+    k, v = np.zeros((L, D)), np.ones((L, D))
+    k[0, 0], k[1:, 0], v[0] = 6, -6, 0
+    q = np.zeros((n, G, D))
+    q[..., 0] = _bf16(below / 12)
+    r = _shared(k, v, q, B)
+    out, lse = (x.double().cpu().numpy().reshape(B, n, G, -1) for x in (r.out, r.lse))
+    k, v = (oracle.decode(*oracle.encode(x))[None, None] for x in (k, v))
+    want = paged_oracle.attention(q, k, v, np.zeros((1, 1), int), [0, n], [L], 1.0, "f16")
+    # the oracle's bound is for steps of 2^-24 of the largest
+    others = np.abs(v).sum() / D
+    tol = want.out_tol - 1.01 * (2.0 ** -25 - 2.0 ** -32) * others + 2.0 ** -8 * np.abs(want.out)
+    assert (tol > 0).all() and (tol < 0.02 * np.abs(want.out)).all()
+    assert (np.abs(out - want.out) <= tol).all()
+    assert (np.abs(lse[..., 0] - want.lse) <= want.lse_tol).all()
