@@ -82,6 +82,10 @@ struct AttnArgs {
   int naps;                     // checked build: polls after which a wait is given up
   float v_gain = 1.f;           // 4-bit cache: a factor of the results
 };
+// A normalised result times the gain of a 4-bit cache's values.  Sums in the workspace
+// are without it: times a large gain they could pass float32's range.
+template <typename S>
+__device__ __forceinline__ float with_gain(const AttnArgs& a, float o) { return S::kFp4 ? o * a.v_gain : o; }
 // A constant in the plain build (an argument there: verify 98.3 against 97.9 us,
 // ragged chunks 54.7 against 54.2).
 __device__ __forceinline__ int naps_of(const AttnArgs& a) { return kChecked ? a.naps : kNaps; }
@@ -728,7 +732,8 @@ __device__ __forceinline__ void attn_join(const AttnArgs& a, const AttnWalk<S>& 
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
       *(uint2*)(a.out + (to * kD + (v * kSpan + col) * 4) * 2) =
-          make_uint2(pack2(o[v].x * inv, o[v].y * inv, E()), pack2(o[v].z * inv, o[v].w * inv, E()));
+          make_uint2(pack2(with_gain<S>(a, o[v].x * inv), with_gain<S>(a, o[v].y * inv), E()),
+                     pack2(with_gain<S>(a, o[v].z * inv), with_gain<S>(a, o[v].w * inv), E()));
     if (a.lse && col == 0) a.lse[to] = row_lse(m, l);
   }
 }
@@ -916,7 +921,7 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
     const size_t slots = (size_t)gridDim.x * 2;
     const size_t slot = (size_t)cta * 2 + (cta == c_first && begins_late ? 1 : 0);
     if (any) {
-      const float inv = S::kFp4 ? row_inverse(l) * a.v_gain : row_inverse(l);
+      const float inv = row_inverse(l);
       // rows of `out` from the unit's first token and head, or rows of the slot
       const long long unit = (long long)(u.units.row.begin + u.first(0)) * a.Hq + u.h * a.G;
       const int to = !mine ? -1 : whole ? (token - u.first(0)) * a.Hq + r_head : t * 128 + r;
@@ -931,15 +936,12 @@ __device__ __forceinline__ void attn_softmax(const AttnArgs& a, AttnWalk<S> u, C
           tmem_wait_load();
           tmem_pin<32>(bits);
         }
-        if (S::kFp4 && !whole)
-#pragma unroll
-          for (int y = 0; y < 32; ++y) bits[y] = __float_as_uint(__uint_as_float(bits[y]) * a.v_gain);
         if (whole) {   // 64 columns make a segment
           uint32_t p[16];
 #pragma unroll
           for (int y = 0; y < 16; ++y)
-            p[y] = pack2(__uint_as_float(bits[2 * y]) * inv, __uint_as_float(bits[2 * y + 1]) * inv,
-                         Out());
+            p[y] = pack2(with_gain<S>(a, __uint_as_float(bits[2 * y]) * inv),
+                         with_gain<S>(a, __uint_as_float(bits[2 * y + 1]) * inv), Out());
           if constexpr (!S::kStaged) {
             store_row(a.flags, base + (long long)to * (kD * 2) + x * 2, to >= 0, p, 4, a.out, out_rows * (kD / 8));
           } else {

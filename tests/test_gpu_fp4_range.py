@@ -96,3 +96,24 @@ def test_a_key_that_outweighs_the_others(form, below):
     assert (tol > 0).all() and (tol < 0.02 * np.abs(want.out)).all()
     assert (np.abs(out - want.out) <= tol).all()
     assert (np.abs(lse[..., 0] - want.lse) <= want.lse_tol).all()
+
+
+@pytest.mark.parametrize("gain", [1e30, 1e-30])
+@pytest.mark.parametrize("form", FORMS)
+def test_parts_of_a_long_sum_with_an_extreme_gain(form, gain):
+    """One request cut into parts of 200000 or more keys, all of the largest value: a part's
+    sum times the gain is past float32's range, the results are not."""
+    n, G, D = FORMS[form], 4, 64
+    gain = float(np.float32(gain))
+    L, repeat = 40 * PAGE, 6000           # 61 million keys
+    v = np.full((L, D), 6 * 448 * gain)
+    r = _shared(np.zeros((L, D)), v, np.ones((n, G, D)), 1, repeat=repeat, gains=(1.0, gain))
+    # A sum of N float32 additions that may truncate is within N 2^-23: a range's products add
+    # 16 keys at a time, the join a part at a time; the normaliser as much; one rounding.
+    keys = L * repeat
+    adds = keys / 152 / 16 + 320
+    tol = 2 * adds * 2.0 ** -23 + 2.0 ** -8
+    assert tol < 0.02
+    assert bool(((r.out.double() / (2688 * gain) - 1).abs() <= tol).all())
+    # tokens before the last see some keys less: at most n of 61 million
+    assert bool(((r.lse.double() - math.log(keys)).abs() <= adds * 2.0 ** -23 + n / keys + 2.0 ** -20).all())
