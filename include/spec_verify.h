@@ -601,8 +601,9 @@ int spec_paged_read_fp4(const void* k_codes, const void* k_scales, const void* v
  * not be NaN where a token does not see them, its keys may.  Probabilities are
  * rounded to 11 bits for both types, and to steps of 2^-31 of a row's largest
  * where they are less than 2^-21 of it.
- * scale * log2(e) * k_gain is a normal float32 number, and max_pages * page_size
- * <= 2^31 - 1024.
+ * scale * log2(e) * k_gain is a normal float32 number; times the largest |q| it
+ * should be one too, else rows on the same key head may get a wrong lse.
+ * max_pages * page_size <= 2^31 - 1024.
  */
 int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_codes, const void* k_scales,
                              const void* v_codes, const void* v_scales, int dtype,

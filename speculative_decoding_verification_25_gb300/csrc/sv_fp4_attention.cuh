@@ -71,7 +71,7 @@ struct Fp4Control {
   uint32_t tmem;
   int abort_word, calm, last;
   unsigned status;
-  int q_exponent[2];
+  int q_exponent[2];          // for the scores' factor
   AttnStart start;
   long long sums[20];
 };
@@ -160,7 +160,7 @@ __device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4
       exponent = (int)(__float_as_uint(top) >> 23) - 127 - 14;   // subnormal: as if 2^-127
     }
     fence_async_shared();
-    if (lane == 0) c->q_exponent[buf] = exponent;
+    if (lane == 0) c->q_exponent[buf] = score_exponent(a.scale_log2, exponent);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_addr(&c->q_full[buf]));
     ++rounds;

@@ -15,6 +15,15 @@ namespace sv {
 // are 1e-4 of the result.  No instruction is added.
 constexpr float kFp4Below = 7.f;
 
+// The power of two that the scores' factor takes for queries that carry 2^exponent, such
+// that the factor is a normal number: with 0 a masked score of -inf would become NaN, with
+// an infinity a score of 0.  Where it would be less, every score (below 2^34 times it)
+// is 0 to all purposes as it is.
+__device__ __forceinline__ int score_exponent(float scale_log2, int exponent) {
+  const int own = (int)(__float_as_uint(scale_log2) >> 23) - 127;
+  return min(max(exponent, -126 - own), 127 - own);
+}
+
 struct Fp4Args : AttnArgs {
   const char* q;
   long long q_pitch;   // bytes between tokens

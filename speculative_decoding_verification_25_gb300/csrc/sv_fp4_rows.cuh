@@ -58,7 +58,7 @@ struct Fp4RowsControl {   // as AttnControl, and:
   volatile int past;
   int abort_word, calm, last;
   unsigned status;
-  int q_exponent[2][2];       // [unit % 2][query tile]
+  int q_exponent[2][2];       // for the scores' factor: [unit % 2][query tile]
   AttnStart start;
   long long sums[16];
 };
@@ -136,7 +136,7 @@ __device__ __forceinline__ void fp4_rows_queries(const Fp4Args& a, AttnWalk<S> u
             *at = make_uint4(v[0], v[1], v[2], v[3]);
           }
       }
-      if (lane == 0) c->q_exponent[rounds % 2][t] = exponent;
+      if (lane == 0) c->q_exponent[rounds % 2][t] = score_exponent(a.scale_log2, exponent);
     }
     fence_async_shared();
     __syncwarp();

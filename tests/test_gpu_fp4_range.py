@@ -117,3 +117,31 @@ def test_parts_of_a_long_sum_with_an_extreme_gain(form, gain):
     assert bool(((r.out.double() / (2688 * gain) - 1).abs() <= tol).all())
     # tokens before the last see some keys less: at most n of 61 million
     assert bool(((r.lse.double() - math.log(keys)).abs() <= adds * 2.0 ** -23 + n / keys + 2.0 ** -20).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_scores_too_small_for_float32(form, D):
+    """scale * log2(e) * k_gain times the power of two of the queries underflows: every
+    score is 0 to all purposes, and masked keys are masked all the same."""
+    n = FORMS[form]
+    c = Fp4Case([(300, n), (n + 133, n), (n, n)], 8, 2, D, 16, "bf16", seed=4, gains=(float(np.float32(1e-20)), 1.0))
+    c.qkv.mul_(1e-24)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_of_zeros_beside_scores_past_float32(form):
+    """Queries so large that the factor of their scores overflows: rows of zeros in the
+    same unit have scores of 0."""
+    n = FORMS[form]
+    c = Fp4Case([(300, n), (n + 133, n)], 8, 2, 64, 16, "bf16", seed=4)
+    c.scale = 1e30
+    want = c.host[0][1][:300 - n + 1].mean(0)      # token 0 of the first request: a uniform average
+    c.qkv.mul_(1e30)
+    c.qkv[0, 0] = 0
+    r = c.run()
+    got = r.out[0, 0].double().cpu().numpy()
+    # sums of values of up to 301 keys, P exact, one rounding each of P's inverse sum and of the result
+    assert (np.abs(got - want[0]) <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -20).all()
+    assert abs(float(r.lse[0, 0]) - math.log(300 - n + 1)) <= 2.0 ** -20
