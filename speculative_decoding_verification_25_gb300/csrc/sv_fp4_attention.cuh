@@ -11,8 +11,9 @@
 // 0.56 bytes a value, and would be the bound of 16-bit tiles (5 bytes a value).
 //
 // Operands are float16 whatever the queries' type.  A code times a scale is exact
-// there.  bfloat16 queries are too, scaled by a power of two that a unit's rows
-// share, except that steps are 2^-40 of the unit's largest magnitude or less.
+// there.  bfloat16 queries are scaled by a power of two that a unit's rows share, and
+// have steps of 2^-32 of the unit's largest magnitude or less (few or none of them
+// need their rounding: eight bits are exact down to 2^-25 of it).
 // Probabilities are rounded to 11 bits (see kFp4Below).  The caller's gains go into
 // the scores' factor and into the results'.
 //
@@ -128,13 +129,13 @@ __device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4
       if (row < cols)
         *(uint4*)(to + row * 128 + ((part % 8) ^ (row % 8)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     };
-    int exponent = 0;
-    float top = 0.f;
-    // Magnitudes between 2^-2 and 2^15 need no scaling: tried first.
+    // The first try is right for a largest magnitude of 2^-3 to 2^5, which is 2^8 to 2^16
+    // then; other units are done again, with their own exponent.
+    int exponent = kBf16 ? -11 : 0;
 #pragma unroll 1
     for (int again = 0; again < 2; ++again) {
-      // 2^-exponent in two factors, each of which is a normal number
-      const float f0 = ldexpf(1.f, -exponent / 2), f1 = ldexpf(1.f, -exponent - -exponent / 2);
+      const uint32_t factor = query_factor(exponent);
+      uint32_t high = 0;
 #pragma unroll 1
       for (int r0 = lane / kLanes; r0 < cols; r0 += kPass * kAhead) {
         uint32_t w[kAhead][4];
@@ -145,19 +146,27 @@ __device__ __forceinline__ void fp4_queries(const Fp4Args& a, AttnWalk<S> u, Fp4
           if (kBf16) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const float lo = __uint_as_float(w[i][x] << 16), hi = __uint_as_float(w[i][x] & 0xffff0000u);
-              if (fabsf(lo) < 3.4e38f) top = fmaxf(top, fabsf(lo));   // neither infinities nor NaN
-              if (fabsf(hi) < 3.4e38f) top = fmaxf(top, fabsf(hi));
-              w[i][x] = pack2(lo * f0 * f1, hi * f0 * f1, __half());
+              high = __vmaxu2(high, bf16_magnitudes(w[i][x], false));
+              w[i][x] = query_pair(w[i][x], factor);
             }
           }
           store(r0 + i * kPass, w[i]);
         }
       }
       if (!kBf16 || again) break;
-      top = redux_max(top);
-      if (top == 0.f || (top >= 0.25f && top < 32768.f)) break;
-      exponent = (int)(__float_as_uint(top) >> 23) - 127 - 14;   // subnormal: as if 2^-127
+      uint32_t top = __reduce_max_sync(0xffffffffu, larger_half(high));
+      if (top >= kBf16Infinity) {   // the largest of the others
+        high = 0;
+#pragma unroll 1
+        for (int r = lane / kLanes; r < cols; r += kPass) {
+          uint32_t w[4];
+          load(r, w);
+          for (int x = 0; x < 4; ++x) high = __vmaxu2(high, bf16_magnitudes(w[x], true));
+        }
+        top = __reduce_max_sync(0xffffffffu, larger_half(high));
+      }
+      if (top == 0 || (top >= 0x3e00u && top < 0x4200u)) break;   // 2^-3, 2^5
+      exponent = query_exponent(top);
     }
     fence_async_shared();
     if (lane == 0) c->q_exponent[buf] = score_exponent(a.scale_log2, exponent);

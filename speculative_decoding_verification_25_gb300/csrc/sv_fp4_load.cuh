@@ -15,6 +15,26 @@ namespace sv {
 // are 1e-4 of the result.  No instruction is added.
 constexpr float kFp4Below = 7.f;
 
+// bfloat16 queries become float16 times 2^-exponent.  Brought to [2^14, 2^15), the largest
+// of a unit leaves the others steps of 2^-38 of it or less.  2^126 is the most that they
+// are multiplied by: then no bfloat16 number is below float16's steps.
+constexpr uint32_t kBf16Infinity = 0x7f80u;
+__device__ __forceinline__ int query_exponent(uint32_t top) { return max((int)(top >> 7) - 127 - 14, -126); }   // of its bits
+__device__ __forceinline__ uint32_t query_factor(int exponent) { return (uint32_t)(127 - exponent) << 7 | (uint32_t)(127 - exponent) << 23; }
+__device__ __forceinline__ uint32_t query_pair(uint32_t w, uint32_t factor) {
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(factor));
+  return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u), __half());
+}
+// The larger magnitude of the two that a word has.
+__device__ __forceinline__ uint32_t larger_half(uint32_t magnitudes) { return max(magnitudes >> 16, magnitudes & 0xffffu); }
+// Magnitudes of a word; `finite`: 0 for infinities and NaN.
+__device__ __forceinline__ uint32_t bf16_magnitudes(uint32_t w, bool finite) {
+  w &= 0x7fff7fffu;
+  if (finite && (w & 0xffffu) >= kBf16Infinity) w &= 0xffff0000u;
+  if (finite && w >> 16 >= kBf16Infinity) w &= 0xffffu;
+  return w;
+}
+
 // The power of two that the scores' factor takes for queries that carry 2^exponent, such
 // that the factor is a normal number: with 0 a masked score of -inf would become NaN, with
 // an infinity a score of 0.  Where it would be less, every score (below 2^34 times it)

@@ -3,8 +3,9 @@
 // over tiles that four warps unpack to 16 bits in shared memory, from a ring of
 // packed ones.
 //
-// Operands are float16 as in sv_fp4_attention.cuh: bfloat16 queries are
-// converted in shared memory, each query tile with a power of two of its own.
+// Operands are float16 as in sv_fp4_attention.cuh: bfloat16 queries are converted in
+// shared memory, each query tile with a power of two of its own (steps of 2^-38 of its
+// largest magnitude).
 //
 // Bound by a tile's chain.  Narrow, 256 x 9 tokens over 2 k to 10 k keys, 64/8
 // heads of 128: 780 us for 1.87 GB, about 2400 clocks per tile of 128 keys: 1716 of
@@ -93,47 +94,29 @@ __device__ __forceinline__ void fp4_rows_queries(const Fp4Args& a, AttnWalk<S> u
       if (std::is_same<E, __nv_bfloat16>::value && u.count(t) > 0) {
         const int pieces = (u.last(t) - u.first(t)) * a.G * 8;   // of 16 bytes in a block of 64 columns
         char* tile = q_ptr + t * S::kQBytes;
-        // magnitudes as integers, two a word, in the order of their numbers
-        uint32_t high = 0;
-#pragma unroll 1
-        for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll 8
-          for (int x = lane; x < pieces; x += 32) {
-            const uint4 w = *(const uint4*)(tile + b * 128 * 128 + x * 16);
-            high = __vmaxu2(__vmaxu2(high, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
-            high = __vmaxu2(__vmaxu2(high, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
-          }
-        float top = __uint_as_float(max(high >> 16, high & 0xffffu) << 16);
-        if (__any_sync(0xffffffffu, !(top <= 3.4e38f))) {   // an infinity or NaN: the largest of the others
-          top = 0.f;
+        auto largest = [&](bool finite) {
+          uint32_t high = 0;
 #pragma unroll 1
           for (int b = 0; b < S::kBlocks; ++b)
-#pragma unroll 1
-            for (int x = lane; x < pieces * 8; x += 32) {
-              const float v =
-                  __uint_as_float((uint32_t)(*(const uint16_t*)(tile + b * 128 * 128 + x * 2) & 0x7fffu) << 16);
-              if (v <= 3.4e38f) top = fmaxf(top, v);
+#pragma unroll 8
+            for (int x = lane; x < pieces; x += 32) {
+              const uint4 w = *(const uint4*)(tile + b * 128 * 128 + x * 16);
+              high = __vmaxu2(__vmaxu2(high, bf16_magnitudes(w.x, finite)), bf16_magnitudes(w.y, finite));
+              high = __vmaxu2(__vmaxu2(high, bf16_magnitudes(w.z, finite)), bf16_magnitudes(w.w, finite));
             }
-        }
-        top = warp_max(top);
-        // magnitudes between 2^-2 and 2^15 need no scaling
-        if (!(top == 0.f || (top >= 0.25f && top < 32768.f)))
-          exponent = (int)(__float_as_uint(top) >> 23) - 127 - 14;   // subnormal: as if 2^-127
-        // 2^-exponent in two factors, each of which is a normal number
-        const float f0 = ldexpf(1.f, -exponent / 2), f1 = ldexpf(1.f, -exponent - -exponent / 2);
+          return __reduce_max_sync(0xffffffffu, larger_half(high));
+        };
+        uint32_t top = largest(false);
+        if (top >= kBf16Infinity) top = largest(true);   // of the others
+        exponent = query_exponent(top);
+        const uint32_t factor = query_factor(exponent);
 #pragma unroll 1
         for (int b = 0; b < S::kBlocks; ++b)
 #pragma unroll 4
           for (int x = lane; x < pieces; x += 32) {
             uint4* at = (uint4*)(tile + b * 128 * 128 + x * 16);
-            uint32_t v[4] = {at->x, at->y, at->z, at->w};
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              float lo = __uint_as_float(v[y] << 16), hi = __uint_as_float(v[y] & 0xffff0000u);
-              if (exponent != 0) lo = lo * f0 * f1, hi = hi * f0 * f1;
-              v[y] = pack2(lo, hi, __half());
-            }
-            *at = make_uint4(v[0], v[1], v[2], v[3]);
+            const uint4 w = *at;
+            *at = make_uint4(query_pair(w.x, factor), query_pair(w.y, factor), query_pair(w.z, factor), query_pair(w.w, factor));
           }
       }
       if (lane == 0) c->q_exponent[rounds % 2][t] = score_exponent(a.scale_log2, exponent);

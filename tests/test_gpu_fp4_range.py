@@ -145,3 +145,20 @@ def test_rows_of_zeros_beside_scores_past_float32(form):
     # sums of values of up to 301 keys, P exact, one rounding each of P's inverse sum and of the result
     assert (np.abs(got - want[0]) <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -20).all()
     assert abs(float(r.lse[0, 0]) - math.log(300 - n + 1)) <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_that_differ_by_far_at_ordinary_sizes(form, D):
+    """Queries of about 1 beside others 2^-20 of that in the same unit, whose scores matter
+    since the keys are large."""
+    n = FORMS[form]
+    c = Fp4Case([(700, n), (n, n), (n + 250, n)], 8, 2, D, 16, "bf16", seed=21)
+    c.qkv[::3, ::2] *= 2.0 ** -20
+    c.qkv[1::3, 1::4] *= 2.0 ** -22
+    c.k_cache.mul_(2.0 ** 20)
+    for kv in c.host:
+        kv[0] *= 2.0 ** 20
+    c.gains = (2.0 ** 20, 1.0)
+    c.encode()
+    c.check(c.run())
