@@ -569,9 +569,10 @@ int spec_paged_append_rotary(const void* q, int64_t q_stride, const void* k_new,
  *   scale = a / (6 gain), rounded to e4m3 (448 at most),
  *   code  = x / (scale gain), rounded to e2m1 (6 at most), 0 where scale is 0,
  * both to the nearest number and of two to the even one, as exact arithmetic
- * rounds them.  A group with a NaN or an infinity gets the scale 0x7f and is
- * all NaN.  positions and cos_sin may be NULL, both of them, with Hq == 0: keys
- * are not rotated.
+ * rounds them, for tables of any size.  A group with a NaN or an infinity (a
+ * rotated value that float32 does not hold is one) gets the scale 0x7f and is all
+ * NaN.  positions and cos_sin may be NULL, both of them, with Hq == 0: keys are not
+ * rotated.
  */
 int spec_paged_append_fp4(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
                           const void* v_new, int64_t v_stride, const int32_t* positions,

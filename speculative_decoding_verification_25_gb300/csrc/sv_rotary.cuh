@@ -205,16 +205,17 @@ __device__ __forceinline__ float2 wide_product(float a, float b) {
 // that is not a border c / 4 of two codes differs from it by at least 2^-14, the
 // smallest border being 1/4; so its product with the rounded inverse, off by 2^-20,
 // is rounded to steps of 2^-18, and falls on the border exactly when it should.
-// Else a value is off by at most 2^-23 (|x| + |y|) for its pair and its quotient by
-// 2^-21 of itself: where four times that could cross a border, one of some hundred
-// warps, pairs of numbers decide.
+// Else a rotated value is off by at most 2^-23 (|x| + |y|) t for its pair and the largest
+// cosine or sine t, and its quotient by 2^-22 of itself, which is at most 2 max(|x|, |y|) t;
+// other values' t is 1.  Where twice that, max(|x|, |y|) times `slope`, 2^-19 t, could cross
+// a border, one of some hundred warps, pairs of numbers decide.
 template <typename E, bool kNeighbours>
 __device__ __forceinline__ void quantise(const float* x, const float* in, const RotaryPlace& at, bool exact,
-                                         float gain, uint32_t* scale, uint32_t* codes) {
+                                         float slope, float gain, uint32_t* scale, uint32_t* codes) {
   float off = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) off = fmaxf(off, fabsf(in[i]));
-  off = exact ? 0.f : off * 0x1p-19f;
+  off *= exact ? 0.f : slope;
   const float off_pair = fmaxf(off, __shfl_xor_sync(0xffffffffu, off, 1));
   const float six = 6.f * gain, sixth = __fdiv_rn(1.f, six);
 #pragma unroll
@@ -293,6 +294,7 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
     for (int i = 0; i < 4; ++i) w[i] = lo[i], w[4 + i] = hi[i];
   };
   RotaryAngles angles;
+  float slope = 0.f;   // 2^-19 of the largest of them
   const float* table = a.table + (long long)pos * a.rot;
   auto look_up = [&]() {
     if (!rotated || !placed || first_head >= a.Hq + a.Hk) return;
@@ -303,6 +305,10 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
     *(float4*)(angles.c + 4) = *(const float4*)(table + next);
     *(float4*)angles.s = *(const float4*)(table + a.rot / 2 + at);
     *(float4*)(angles.s + 4) = *(const float4*)(table + a.rot / 2 + next);
+    if (!kFp4) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) slope = fmaxf(slope, fmaxf(fabsf(angles.c[i]), fabsf(angles.s[i])));
+    slope *= 0x1p-19f;
   };
   auto finish = [&](int h, const uint32_t* w, auto coded) {   // `coded`: keys and values become codes
     constexpr bool kCoded = decltype(coded)::value;
@@ -333,7 +339,8 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
       const bool exact = !turn && (is_k ? a.k_plain : a.v_plain);
       const RotaryPlace at = {goes ? source(h) : nullptr, table, a.rot, p0, p1, part, turn};
       // a lane whose head goes nowhere has nothing to decide
-      quantise<E, kNeighbours>(x, in, at, exact || !goes, is_k ? a.k_gain : a.v_gain, scale, codes);
+      quantise<E, kNeighbours>(x, in, at, exact || !goes, turn ? slope : 0x1p-19f, is_k ? a.k_gain : a.v_gain, scale,
+                                codes);
       if (!goes) return;
       char* code_row = (is_k ? a.k_cache : a.v_cache) + row * (kD / 2);
       uint8_t* scale_row = (is_k ? a.k_scale : a.v_scale) + row * (kD / kFp4Group);
