@@ -161,8 +161,10 @@ __device__ __forceinline__ void fp4_rows_unpack(const Fp4Args& a, AttnWalk<S> u,
     for (int p = 0; p < kD / 32; ++p) {
       if (!S::kAhead) w4 = load(p);
       const uint32_t pair = fp4_scales(S::kAhead ? bytes.x & 0xffff : *(const uint16_t*)(scales + p * 2));
-      bytes.x = __funnelshift_r(bytes.x, bytes.y, 16);
-      bytes.y >>= 16;
+      if (S::kAhead) {
+        bytes.x = __funnelshift_r(bytes.x, bytes.y, 16);
+        bytes.y >>= 16;
+      }
       const uint32_t s[2] = {__byte_perm(pair, 0, 0x1010), __byte_perm(pair, 0, 0x3232)};
       const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
       if (S::kAhead && p + 1 < kD / 32) w4 = load(p + 1);

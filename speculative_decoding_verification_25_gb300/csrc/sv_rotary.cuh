@@ -91,11 +91,11 @@ struct RotaryAngles {
 __device__ __forceinline__ int pair_x(bool neighbours, int i) { return neighbours ? 2 * i : i; }
 __device__ __forceinline__ int pair_y(bool neighbours, int i) { return neighbours ? 2 * i + 1 : i + 8; }
 
-template <typename F, bool kNeighbours>
-__device__ __forceinline__ void rotate(const RotaryAngles& a, const float* in, F* out) {
+template <bool kNeighbours>
+__device__ __forceinline__ void rotate(const RotaryAngles& a, const float* in, float* out) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const F x = in[pair_x(kNeighbours, i)], y = in[pair_y(kNeighbours, i)], c = a.c[i], s = a.s[i];
+    const float x = in[pair_x(kNeighbours, i)], y = in[pair_y(kNeighbours, i)], c = a.c[i], s = a.s[i];
     out[pair_x(kNeighbours, i)] = x * c - y * s;
     out[pair_y(kNeighbours, i)] = x * s + y * c;
   }
@@ -322,7 +322,7 @@ __device__ __forceinline__ void rotary_token(const RotaryArgs& a, int token, int
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = in[i];
     const bool turn = rotated && placed && (is_q || is_k);
-    if (turn) rotate<float, kNeighbours>(angles, in, x);
+    if (turn) rotate<kNeighbours>(angles, in, x);
     const long long row = slot_row + ((long long)hk << a.page_shift);
     if (is_q || (!kCoded && goes)) {
       char* to = is_q ? a.q_out + token * a.out_pitch + (long long)h * kD * 2
