@@ -538,7 +538,7 @@ int spec_paged_attention_device_errors(void* workspace, void* stream, uint32_t* 
  *   cos_sin      [max_positions, rotary_dim] float32, 16-byte aligned.
  *   rotary_dim   a multiple of 32, at most D (64 or 128).
  *   q_out        [T, Hq, D], tokens q_out_stride elements apart; it may be q
- *                itself, with its stride.
+ *                itself, with its stride, and overlaps no other argument.
  *   slot_map, k_cache, v_cache, flags: as for spec_paged_append.
  *
  * One launch.  Returns SV_OK, SV_ERR_DTYPE, SV_ERR_SHAPE, SV_ERR_NULL,
@@ -599,7 +599,9 @@ int spec_paged_read_fp4(const void* k_codes, const void* k_scales, const void* v
  * arguments, its workspace (spec_paged_attention_workspace_bytes, which calls
  * of both kinds may share, one after the other) and its waits, with the cache in
  * four arrays, 16-byte aligned, and its gains.  As there, a request's values may
- * not be NaN where a token does not see them, its keys may.  Probabilities are
+ * not be NaN where a token does not see them, its keys may.  Both products take
+ * float16: bfloat16 queries have steps of 2^-32, or less, of the largest magnitude
+ * among up to 128 rows of a request that share a key head.  Probabilities are
  * rounded to 11 bits for both types, and to steps of 2^-31 of a row's largest
  * where they are less than 2^-21 of it.
  * scale * log2(e) * k_gain is a normal float32 number; times the largest |q| it

@@ -162,3 +162,21 @@ def test_rows_that_differ_by_far_at_ordinary_sizes(form, D):
     c.gains = (2.0 ** 20, 1.0)
     c.encode()
     c.check(c.run())
+
+
+@pytest.mark.parametrize("factor", [2.0 ** -50, 1.0, 2.0 ** 60])
+@pytest.mark.parametrize("form", FORMS)
+def test_queries_that_are_not_finite_beside_others(form, factor):
+    """Rows of NaN and infinities leave the power of two of their unit to the others."""
+    n = FORMS[form]
+    c = Fp4Case([(300, n), (n + 133, n), (n, n)], 8, 2, 64, 16, "bf16", seed=9)
+    c.qkv.mul_(factor)
+    c.scale = float(np.float32(c.scale / factor))
+    c.qkv[1::n, 2], c.qkv[2::n, 5, 7], c.qkv[0, 6, 60] = float("nan"), float("inf"), -float("inf")
+    bad = ~c.q.isfinite().all(-1).cpu().numpy()
+    r = c.run()
+    out, lse = r.out.double().cpu().numpy(), r.lse.double().cpu().numpy()
+    c.qkv.nan_to_num_(0.0, 0.0, 0.0)      # the oracle's rows are each by itself
+    want = c.reference()
+    assert bad.sum() == 7 and np.isnan(out[bad]).all() and np.isnan(lse[bad]).all()
+    assert (np.abs(out - want.out) <= want.out_tol)[~bad].all() and (np.abs(lse - want.lse) <= want.lse_tol)[~bad].all()
