@@ -26,9 +26,10 @@
 // Work is cut into ranges and joined as in sv_paged_attention.cuh.
 //
 // Bound by instruction issue over long contexts: 4 x 1 token over 60 k to 131 k
-// keys, 64/8 heads of 128, 118 us for 426 MB, 3.6 TB/s, issue at 68% of its slots, the
-// tensor pipe at 9% (one CTA per SM and products issued by a chosen lane: 204).
-// Drafts (64 x 5 tokens over 203 to 4099 keys, 32/8 heads, 32 rows) 89 us for 162 MB:
+// keys, 64/8 heads of 128, 120 us for 426 MB, 3.5 TB/s, issue at 68% of its slots, the
+// tensor pipe at 8% (one CTA per SM and products issued by a chosen lane: 204).
+// It is compiled for 64 registers and spills 168 bytes a thread (16 rows, D = 128).
+// Drafts (64 x 5 tokens over 203 to 4099 keys, 32/8 heads, 32 rows) 90 us for 162 MB:
 // units of up to 33 tiles, whose start and end take about 10 us each.
 #pragma once
 

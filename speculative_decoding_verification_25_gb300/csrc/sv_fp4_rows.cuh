@@ -8,11 +8,11 @@
 // largest magnitude).
 //
 // Bound by a tile's chain.  Narrow, 256 x 9 tokens over 2 k to 10 k keys, 64/8
-// heads of 128: 780 us for 1.87 GB, about 2400 clocks per tile of 128 keys: 1716 of
+// heads of 128: 768 us for 1.87 GB, about 2400 clocks per tile of 128 keys: 1716 of
 // them are waits and handing over (measured without unpacking, exponentials and all
 // but one step of each product), the rest is what unpacking and softmax add
 // (transposed as in sv_fp4_attention.cuh 1726 us).  Wide, 2 x 2048 tokens over 5 k
-// to 7 k: 375 us, 1.26 PFLOP/s, beside 310 of 16 bits: the unpacking shares the
+// to 7 k: 371 us, 1.27 PFLOP/s, beside 310 of 16 bits: the unpacking shares the
 // schedulers with the softmax.
 #pragma once
 

@@ -11,9 +11,10 @@
 // pieces, so two lanes share a group of 16.  A warp takes kRotaryHeads passes of
 // heads of one token, all in flight; the lane's cosines and sines serve all of them.
 // 32768 tokens of 32/8 heads of 128, bfloat16: 130 us for 0.82 GB, 6.3 TB/s (heads
-// one after the other 146).  Into 4 bits 155 us, bound by instruction issue (58% of
+// one after the other 146).  Into 4 bits 158 us, bound by instruction issue (58% of
 // slots): there one copy of the long code runs while the next head's loads are
-// under way (all heads unrolled 205).  Reading 4 bits back: 38 us.
+// under way (all heads unrolled 205); without queries and rotation 75 us for 0.17 GB.
+// Reading 4 bits back 38 us: short threads, HBM at 43% and issue at 45%.
 //
 // Codes and scales are those of exact arithmetic: where a rotated value's error in
 // float32 could pass the border of two codes (one of a few hundred warps), the
