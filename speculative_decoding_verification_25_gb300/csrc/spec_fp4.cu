@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
-
 #include "spec_verify.h"
 #include "sv_fp4_attention.cuh"
 #include "sv_fp4_rows.cuh"
@@ -16,11 +14,10 @@ namespace {
 using sv::aligned_to;
 using sv::done;
 using sv::k2_31;
+using sv::kMaxDevices;
 using sv::launch_early;
 using sv::page_shift_of;
-
-using sv::EncodeTiled;
-using sv::kMaxDevices;
+using sv::PagedDevice;
 
 // Most keys of a request: the walk looks up to two key tiles past the last key, and a
 // unit's cost, which is higher here than over 16 bits, past its keys, in 32 bits.
@@ -32,13 +29,7 @@ static_assert(fits<sv::Fp4Shape<64, 16>> && fits<sv::Fp4Shape<64, 32>> && fits<s
 static_assert(fits<sv::Fp4RowsShape<64, false>> && fits<sv::Fp4RowsShape<64, true>> &&
                   fits<sv::Fp4RowsShape<128, false>> && fits<sv::Fp4RowsShape<128, true>>, "fits");
 
-struct Fp4Device {
-  std::once_flag once;
-  int sm_count = 0;
-  EncodeTiled encode = nullptr;
-  cudaError_t error = cudaSuccess;
-};
-Fp4Device g_fp4[kMaxDevices];
+PagedDevice g_fp4[kMaxDevices];
 
 struct Variant {
   const void* fn;
@@ -68,24 +59,19 @@ Variant variant_of(int dtype, int D, Form form) {
   return D == 128 ? variant_of<__half, 128>(form) : variant_of<__half, 64>(form);
 }
 
-// SM count, shared memory limits and the tensor map encoder; once per device.
-Fp4Device* fp4_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-  Fp4Device& d = g_fp4[dev];
-  std::call_once(d.once, [&d, dev]() {
-    d.error = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev);
-    for (int i = 0; i < 4 * kForms && d.error == cudaSuccess; ++i) {
+PagedDevice* fp4_device() {
+  return sv::current_device(g_fp4, []() {
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 4 * kForms && e == cudaSuccess; ++i) {
       const Variant v = variant_of(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, (Form)(i / 4));
-      d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
+      e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
     }
-    if (d.error == cudaSuccess) d.error = sv::find_encoder(&d.encode);
+    return e;
   });
-  return d.error == cudaSuccess ? &d : nullptr;
 }
 
 // A map of the codes' rows, one for a token and key head, in boxes of `box` rows.
-bool encode_codes(const Fp4Device& d, CUtensorMap* map, const void* base, int D, long long rows, int box) {
+bool encode_codes(const PagedDevice& d, CUtensorMap* map, const void* base, int D, long long rows, int box) {
   const cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows};
   const cuuint64_t pitches[1] = {(cuuint64_t)D / 2};
   const cuuint32_t boxes[2] = {(cuuint32_t)D / 2, (cuuint32_t)box}, ones[2] = {1, 1};
@@ -131,7 +117,7 @@ int spec_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_code
       !aligned_to(cu_new, 4) || !aligned_to(kv_len, 4) || !aligned_to(lse, 4) || !aligned_to(flags, 4))
     return SV_ERR_ALIGN;
   if (workspace_bytes < spec_paged_attention_workspace_bytes(D)) return SV_ERR_WORKSPACE;
-  Fp4Device* dev = fp4_device();
+  PagedDevice* dev = fp4_device();
   if (!dev) return SV_ERR_CUDA;
   const int G = Hq / Hk;
   // The host knows the mean of a request's rows (the G heads of its tokens on one key

@@ -5,8 +5,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
-
 #include "spec_verify.h"
 #include "sv_paged_append.cuh"
 #include "sv_paged_attention.cuh"
@@ -18,21 +16,15 @@ namespace {
 using sv::aligned_to;
 using sv::done;
 using sv::encode_map;
-using sv::EncodeTiled;
 using sv::k2_31;
 using sv::kMaxDevices;
 using sv::kMostKeys;
 using sv::launch_early;
 using sv::page_shift_of;
+using sv::PagedDevice;
 
 constexpr int kMaxCluster = 8;   // portable cluster size
 
-struct PagedDevice {
-  std::once_flag once;
-  int sm_count = 0;
-  EncodeTiled encode = nullptr;   // the driver's tensor map encoder
-  cudaError_t error = cudaSuccess;
-};
 PagedDevice g_paged[kMaxDevices];
 
 // The attention kernel's variants.
@@ -55,25 +47,17 @@ AttentionVariant attention_variant(int dtype, int D, bool wide) {
   return wide ? variant<__half, 64, true>() : variant<__half, 64, false>();
 }
 
-// SM count, the kernels' shared memory limits and the tensor map encoder;
-// once per device.
 PagedDevice* paged_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
-  PagedDevice& d = g_paged[dev];
-  std::call_once(d.once, [&d, dev]() {
-    d.error = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev);
-    if (d.error == cudaSuccess)
-      d.error = cudaFuncSetAttribute((const void*)sv::sv_paged_plan_kernel,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     SV_MAX_PLAN_ROWS * sv::kPlanRowBytes);
-    for (int i = 0; i < 8 && d.error == cudaSuccess; ++i) {
+  return sv::current_device(g_paged, []() {
+    cudaError_t e = cudaFuncSetAttribute((const void*)sv::sv_paged_plan_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         SV_MAX_PLAN_ROWS * sv::kPlanRowBytes);
+    for (int i = 0; i < 8 && e == cudaSuccess; ++i) {
       const AttentionVariant v = attention_variant(i & 1 ? SV_BF16 : SV_F16, i & 2 ? 128 : 64, i & 4);
-      d.error = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
+      e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem_bytes);
     }
-    if (d.error == cudaSuccess) d.error = sv::find_encoder(&d.encode);
+    return e;
   });
-  return d.error == cudaSuccess ? &d : nullptr;
 }
 
 static_assert(sv::kAttnMaxCtas * sizeof(int) <= SV_ATTENTION_COUNTER_BYTES - sizeof(uint32_t),

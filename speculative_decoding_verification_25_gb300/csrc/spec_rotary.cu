@@ -39,6 +39,28 @@ const void* rotary_kernel(int dtype, int D, bool fp4) {
              : (const void*)sv::sv_rotary_kernel<__half, 64, false>;
 }
 
+// What both appends take, as it comes.
+sv::RotaryArgs rotary_args(const void* q, const void* k_new, const void* v_new, const int32_t* positions,
+                           const float* cos_sin, int max_positions, int rotary_dim, int interleaved,
+                           const int32_t* slot_map, int T, int Hq, int Hk, void* q_out, uint32_t* flags) {
+  sv::RotaryArgs a = {};
+  a.q = (const char*)q;
+  a.k_new = (const char*)k_new;
+  a.v_new = (const char*)v_new;
+  a.positions = positions;
+  a.table = cos_sin;
+  a.slot_map = slot_map;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hk = Hk;
+  a.max_positions = max_positions;
+  a.rot = rotary_dim;
+  a.neighbours = interleaved != 0;
+  a.q_out = (char*)q_out;
+  a.flags = flags;
+  return a;
+}
+
 int launch_rotary(sv::RotaryArgs& a, int dtype, int D, bool fp4, int64_t q_stride, int64_t k_stride,
                   int64_t v_stride, int64_t out_stride, int page_size, int n_pages, void* stream) {
   if (dtype != SV_BF16 && dtype != SV_F16) return SV_ERR_DTYPE;
@@ -86,23 +108,10 @@ int spec_paged_append_rotary(const void* q, int64_t q_stride, const void* k_new,
                              int page_size, int n_pages, void* q_out, int64_t q_out_stride,
                              void* k_cache, void* v_cache, uint32_t* flags, void* stream) {
   if (T > 0 && (!positions || !cos_sin)) return SV_ERR_NULL;
-  sv::RotaryArgs a = {};
-  a.q = (const char*)q;
-  a.k_new = (const char*)k_new;
-  a.v_new = (const char*)v_new;
-  a.positions = positions;
-  a.table = cos_sin;
-  a.slot_map = slot_map;
-  a.T = T;
-  a.Hq = Hq;
-  a.Hk = Hk;
-  a.max_positions = max_positions;
-  a.rot = rotary_dim;
-  a.neighbours = interleaved != 0;
-  a.q_out = (char*)q_out;
+  sv::RotaryArgs a = rotary_args(q, k_new, v_new, positions, cos_sin, max_positions, rotary_dim, interleaved, slot_map, T,
+                                 Hq, Hk, q_out, flags);
   a.k_cache = (char*)k_cache;
   a.v_cache = (char*)v_cache;
-  a.flags = flags;
   return launch_rotary(a, dtype, D, false, q_stride, k_stride, v_stride, q_out_stride, page_size,
                        n_pages, stream);
 }
@@ -115,20 +124,8 @@ int spec_paged_append_fp4(const void* q, int64_t q_stride, const void* k_new, in
                           int64_t q_out_stride, void* k_codes, void* k_scales, void* v_codes,
                           void* v_scales, uint32_t* flags, void* stream) {
   if (!gain_ok(k_gain) || !gain_ok(v_gain)) return SV_ERR_SHAPE;
-  sv::RotaryArgs a = {};
-  a.q = (const char*)q;
-  a.k_new = (const char*)k_new;
-  a.v_new = (const char*)v_new;
-  a.positions = positions;
-  a.table = cos_sin;
-  a.slot_map = slot_map;
-  a.T = T;
-  a.Hq = Hq;
-  a.Hk = Hk;
-  a.max_positions = max_positions;
-  a.rot = rotary_dim;
-  a.neighbours = interleaved != 0;
-  a.q_out = (char*)q_out;
+  sv::RotaryArgs a = rotary_args(q, k_new, v_new, positions, cos_sin, max_positions, rotary_dim, interleaved, slot_map, T,
+                                 Hq, Hk, q_out, flags);
   a.k_cache = (char*)k_codes;
   a.v_cache = (char*)v_codes;
   a.k_scale = (uint8_t*)k_scales;
@@ -137,7 +134,6 @@ int spec_paged_append_fp4(const void* q, int64_t q_stride, const void* k_new, in
   a.v_gain = v_gain;
   a.k_plain = power_of_two(k_gain);
   a.v_plain = power_of_two(v_gain);
-  a.flags = flags;
   return launch_rotary(a, dtype, D, true, q_stride, k_stride, v_stride, q_out_stride, page_size,
                        n_pages, stream);
 }

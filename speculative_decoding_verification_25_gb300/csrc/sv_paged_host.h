@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "spec_verify.h"
 #include "sv_host.h"
 
@@ -36,6 +38,28 @@ inline cudaError_t find_encoder(EncodeTiled* encode) {
   if (e == cudaSuccess && found != cudaDriverEntryPointSuccess) e = cudaErrorSymbolNotFound;
   *encode = (EncodeTiled)fn;
   return e;
+}
+
+// What a host side keeps of each device.
+struct PagedDevice {
+  std::once_flag once;
+  int sm_count = 0;
+  EncodeTiled encode = nullptr;   // the driver's tensor map encoder
+  cudaError_t error = cudaSuccess;
+};
+// The current device's of `devices`; nullptr if it cannot be used.  Once per device, `limits`
+// sets what the kernels need.
+template <typename Limits>
+inline PagedDevice* current_device(PagedDevice (&devices)[kMaxDevices], Limits limits) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+  PagedDevice& d = devices[dev];
+  std::call_once(d.once, [&d, dev, &limits]() {
+    d.error = cudaDeviceGetAttribute(&d.sm_count, cudaDevAttrMultiProcessorCount, dev);
+    if (d.error == cudaSuccess) d.error = limits();
+    if (d.error == cudaSuccess) d.error = find_encoder(&d.encode);
+  });
+  return d.error == cudaSuccess ? &d : nullptr;
 }
 
 // A map of 16-bit elements for boxes of 64 columns (128 bytes, swizzled) by
